@@ -14,11 +14,15 @@ import threading
 
 import torch
 
+from . import attention
+from .attention import block_attention, block_means, block_scores
+
 __all__ = [
     "PATH_AUTO", "PATH_LOCAL", "PATH_SPLIT", "PATH_CHUNKS", "PATH_PERSIST", "PLAN_PERSIST",
     "library_path", "load_library", "topk_indices", "workspace_size",
     "plan_describe", "debug_keys", "workspace_error", "status_string",
     "c128a_active_width", "c128a_topk_metadata",
+    "block_means", "block_scores", "block_attention",
 ]
 
 PATH_AUTO, PATH_LOCAL, PATH_SPLIT, PATH_CHUNKS, PATH_PERSIST = 0, 1, 2, 3, 4
@@ -73,6 +77,7 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.c128a_active_width.restype = i32
     lib.c128a_topk_metadata.argtypes = [vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp, vp, i64, i32, vp]
     lib.c128a_topk_metadata.restype = ctypes.c_int
+    attention.declare(lib)
     return lib
 
 

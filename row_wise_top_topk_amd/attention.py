@@ -1,0 +1,297 @@
+"""Block scores and block sparse attention: what produces the rows that
+``topk_indices`` selects from, and what reads the blocks that it selects.
+
+Argument marshalling only, as in the package's other functions: every step
+runs in the library's HIP kernels on the current stream of the tensors'
+device.  Outputs and scratch memory come from PyTorch's allocator, so a call
+can be captured into a graph, and two graphs share nothing.
+
+    means = block_means(k, 64)
+    scores, counts = block_scores(q, means, 64, max_blocks)
+    blocks = topk_indices(scores.flatten(0, 1), counts.flatten(), 16)
+    out, lse = block_attention(q, k, v, blocks.view(tokens, kv_heads, 16), 64)
+
+Packed sequences: ``cu_seqlens`` (int32, one entry more than sequences, first
+0, not decreasing, on the device) gives each sequence's queries,
+``cu_seqlens_k`` its keys (default: the same).  Query r of a sequence with n
+queries and m keys stands at position ``m - n + r``.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+__all__ = ["block_means", "block_scores", "block_attention", "block_attention_backward"]
+
+BLOCK_SIZES = (16, 32, 64, 128)
+HEAD_DIMS = (64, 128)
+MAX_SELECT = 1024
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_STATUS = {1: "invalid argument", 2: "workspace too small", 3: "kernel launch failed"}
+
+_vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class _ScoreArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("q", "means", "cu_q", "cu_k", "lengths", "block_table", "scores", "counts")]
+                + [(n, _i64) for n in ("q_stride_t", "q_stride_h", "total_q", "total_k", "mean_rows", "block_table_stride")]
+                + [(n, _i32) for n in ("dtype", "num_seqs", "heads", "kv_heads", "dim", "block_size", "max_blocks",
+                                       "first", "last")]
+                + [("scale", _f32)])
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "blocks", "cu_q", "cu_k", "out", "lse", "dout", "dq", "dk", "dv",
+                                    "workspace")]
+                + [("workspace_bytes", ctypes.c_uint64)]
+                + [(n, _i64) for n in ("q_stride_t", "q_stride_h", "k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h",
+                                       "dout_stride_t", "dout_stride_h", "total_q", "total_k")]
+                + [(n, _i32) for n in ("dtype", "num_seqs", "heads", "kv_heads", "dim", "block_size", "select", "causal")]
+                + [("scale", _f32)])
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Argument and result types of the exported functions of this module."""
+    lib.block_means.argtypes = [_i32, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp]
+    lib.block_means.restype = ctypes.c_int
+    lib.block_scores.argtypes = [ctypes.POINTER(_ScoreArgs), _vp]
+    lib.block_scores.restype = ctypes.c_int
+    lib.block_attention.argtypes = [ctypes.POINTER(_AttentionArgs), _vp]
+    lib.block_attention.restype = ctypes.c_int
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _check(status: int, what: str) -> None:
+    if status != 0:
+        raise RuntimeError(f"{what} failed: {_STATUS.get(status, 'unknown status')} (status {status})")
+
+
+def _heads(t, what: str, device=None, dtype=None, dim=None) -> None:
+    """A [tokens, heads, dim] operand as the kernels read it."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype not in _DTYPES:
+        raise ValueError(f"{what} must be a 3-D bfloat16 or float16 tensor [tokens, heads, dim]")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must have the others' type and device")
+    if t.shape[2] not in HEAD_DIMS or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{what} must have a head dimension in {HEAD_DIMS}, the same for all")
+    if t.shape[1] < 1:
+        raise ValueError(f"{what} must have at least one head")
+    if t.numel() and (t.stride(2) != 1 or t.data_ptr() % 16
+                      or any(t.shape[i] > 1 and (t.stride(i) % 8 or t.stride(i) < 0) for i in (0, 1))):
+        raise ValueError(f"{what} must have unit stride along its last axis, 16-byte-aligned data and other strides "
+                         "that are multiples of 8 elements")
+
+
+def _strides(t):
+    """(token, head) strides; of an axis of one entry, 0."""
+    return (int(t.stride(0)) if t.shape[0] > 1 else 0, int(t.stride(1)) if t.shape[1] > 1 else 0)
+
+
+def _ints(t, what: str, device, dims: int, shape=None) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims or t.device != device:
+        raise ValueError(f"{what} must be a {dims}-D int32 tensor on the others' device")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have the shape {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _sequences(cu_q, cu_k, device, total_q: int, total_k: int):
+    """(cu_q, cu_k, sequences) with the defaults filled in."""
+    if cu_q is None and cu_k is None:
+        return None, None, 1
+    if cu_q is None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    if cu_k is None:
+        if total_q != total_k:
+            raise ValueError("cu_seqlens_k is needed where queries and keys differ in number")
+        cu_k = cu_q
+    for t, what in ((cu_q, "cu_seqlens"), (cu_k, "cu_seqlens_k")):
+        _ints(t, what, device, 1)
+        if t.shape[0] < 1 or t.shape[0] != cu_q.shape[0]:
+            raise ValueError(f"{what} must have one entry more than there are sequences")
+    return cu_q, cu_k, int(cu_q.shape[0]) - 1
+
+
+def _block_size(block_size) -> int:
+    if block_size not in BLOCK_SIZES:
+        raise ValueError(f"block_size must be one of {BLOCK_SIZES}")
+    return int(block_size)
+
+
+def _scale(scale, dim: int) -> float:
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    if not 0.0 < scale < math.inf:
+        raise ValueError("scale must be positive and finite")
+    return scale
+
+
+def _groups(heads: int, kv_heads: int) -> None:
+    if heads % kv_heads or heads // kv_heads > 128:
+        raise ValueError("the query heads must be a multiple of the key heads, 128 times as many at most")
+
+
+def _output(out, shape, dtype, device, what: str):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if (not isinstance(out, torch.Tensor) or out.dtype != dtype or tuple(out.shape) != tuple(shape)
+            or not out.is_contiguous() or out.device != device):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the others' device")
+    return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_means(k: torch.Tensor, block_size: int, cu_seqlens: torch.Tensor = None,
+                out: torch.Tensor = None) -> torch.Tensor:
+    """Mean of the keys of each block of ``block_size`` tokens.
+
+    ``k``: bfloat16 or float16 ``[tokens, kv_heads, dim]``.  Returns float32
+    ``[tokens // block_size + sequences, kv_heads, dim]``: block b of sequence
+    i is row ``cu_seqlens[i] // block_size + i + b``; rows that are no block
+    are 0."""
+    bs = _block_size(block_size)
+    _heads(k, "k")
+    total, hk, dim = (int(x) for x in k.shape)
+    cu, _, n = _sequences(cu_seqlens, None, k.device, total, total)
+    out = _output(out, (total // bs + n, hk, dim), torch.float32, k.device, "out")
+    st, sh = _strides(k)
+    with torch.cuda.device(k.device):
+        _check(_lib().block_means(_DTYPES[k.dtype], k.data_ptr(), st, sh, total, hk, dim, bs, _ptr(cu), n,
+                                  out.data_ptr(), torch.cuda.current_stream(k.device).cuda_stream), "block_means")
+    return out
+
+
+def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_blocks: int,
+                 cu_seqlens: torch.Tensor = None, cu_seqlens_k: torch.Tensor = None,
+                 lengths: torch.Tensor = None, block_table: torch.Tensor = None,
+                 first: int = 1, last: int = 1, scale: float = None):
+    """Scores of key blocks for each query and key head, as the rows that
+    ``topk_indices`` selects from.
+
+    Returns ``(scores, counts)``: float32 ``[tokens, kv_heads, max_blocks]``
+    and int32 ``[tokens, kv_heads]``.  A block's score is the largest
+    ``scale * q . mean`` of the group's query heads; the first ``first`` and
+    the last ``last`` of the ``counts`` blocks that the query can see have
+    +inf, so a selection always takes them, and the blocks behind have -inf.
+    The last visible block is the query's own: its mean covers tokens behind
+    the query, which ``last >= 1`` keeps out of the selection.
+
+    Packed form: ``means`` of ``block_means`` (over ``cu_seqlens_k``, default
+    ``cu_seqlens``; without both, one sequence with as many keys as queries).
+    Paged form: ``block_table`` (int32 ``[sequences,
+    >= max_blocks]``), ``lengths`` (int32 ``[sequences]``, keys with the
+    queries' own) and ``means`` float32 ``[pages, kv_heads, dim]``; without
+    ``cu_seqlens`` each sequence has one query.  An entry of the table outside
+    the pages gives its block -inf.  Rows behind the last sequence are -inf
+    with count 0."""
+    bs = _block_size(block_size)
+    _heads(q, "q")
+    device = q.device
+    total, heads, dim = (int(x) for x in q.shape)
+    if (not isinstance(means, torch.Tensor) or means.dtype != torch.float32 or means.dim() != 3 or means.device != device
+            or not means.is_contiguous() or means.shape[2] != dim or means.shape[1] < 1):
+        raise ValueError("means must be a contiguous float32 tensor [rows, kv_heads, dim] on q's device")
+    if means.numel() and means.data_ptr() % 16:
+        raise ValueError("means must be 16-byte aligned")
+    hk = int(means.shape[1])
+    _groups(heads, hk)
+    max_blocks, first, last = int(max_blocks), int(first), int(last)
+    if max_blocks < 1 or max_blocks >= 1 << 22 or first < 0 or last < 0:
+        raise ValueError("max_blocks must be in [1, 2^22), first and last not negative")
+    a = _ScoreArgs()
+    if block_table is not None:
+        if lengths is None or cu_seqlens_k is not None:
+            raise ValueError("the paged form takes block_table and lengths, without cu_seqlens_k")
+        if (not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2
+                or block_table.device != device or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+            raise ValueError("block_table must be a 2-D int32 tensor on q's device with unit stride along its last axis")
+        n = int(block_table.shape[0])
+        if block_table.shape[1] < max_blocks:
+            raise ValueError("block_table must have max_blocks columns at least")
+        _ints(lengths, "lengths", device, 1, (n,))
+        if cu_seqlens is not None:
+            _ints(cu_seqlens, "cu_seqlens", device, 1, (n + 1,))
+        elif total != n:
+            raise ValueError("without cu_seqlens there must be one query for each sequence")
+        cu_q, cu_k = cu_seqlens, None
+        a.block_table_stride = max(int(block_table.stride(0)), max_blocks) if n <= 1 else int(block_table.stride(0))
+        if a.block_table_stride < max_blocks:
+            raise ValueError("block_table's rows must not overlap")
+    else:
+        if lengths is not None:
+            raise ValueError("lengths goes with block_table")
+        cu_q, cu_k, n = _sequences(cu_seqlens, cu_seqlens if cu_seqlens_k is None else cu_seqlens_k, device, total, total)
+        if cu_q is None and means.shape[0] < total // bs + 1:
+            raise ValueError("means must have a row for every block, as block_means gives them")
+    scores = torch.empty((total, hk, max_blocks), dtype=torch.float32, device=device)
+    counts = torch.empty((total, hk), dtype=torch.int32, device=device)
+    a.q, a.means, a.cu_q, a.cu_k = q.data_ptr(), means.data_ptr(), _ptr(cu_q), _ptr(cu_k)
+    a.lengths, a.block_table, a.scores, a.counts = _ptr(lengths), _ptr(block_table), scores.data_ptr(), counts.data_ptr()
+    a.q_stride_t, a.q_stride_h = _strides(q)
+    a.total_q, a.total_k, a.mean_rows = total, total, int(means.shape[0])
+    a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
+    a.max_blocks, a.first, a.last, a.scale = max_blocks, first, last, _scale(scale, dim)
+    with torch.cuda.device(device):
+        _check(_lib().block_scores(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "block_scores")
+    return scores, counts
+
+
+def _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
+    bs = _block_size(block_size)
+    _heads(q, "q")
+    total, heads, dim = (int(x) for x in q.shape)
+    _heads(k, "k", q.device, q.dtype, dim)
+    _heads(v, "v", q.device, q.dtype, dim)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    total_k, hk = int(k.shape[0]), int(k.shape[1])
+    _groups(heads, hk)
+    if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or not 1 <= blocks.shape[2] <= MAX_SELECT:
+        raise ValueError(f"blocks must be an int32 tensor [tokens, kv_heads, selected], selected in [1, {MAX_SELECT}]")
+    _ints(blocks, "blocks", q.device, 3, (total, hk, blocks.shape[2]))
+    cu_q, cu_k, n = _sequences(cu_seqlens, cu_seqlens_k, q.device, total, total_k)
+    a = _AttentionArgs()
+    a.q, a.k, a.v, a.blocks, a.cu_q, a.cu_k = (_ptr(t) for t in (q, k, v, blocks, cu_q, cu_k))
+    a.q_stride_t, a.q_stride_h = _strides(q)
+    a.k_stride_t, a.k_stride_h = _strides(k)
+    a.v_stride_t, a.v_stride_h = _strides(v)
+    a.total_q, a.total_k = total, total_k
+    a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
+    a.select, a.causal, a.scale = int(blocks.shape[2]), int(bool(causal)), _scale(scale, dim)
+    return a
+
+
+def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: torch.Tensor, block_size: int,
+                    cu_seqlens: torch.Tensor = None, cu_seqlens_k: torch.Tensor = None, scale: float = None,
+                    causal: bool = True, out: torch.Tensor = None):
+    """Attention of each query over the key blocks that it selects.
+
+    ``q`` ``[tokens, heads, dim]``, ``k`` and ``v`` ``[keys, kv_heads, dim]``
+    (bfloat16 or float16, dim 64 or 128, any strides that are multiples of 8
+    elements with unit stride along dim); ``blocks`` int32 ``[tokens, kv_heads,
+    selected]``, block numbers within the query's sequence in any order, where
+    an entry that is negative or names no block selects nothing and a repeated
+    one counts once.  ``causal`` hides the keys behind the query's position.
+
+    Returns ``(out, lse)``: ``[tokens, heads, dim]`` of q's type, and the
+    log-sum of the scaled scores' exponentials, float32 ``[tokens, heads]``.  A
+    query that sees no key, and a row behind the last sequence, has 0 and -inf."""
+    a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
+    out = _output(out, q.shape, q.dtype, q.device, "out")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    a.out, a.lse = out.data_ptr(), lse.data_ptr()
+    with torch.cuda.device(q.device):
+        _check(_lib().block_attention(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream), "block_attention")
+    return out, lse

@@ -1,0 +1,147 @@
+// Device helpers shared by the attention kernels for gfx950 (CDNA4): element
+// types, matrix-core wrappers, LDS tiles and the packed-sequence lookup.
+//
+// Matrix layouts used here (64 lanes, l = lane):
+//   32x32x16: A lane l holds row l & 31, k = (l >> 5) * 8 + j;  B lane l holds
+//   column l & 31, k likewise;  C lane l holds column l & 31, rows
+//   8 * (r >> 2) + 4 * (l >> 5) + (r & 3), r = 0..15.
+//   16x16x32: A row / B column l & 15, k = (l >> 4) * 8 + j;  C column l & 15,
+//   rows 4 * (l >> 4) + r, r = 0..3.
+// Scores are computed transposed (keys as rows), so that a lane holds one
+// query's scores: the softmax statistics stay within a lane and its partners,
+// and the probabilities are already in the B layout of the second product up
+// to a permutation of the keys, which the transposing LDS reads of V follow.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace miattn {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+#define MI_LDS __attribute__((address_space(3)))
+#define MI_GLOBAL __attribute__((address_space(1)))
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+
+struct Bf16 {
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  // two floats rounded to nearest even, packed (x in the low half)
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
+  static __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+};
+
+struct Fp16 {
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), f16x2));
+  }
+  static __device__ __forceinline__ float lo(uint32_t v) { return static_cast<float>(__builtin_bit_cast(f16x2, v)[0]); }
+  static __device__ __forceinline__ float hi(uint32_t v) { return static_cast<float>(__builtin_bit_cast(f16x2, v)[1]); }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Address of a shared-memory byte as the LDS builtins take it.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const MI_LDS void*)p));
+}
+
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
+  return *reinterpret_cast<const MI_LDS u32x4*>(at);
+}
+
+// Four rows of 16 elements transposed within each 16-lane group: lane i reads
+// 8 bytes (row i >> 2, elements 4 (i & 3)..) and gets element i of the rows.
+__device__ __forceinline__ u32x2 lds_read_tr16(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<MI_LDS s16x4*>(at)));
+}
+
+// A tile of rows of D 16-bit elements in LDS: 16-byte chunks, chunk c of row r
+// at place c ^ swizzle(r).  The swizzle takes rows four apart to neighbouring
+// chunks and rows within a group of four to different quarters of a row, so
+// that both the row reads (16 lanes, 16 rows, one chunk) and the transposing
+// reads (32 lanes, 4 rows, 4 chunks) touch every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+  return D == 128 ? ((row & 3u) << 2) | ((row >> 2) & 3u) : (((row >> 1) & 1u) << 2) | ((row >> 2) & 3u);
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(uint32_t row, uint32_t chunk) {
+  return row * (2 * D) + ((chunk ^ swizzle<D>(row)) << 4);
+}
+
+// Which packed sequence a tile slot belongs to.  Sequence i owns the slots
+// [cu[i] / per + i, cu[i + 1] / per + i + 1), at least as many as it has tiles
+// of `per` tokens (with one token a tile, exactly [cu[i], cu[i + 1])); sequence
+// `num` stands for the rows behind the last one.  Without cu there is one
+// sequence, or one token for each of several.
+inline int64_t slots_of(int64_t total, int num, int per) { return per == 1 ? total : total / per + num + 1; }
+
+struct Place {
+  int seq;        // num for rows behind the last sequence
+  int64_t first;  // first token of the tile
+  int64_t end;    // end of the sequence
+  int64_t begin;
+};
+
+__device__ __forceinline__ int64_t cu_at(const int32_t* cu, int num, int64_t total, int i) {
+  if (i > num) return total;
+  if (cu == nullptr) return num == 1 ? (i == 0 ? 0 : total) : (i < total ? i : total);
+  const int64_t c = cu[i];
+  return c < 0 ? 0 : (c > total ? total : c);
+}
+
+__device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per) {
+  const int64_t extra = per == 1 ? 0 : 1;
+  int lo = 0, hi = num;  // the last i with first slot <= slot
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu_at(cu, num, total, mid) / per + mid * extra <= slot) lo = mid; else hi = mid - 1;
+  }
+  Place r;
+  r.seq = lo;
+  r.begin = cu_at(cu, num, total, lo);
+  r.end = cu_at(cu, num, total, lo + 1);
+  r.first = r.begin + (slot - (r.begin / per + lo * extra)) * per;
+  return r;
+}
+
+// Maximum and sum over a lane and its partner in the other half wavefront.
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+}  // namespace miattn

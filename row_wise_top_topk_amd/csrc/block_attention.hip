@@ -1,0 +1,392 @@
+// Block sparse attention: forward, and the gradient of the queries.
+//
+//   out = sum_j p_j v_j over the keys j of the blocks that each query selects.
+//
+// A workgroup takes 128 rows of one key head: TQ = 128 / G consecutive tokens
+// with the G query heads that share the key head, 32 rows a wavefront.  It
+// walks over the blocks that any of its tokens selects, 64 keys at a time, so
+// neighbouring tokens that select the same blocks read them once; each row
+// masks what its own token did not select, and a wavefront none of whose rows
+// selects a tile skips it.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attention/mi_block_attention.h"
+#include "attn_device.hpp"
+#include "block_attention.hpp"
+
+namespace miattn {
+namespace {
+
+constexpr int kRows = 128;        // rows of a workgroup
+constexpr int kTile = 64;         // keys of a tile
+constexpr int kMaskWords = 2048;  // words of token bits, window of block numbers x words per block
+
+struct Select {
+  uint32_t mask[kMaskWords];
+  uint16_t list[kMaskWords];
+  uint32_t wave_count[4];
+};
+
+// The tokens of one workgroup and how its rows map to them.
+struct Group {
+  int64_t t0, begin, tk0;  // first token; the sequence's first token and first key
+  int32_t tokens;          // tokens of this workgroup
+  int32_t len_k;
+  int32_t shift;           // position of token t: t - begin + shift
+  int32_t blocks;          // blocks that any of its rows can see
+};
+
+__device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
+  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, tq);
+  Group g;
+  g.t0 = at.first;
+  g.begin = at.begin;
+  const int64_t left = at.end - at.first;
+  g.tokens = static_cast<int32_t>(left < 0 ? 0 : (left < tq ? left : tq));
+  g.tk0 = 0;
+  g.len_k = 0;
+  if (at.seq < p.num_seqs) {
+    g.tk0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
+    const int64_t n = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - g.tk0;
+    g.len_k = static_cast<int32_t>(n < 0 ? 0 : n);
+  }
+  g.shift = g.len_k - static_cast<int32_t>(at.end - at.begin);
+  int64_t seen = g.len_k;
+  if (p.causal) {
+    const int64_t last = at.first - at.begin + g.tokens - 1 + g.shift;
+    if (last + 1 < seen) seen = last + 1 < 0 ? 0 : last + 1;
+  }
+  g.blocks = g.tokens > 0 ? static_cast<int32_t>((seen + p.bs - 1) >> p.lb) : 0;
+  return g;
+}
+
+// Marks which tokens select each block of [w0, w0 + width) and lists the blocks
+// that any does, ascending.  Returns their number.  Ends with a barrier.
+__device__ __forceinline__ int list_window(const Args& p, const Group& g, int hk, int w0, int width, int nw, Select& s) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  for (int i = tid; i < width * nw; i += 256) s.mask[i] = 0;
+  __syncthreads();
+  const int most = min(width, g.blocks - w0);
+  const int32_t* rows = p.blocks + (g.t0 * p.kv_heads + hk) * static_cast<int64_t>(p.select);
+  const int64_t stride = static_cast<int64_t>(p.kv_heads) * p.select;
+  const int total = g.tokens * p.select;
+  for (int i = tid; i < total; i += 256) {
+    const int tl = i / p.select;
+    const int b = rows[tl * stride + (i - tl * p.select)] - w0;
+    if (b >= 0 && b < most) atomicOr(&s.mask[b * nw + (tl >> 5)], 1u << (tl & 31));
+  }
+  __syncthreads();
+  // every thread has width / 256 consecutive blocks; counts are summed over
+  // the lanes, then over the wavefronts
+  const int each = (width + 255) >> 8;
+  int mine = 0;
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    uint32_t any = 0;
+    if (b < most)
+      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
+    mine += any != 0;
+  }
+  int sum = mine;
+  const int lane = tid & 63, wave = tid >> 6;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(sum, d);
+    if (lane >= d) sum += up;
+  }
+  if (lane == 63) s.wave_count[wave] = sum;
+  __syncthreads();
+  int at = sum - mine;
+  int count = 0;
+  for (int w = 0; w < 4; ++w) {
+    const int c = s.wave_count[w];
+    if (w < wave) at += c;
+    count += c;
+  }
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    uint32_t any = 0;
+    if (b < most)
+      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
+    if (any != 0) s.list[at++] = static_cast<uint16_t>(b);
+  }
+  __syncthreads();
+  return count;
+}
+
+// The four 16-key groups of a tile: first key of each in its sequence, or -1.
+struct Keys {
+  int32_t key[4];
+  int32_t id[4];  // place of the block in the window
+};
+
+__device__ __forceinline__ Keys keys_of(const Select& s, int lb, int bs, int w0, int active, int tile) {
+  Keys k;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = tile * kTile + 16 * i;
+    const int e = a >> lb;
+    k.key[i] = -1;
+    k.id[i] = 0;
+    if (e < active) {
+      k.id[i] = __builtin_amdgcn_readfirstlane(s.list[e]);
+      k.key[i] = ((w0 + k.id[i]) << lb) + (a & (bs - 1));
+    }
+  }
+  return k;
+}
+
+// Copies 64 rows of D elements into an LDS tile, straight from memory.
+template <int D>
+__device__ __forceinline__ void stage_tile(void* tile, const char* base, int64_t stride_bytes, const Keys& k, int len_k,
+                                           int wave, int lane) {
+  constexpr int kChunks = D / 8;
+  constexpr int kRowsPer = 64 / kChunks;  // rows of one instruction
+  const int sub = lane / kChunks, chunk = lane % kChunks;
+#pragma unroll
+  for (int j = 0; j < kTile / (4 * kRowsPer); ++j) {
+    const int row0 = (j * 4 + wave) * kRowsPer;
+    const int row = row0 + sub;
+    int key = k.key[0];
+    if (row0 >= 16) key = k.key[1];
+    if (row0 >= 32) key = k.key[2];
+    if (row0 >= 48) key = k.key[3];
+    key += row & 15;
+    key = max(0, min(key, len_k - 1));
+    const char* from = base + key * stride_bytes + ((chunk ^ swizzle<D>(row)) << 4);
+    __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(from), (MI_LDS void*)(static_cast<char*>(tile) + row0 * 2 * D), 16, 0, 0);
+  }
+}
+
+// What a lane's row may see of a tile: for each 16-key group the last visible
+// offset (relative to the group's first key), -1 for none.
+struct Sight {
+  int32_t last[4];
+  bool any;   // some row of the wavefront sees something
+  bool full;  // every valid row sees all 64 keys
+};
+
+__device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw, int word, int bit, int limit, bool valid) {
+  Sight v;
+  bool some = false, all = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.last[i] = -1;
+    if (k.key[i] >= 0 && ((s.mask[k.id[i] * nw + word] >> bit) & 1u)) v.last[i] = limit - k.key[i];
+    some |= v.last[i] >= 0;
+    all &= v.last[i] >= 15;
+  }
+  v.any = __any(valid && some);
+  v.full = __all(!valid || all);
+  return v;
+}
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <typename T, int D>
+struct Shared {
+  char k[2][kTile * 2 * D];
+  char v[2][kTile * 2 * D];
+  Select sel;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem);
+  const int hk = blockIdx.x % p.kv_heads;
+  // later tiles see more blocks: they start first
+  const int64_t slot = p.slots - 1 - static_cast<int64_t>(blockIdx.x / p.kv_heads);
+  const int tq = p.tokens_per;
+  const Group g = group_of(p, slot, tq);
+  if (g.tokens == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5;
+  const int row = wave * 32 + (lane & 31);
+  const int tl = row / p.group, head = hk * p.group + row % p.group;
+  const bool valid = tl < g.tokens;
+  const int64_t tok = g.t0 + (valid ? tl : 0);
+  int limit = -1;
+  if (valid) {
+    const int64_t pos = tok - g.begin + g.shift;
+    limit = p.causal ? static_cast<int>(pos < g.len_k ? pos : g.len_k - 1) : g.len_k - 1;
+  }
+
+  // the row's query: D / 16 operands of 8 elements
+  u32x4 q[D / 16];
+  {
+    const char* from = static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h) * 2 + half * 16;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) q[i] = valid ? *reinterpret_cast<const u32x4*>(from + i * 32) : u32x4{0, 0, 0, 0};
+  }
+  const char* kbase = static_cast<const char*>(p.k) + (g.tk0 * p.k_t + hk * p.k_h) * 2;
+  const char* vbase = static_cast<const char*>(p.v) + (g.tk0 * p.v_t + hk * p.v_h) * 2;
+
+  f32x16 acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+  float m = -kInf, sum = 0.f;
+  const float c = p.scale * kLog2e;
+
+  const int nw = (tq + 31) >> 5;
+  const int width = kMaskWords / nw;
+  const uint32_t kread = (lane & 31) * (2 * D) + ((half ^ swizzle<D>(lane & 31)) << 4);
+  // transposing read of V: row 4 half + (li >> 2), elements 16 dhalf + 4 (li & 3)
+  const int li = lane & 15, dhalf = (lane >> 4) & 1;
+  const uint32_t vrow = 4 * half + (li >> 2);
+  const uint32_t vchunk = dhalf * 2 + ((li & 3) >> 1);
+
+  for (int w0 = 0; w0 < g.blocks; w0 += width) {
+    const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
+    const int tiles = ((active << p.lb) + kTile - 1) / kTile;
+    Keys next = keys_of(sh.sel, p.lb, p.bs, w0, active, 0);
+    if (tiles > 0) {
+      stage_tile<D>(sh.k[0], kbase, p.k_t * 2, next, g.len_k, wave, lane);
+      stage_tile<D>(sh.v[0], vbase, p.v_t * 2, next, g.len_k, wave, lane);
+    }
+    for (int tile = 0; tile < tiles; ++tile) {
+      const Keys keys = next;
+      wait_loads();
+      __syncthreads();
+      const int buf = tile & 1;
+      if (tile + 1 < tiles) {
+        next = keys_of(sh.sel, p.lb, p.bs, w0, active, tile + 1);
+        stage_tile<D>(sh.k[buf ^ 1], kbase, p.k_t * 2, next, g.len_k, wave, lane);
+        stage_tile<D>(sh.v[buf ^ 1], vbase, p.v_t * 2, next, g.len_k, wave, lane);
+      }
+      const Sight see = sight_of(sh.sel, keys, nw, tl >> 5 < nw ? tl >> 5 : 0, tl & 31, limit, valid);
+      if (!see.any) continue;
+      const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
+      f32x16 s[2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          s[mt] = T::mfma32(lds_read16(ks + mt * 32 * 2 * D + (kread ^ (i * 32))), q[i], s[mt]);
+      }
+      if (!see.full) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int off = 8 * ((r >> 2) & 1) + (r & 3);
+            if (off + 4 * half > see.last[mt * 2 + (r >> 3)]) s[mt][r] = -kInf;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, s[0][r]);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[1][r]);
+      top = half_max(top);
+      if (__any(top > m)) {
+        const float now = fmaxf(m, top);
+        const float shrink = now == -kInf ? 1.f : exp2_fast((m - now) * c);
+        m = now;
+        sum *= shrink;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][r] *= shrink;
+      }
+      const float base = m == -kInf ? 0.f : m * c;
+      u32x4 pr[4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+          const float x = exp2_fast(fmaf(s[mt][r], c, -base)), y = exp2_fast(fmaf(s[mt][r + 1], c, -base));
+          sum += x + y;
+          pr[mt * 2 + (r >> 3)][(r & 7) >> 1] = T::pack(x, y);
+        }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int st = 0; st < 4; ++st) {
+          const uint32_t r0 = 16 * st + vrow;
+          const uint32_t a0 = vs + tile_at<D>(r0, 4 * i + vchunk) + (li & 1) * 8;
+          const uint32_t a1 = vs + tile_at<D>(r0 + 8, 4 * i + vchunk) + (li & 1) * 8;
+          const u32x2 x = lds_read_tr16(a0), y = lds_read_tr16(a1);
+          acc[i] = T::mfma32(u32x4{x[0], x[1], y[0], y[1]}, pr[st], acc[i]);
+        }
+    }
+  }
+  sum = half_sum(sum);
+  if (!valid) return;
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  char* to = static_cast<char*>(p.out) + (tok * p.heads + head) * (2 * D) + half * 8;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      u32x2 w;
+      w[0] = T::pack(acc[i][r] * inv, acc[i][r + 1] * inv);
+      w[1] = T::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv);
+      *reinterpret_cast<u32x2*>(to + i * 64 + (r >> 2) * 16) = w;
+    }
+  if (half == 0) p.lse[tok * p.heads + head] = m == -kInf ? -kInf : m * p.scale + __logf(sum);
+}
+
+template <typename T, int D>
+int launch(const Args& p, hipStream_t stream) {
+  const int64_t grid = p.slots * p.kv_heads;
+  if (grid > INT32_MAX) return MI_ATTN_EINVAL;
+  block_attention_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(Shared<T, D>), stream>>>(p);
+  return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
+}
+
+}  // namespace
+
+// Checks what the forward and the backward share and fills the kernels' form.
+int make_args(const mi_block_attention_args* a, Args& p) {
+  if (a == nullptr) return MI_ATTN_EINVAL;
+  if (a->total_q < 0 || a->total_q > INT32_MAX || a->total_k < 0 || a->total_k > INT32_MAX || a->num_seqs < 0) return MI_ATTN_EINVAL;
+  if (a->dtype != MI_ATTN_BF16 && a->dtype != MI_ATTN_FP16) return MI_ATTN_EINVAL;
+  if (a->dim != 64 && a->dim != 128) return MI_ATTN_EINVAL;
+  if (a->block_size != 16 && a->block_size != 32 && a->block_size != 64 && a->block_size != 128) return MI_ATTN_EINVAL;
+  if (a->kv_heads < 1 || a->heads < a->kv_heads || a->heads % a->kv_heads || a->heads / a->kv_heads > kRows) return MI_ATTN_EINVAL;
+  if (a->select < 1 || a->select > MI_ATTN_MAX_SELECT) return MI_ATTN_EINVAL;
+  if (!(a->scale > 0.f) || !(a->scale < kInf)) return MI_ATTN_EINVAL;
+  if ((a->cu_q == nullptr || a->cu_k == nullptr) && (a->cu_q != a->cu_k || a->num_seqs != 1)) return MI_ATTN_EINVAL;
+  const int64_t strides[] = {a->q_stride_t, a->q_stride_h, a->k_stride_t, a->k_stride_h, a->v_stride_t, a->v_stride_h};
+  for (int64_t s : strides)
+    if (s < 0 || (s & 7)) return MI_ATTN_EINVAL;
+  const bool some_q = a->total_q > 0, some_k = a->total_k > 0;
+  if (some_q && (a->q == nullptr || a->blocks == nullptr || a->out == nullptr || a->lse == nullptr)) return MI_ATTN_EINVAL;
+  if (some_k && (a->k == nullptr || a->v == nullptr)) return MI_ATTN_EINVAL;
+  const void* wide[] = {a->q, a->k, a->v, a->out};
+  for (const void* x : wide)
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return MI_ATTN_EINVAL;
+  const void* words[] = {a->blocks, a->cu_q, a->cu_k, a->lse};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return MI_ATTN_EINVAL;
+  p.q = a->q; p.k = a->k; p.v = a->v; p.blocks = a->blocks; p.cu_q = a->cu_q; p.cu_k = a->cu_k;
+  p.out = a->out; p.lse = a->lse; p.dout = a->dout; p.dq = a->dq; p.dk = a->dk; p.dv = a->dv;
+  p.q_t = a->q_stride_t; p.q_h = a->q_stride_h; p.k_t = a->k_stride_t; p.k_h = a->k_stride_h;
+  p.v_t = a->v_stride_t; p.v_h = a->v_stride_h; p.do_t = a->dout_stride_t; p.do_h = a->dout_stride_h;
+  p.total_q = a->total_q; p.total_k = a->total_k;
+  p.num_seqs = a->num_seqs; p.heads = a->heads; p.kv_heads = a->kv_heads; p.group = a->heads / a->kv_heads;
+  p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
+  p.select = a->select; p.causal = a->causal != 0; p.scale = a->scale;
+  p.tokens_per = kRows / p.group;
+  p.slots = slots_of(p.total_q, p.num_seqs, p.tokens_per);
+  return MI_ATTN_OK;
+}
+
+}  // namespace miattn
+
+using namespace miattn;
+
+MI_ATTN_EXPORT int block_attention(const mi_block_attention_args* args, hipStream_t stream) {
+  Args p;
+  const int st = make_args(args, p);
+  if (st != MI_ATTN_OK || p.total_q == 0) return st;
+  if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128>(p, stream) : launch<Bf16, 64>(p, stream);
+  return args->dim == 128 ? launch<Fp16, 128>(p, stream) : launch<Fp16, 64>(p, stream);
+}
