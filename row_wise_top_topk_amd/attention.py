@@ -1,5 +1,6 @@
-"""Block scores and block sparse attention: what produces the rows that
-``topk_indices`` selects from, and what reads the blocks that it selects.
+"""Block scores, block sparse attention and the 8-bit paged cache: what produces
+the rows that ``topk_indices`` selects from, and what reads the blocks that it
+selects.
 
 Argument marshalling only, as in the package's other functions: every step
 runs in the library's HIP kernels on the current stream of the tensors'
@@ -24,7 +25,7 @@ import math
 
 import torch
 
-__all__ = ["block_means", "block_scores", "block_attention", "block_attention_backward"]
+__all__ = ["block_means", "block_scores", "block_attention", "kv8_append", "kv8_attention"]
 
 BLOCK_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
@@ -53,6 +54,24 @@ class _AttentionArgs(ctypes.Structure):
                 + [("scale", _f32)])
 
 
+class _AppendArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("k", "v", "k_cache", "v_cache", "k_scale", "v_scale", "k_mean", "block_table", "lengths",
+                                    "cu")]
+                + [(n, _i64) for n in ("k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h", "total", "num_pages",
+                                       "block_table_stride")]
+                + [(n, _i32) for n in ("block_table_cols", "dtype", "num_seqs", "kv_heads", "dim", "block_size")])
+
+
+class _DecodeArgs(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "lengths", "cu", "blocks",
+                                    "out", "lse", "workspace")]
+                + [("workspace_bytes", ctypes.c_uint64)]
+                + [(n, _i64) for n in ("q_stride_t", "q_stride_h", "total_q", "num_pages", "block_table_stride", "max_length")]
+                + [(n, _i32) for n in ("block_table_cols", "dtype", "num_seqs", "heads", "kv_heads", "dim", "block_size",
+                                       "select")]
+                + [("scale", _f32)])
+
+
 def declare(lib: ctypes.CDLL) -> None:
     """Argument and result types of the exported functions of this module."""
     lib.block_means.argtypes = [_i32, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp]
@@ -61,6 +80,12 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.block_scores.restype = ctypes.c_int
     lib.block_attention.argtypes = [ctypes.POINTER(_AttentionArgs), _vp]
     lib.block_attention.restype = ctypes.c_int
+    lib.kv8_append.argtypes = [ctypes.POINTER(_AppendArgs), _vp]
+    lib.kv8_append.restype = ctypes.c_int
+    lib.kv8_attention.argtypes = [ctypes.POINTER(_DecodeArgs), _vp]
+    lib.kv8_attention.restype = ctypes.c_int
+    lib.kv8_attention_workspace.argtypes = [ctypes.POINTER(_DecodeArgs)]
+    lib.kv8_attention_workspace.restype = ctypes.c_uint64
 
 
 def _lib():
@@ -120,6 +145,15 @@ def _sequences(cu_q, cu_k, device, total_q: int, total_k: int):
         if t.shape[0] < 1 or t.shape[0] != cu_q.shape[0]:
             raise ValueError(f"{what} must have one entry more than there are sequences")
     return cu_q, cu_k, int(cu_q.shape[0]) - 1
+
+
+def _table(t, device):
+    """(sequences, columns, stride) of a block table."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2 or t.device != device
+            or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+        raise ValueError("block_table must be a 2-D int32 tensor on the others' device with unit stride along its last axis")
+    n, cols = int(t.shape[0]), int(t.shape[1])
+    return n, cols, int(t.stride(0)) if n > 1 else cols
 
 
 def _block_size(block_size) -> int:
@@ -214,11 +248,8 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     if block_table is not None:
         if lengths is None or cu_seqlens_k is not None:
             raise ValueError("the paged form takes block_table and lengths, without cu_seqlens_k")
-        if (not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2
-                or block_table.device != device or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
-            raise ValueError("block_table must be a 2-D int32 tensor on q's device with unit stride along its last axis")
-        n = int(block_table.shape[0])
-        if block_table.shape[1] < max_blocks:
+        n, cols, a.block_table_stride = _table(block_table, device)
+        if cols < max_blocks:
             raise ValueError("block_table must have max_blocks columns at least")
         _ints(lengths, "lengths", device, 1, (n,))
         if cu_seqlens is not None:
@@ -226,9 +257,6 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
         elif total != n:
             raise ValueError("without cu_seqlens there must be one query for each sequence")
         cu_q, cu_k = cu_seqlens, None
-        a.block_table_stride = max(int(block_table.stride(0)), max_blocks) if n <= 1 else int(block_table.stride(0))
-        if a.block_table_stride < max_blocks:
-            raise ValueError("block_table's rows must not overlap")
     else:
         if lengths is not None:
             raise ValueError("lengths goes with block_table")
@@ -294,4 +322,120 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     a.out, a.lse = out.data_ptr(), lse.data_ptr()
     with torch.cuda.device(q.device):
         _check(_lib().block_attention(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream), "block_attention")
+    return out, lse
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, device, hk=None, dim=None):
+    """Pages of the 8-bit cache; returns (pages, kv_heads, block_size, dim)."""
+    for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float8_e4m3fn or t.dim() != 4 or t.device != device
+                or not t.is_contiguous() or t.shape != k_cache.shape or (t.numel() and t.data_ptr() % 16)):
+            raise ValueError(f"{what} must be a contiguous float8_e4m3fn tensor [pages, kv_heads, block_size, dim] on the "
+                             "others' device, 16-byte aligned, k_cache and v_cache of one shape")
+    pages, heads, bs, d = (int(x) for x in k_cache.shape)
+    _block_size(bs)
+    if d not in HEAD_DIMS or heads < 1 or (hk is not None and heads != hk) or (dim is not None and d != dim):
+        raise ValueError(f"the cache must have the others' heads and head dimension, one of {HEAD_DIMS}")
+    for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (pages, heads)
+                or not t.is_contiguous() or t.device != device):
+            raise ValueError(f"{what} must be a contiguous float32 tensor [pages, kv_heads] on the others' device")
+    return pages, heads, bs, d
+
+
+def _cache_sequences(cu, lengths, n: int, total: int, device):
+    _ints(lengths, "lengths", device, 1, (n,))
+    if cu is not None:
+        _ints(cu, "cu_seqlens", device, 1, (n + 1,))
+    elif total != n:
+        raise ValueError("without cu_seqlens there must be one token for each sequence")
+
+
+def kv8_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+               v_scale: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, cu_seqlens: torch.Tensor = None,
+               k_mean: torch.Tensor = None) -> None:
+    """Stores new tokens' keys and values in the 8-bit paged cache, in place.
+
+    ``k``, ``v`` ``[tokens, kv_heads, dim]``: each sequence's last tokens, those
+    of sequence i at ``cu_seqlens[i]:cu_seqlens[i + 1]`` (default: one each);
+    ``lengths`` int32 ``[sequences]`` counts them already.  ``k_cache``,
+    ``v_cache`` float8_e4m3fn ``[pages, kv_heads, block_size, dim]``, ``k_scale``,
+    ``v_scale`` float32 ``[pages, kv_heads]``; block b of sequence i is page
+    ``block_table[i, b]``.
+
+    A page's scale is the smallest power of two that brings what it holds to
+    448 or less; it grows when a token needs it (the codes that are there are
+    rounded again) and starts anew in a page whose first token is stored.
+    Pages outside the cache store nothing; no two sequences may store into one
+    page.  ``k_mean`` (float32 ``[pages, kv_heads, dim]``) receives the mean of
+    the keys of each page that got tokens: the ``means`` of ``block_scores``."""
+    _heads(k, "k")
+    device = k.device
+    _heads(v, "v", device, k.dtype, int(k.shape[2]))
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    total, hk, dim = (int(x) for x in k.shape)
+    pages, _, bs, _ = _cache(k_cache, v_cache, k_scale, v_scale, device, hk, dim)
+    a = _AppendArgs()
+    n, a.block_table_cols, a.block_table_stride = _table(block_table, device)
+    _cache_sequences(cu_seqlens, lengths, n, total, device)
+    if k_mean is not None:
+        _output(k_mean, (pages, hk, dim), torch.float32, device, "k_mean")
+    (a.k, a.v, a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.k_mean, a.block_table, a.lengths, a.cu) = (
+        _ptr(t) for t in (k, v, k_cache, v_cache, k_scale, v_scale, k_mean, block_table, lengths, cu_seqlens))
+    a.k_stride_t, a.k_stride_h = _strides(k)
+    a.v_stride_t, a.v_stride_h = _strides(v)
+    a.total, a.num_pages, a.num_seqs = total, pages, n
+    a.dtype, a.kv_heads, a.dim, a.block_size = _DTYPES[k.dtype], hk, dim, bs
+    with torch.cuda.device(device):
+        _check(_lib().kv8_append(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "kv8_append")
+
+
+def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                  v_scale: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
+                  cu_seqlens: torch.Tensor = None, blocks: torch.Tensor = None, max_length: int = None,
+                  scale: float = None, out: torch.Tensor = None):
+    """Causal attention of each sequence's last tokens over the 8-bit paged cache
+    (``kv8_append`` gives the layout), over all of it or at selected blocks.
+
+    ``q`` ``[tokens, heads, dim]``; those of sequence i are its last ones
+    (``cu_seqlens``; default one each) and ``lengths`` counts them.  ``blocks``
+    (int32 ``[tokens, kv_heads, selected]``) names the blocks that each query
+    reads, as for ``block_attention``.  ``max_length`` bounds the lengths where
+    the caller knows them (default: what the table can hold); it only decides
+    how the work is split.
+
+    Returns ``(out, lse)`` as ``block_attention`` does."""
+    _heads(q, "q")
+    device = q.device
+    total, heads, dim = (int(x) for x in q.shape)
+    pages, hk, bs, _ = _cache(k_cache, v_cache, k_scale, v_scale, device, None, dim)
+    _groups(heads, hk)
+    a = _DecodeArgs()
+    n, a.block_table_cols, a.block_table_stride = _table(block_table, device)
+    _cache_sequences(cu_seqlens, lengths, n, total, device)
+    if a.block_table_cols * bs >= 1 << 30:
+        raise ValueError("a sequence can hold less than 2^30 tokens")
+    if blocks is not None:
+        if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or not 1 <= blocks.shape[2] <= MAX_SELECT:
+            raise ValueError(f"blocks must be an int32 tensor [tokens, kv_heads, selected], selected in [1, {MAX_SELECT}]")
+        _ints(blocks, "blocks", device, 3, (total, hk, blocks.shape[2]))
+    max_length = a.block_table_cols * bs if max_length is None else int(max_length)
+    if max_length < 0:
+        raise ValueError("max_length must not be negative")
+    out = _output(out, q.shape, q.dtype, device, "out")
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
+    a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.block_table, a.lengths, a.cu, a.blocks, a.out, a.lse = (
+        _ptr(t) for t in (q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens, blocks, out, lse))
+    a.q_stride_t, a.q_stride_h = _strides(q)
+    a.total_q, a.num_pages, a.max_length, a.num_seqs = total, pages, max_length, n
+    a.dtype, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], heads, hk, dim, bs
+    a.select, a.scale = 0 if blocks is None else int(blocks.shape[2]), _scale(scale, dim)
+    lib = _lib()
+    with torch.cuda.device(device):
+        a.workspace_bytes = lib.kv8_attention_workspace(ctypes.byref(a))
+        if a.workspace_bytes:
+            workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
+            a.workspace = workspace.data_ptr()
+        _check(lib.kv8_attention(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "kv8_attention")
     return out, lse

@@ -27,6 +27,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -81,6 +82,12 @@ __device__ __forceinline__ u32x4 lds_read16(uint32_t at) {
 // 8 bytes (row i >> 2, elements 4 (i & 3)..) and gets element i of the rows.
 __device__ __forceinline__ u32x2 lds_read_tr16(uint32_t at) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<MI_LDS s16x4*>(at)));
+}
+
+// Eight rows of 16 bytes transposed likewise: lane i reads 8 bytes (row i >> 1,
+// half i & 1) and gets byte i of the rows.
+__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<MI_LDS i32x2*>(at)));
 }
 
 // A tile of rows of D 16-bit elements in LDS: 16-byte chunks, chunk c of row r

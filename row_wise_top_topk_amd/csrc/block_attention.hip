@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
   }
   sum = half_sum(sum);
   if (!valid) return;
-  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   char* to = static_cast<char*>(p.out) + (tok * p.heads + head) * (2 * D) + half * 8;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
       w[1] = T::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv);
       *reinterpret_cast<u32x2*>(to + i * 64 + (r >> 2) * 16) = w;
     }
-  if (half == 0) p.lse[tok * p.heads + head] = m == -kInf ? -kInf : m * p.scale + __logf(sum);
+  if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : m * p.scale + __logf(sum);
 }
 
 template <typename T, int D>

@@ -1,0 +1,584 @@
+// Attention over the 8-bit paged cache.
+//
+//   out = sum_j p_j V_j s_v,  p_j = softmax(scale q.K_j s_k)   (s_k, s_v of j's page)
+//
+// A call reads every visible code once, so it is bound by memory.  A workgroup
+// takes the rows of one key head (tokens x the heads of its group, MT tiles of
+// 16) and a chunk of the keys; its four wavefronts take 32 keys at a time in
+// turn, each with its own running softmax, and are joined at the end.  A second
+// kernel joins the chunks.  The codes become 16-bit elements exactly; a page's
+// K scale multiplies its scores.  Its V scale joins the exponent: the running
+// maximum is that of x = s + log2 s_v, the weights are 2^(x - max), and the sum
+// of the probabilities adds a page's weights divided by s_v.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attention/mi_kv8.h"
+#include "attn_device.hpp"
+#include "block_attention.hpp"
+
+namespace miattn {
+namespace {
+
+constexpr int kSeg = 256;          // blocks whose page numbers and scales are in LDS at a time
+constexpr float kLeast = 0x1p-100f, kMost = 0x1p100f;  // V scales are held between these
+
+struct DecodeArgs {
+  const void* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* cu;
+  const int32_t* blocks;
+  void* out;
+  float* lse;
+  float* part;       // [item][split][R][D], then [item][split][R][2]
+  float* part_ml;
+  int64_t q_t, q_h, total_q, num_pages, table_stride, slots;
+  int32_t table_cols, num_seqs, heads, kv_heads, group, bs, lb, select, tokens_per, head_chunks, splits, chunk;
+  float scale;
+};
+
+// The rows of a workgroup.
+struct Rows {
+  int seq, tokens, heads;  // sequence; tokens and heads of a group in this workgroup
+  int64_t first;           // first token
+  int64_t pos;             // position of the first token
+  int hk, head0;
+  int len;                 // keys of the sequence that the table can hold
+};
+
+__device__ __forceinline__ Rows rows_of(const DecodeArgs& p, int64_t item, int rows) {
+  Rows r;
+  const int hc = static_cast<int>(item % p.head_chunks);
+  const int64_t rest = item / p.head_chunks;
+  r.hk = static_cast<int>(rest % p.kv_heads);
+  const Place at = place_of(p.cu, p.num_seqs, p.total_q, rest / p.kv_heads, p.tokens_per);
+  r.seq = at.seq;
+  r.first = at.first;
+  const int64_t left = at.end - at.first;
+  r.tokens = static_cast<int>(left < 0 ? 0 : (left < p.tokens_per ? left : p.tokens_per));
+  const int per = p.head_chunks == 1 ? p.group : rows;
+  r.head0 = r.hk * p.group + hc * per;
+  r.heads = min(per, p.group - hc * per);
+  r.len = 0;
+  r.pos = -1;
+  if (at.seq < p.num_seqs && r.tokens > 0) {
+    const int64_t len = p.lengths[at.seq], most = static_cast<int64_t>(p.table_cols) << p.lb;
+    r.pos = len - (at.end - at.begin) + (at.first - at.begin);
+    r.len = static_cast<int>(len < 0 ? 0 : (len < most ? len : most));
+  }
+  return r;
+}
+
+// Blocks that a workgroup's rows can see: those up to the last token's position.
+__device__ __forceinline__ int blocks_seen(const DecodeArgs& p, const Rows& r) {
+  int64_t seen = r.pos + r.tokens;
+  if (seen > r.len) seen = r.len;
+  return seen <= 0 ? 0 : static_cast<int>((seen + p.bs - 1) >> p.lb);
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {  // 16-byte chunks of a row of D codes
+  return D == 128 ? row * 128 + ((chunk ^ ((row >> 1) & 7u)) << 4) : row * 64 + ((chunk ^ ((row >> 2) & 3u)) << 4);
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 widen(u32x2 c) {  // 8 codes, exactly
+  u32x4 r;
+  if constexpr (__is_same(T, Bf16)) {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, true));
+  } else {
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], 1.0f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], 1.0f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], 1.0f, true));
+  }
+  return r;
+}
+
+// Maximum and sum over the four lanes that hold one row (16 lanes apart).
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return half_max(x);
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return half_sum(x);
+}
+
+template <int D>
+struct DecodeShared {
+  union {
+    char v[4][32 * D];
+    float join[4][16][D + 4];
+  };
+  float ml[4][64][2];
+  int32_t page[kSeg];  // -1: not there
+  int32_t block[kSeg];
+  float ks[kSeg], vs[kSeg];
+  int32_t list[MI_ATTN_MAX_SELECT];
+  int32_t count[4];
+};
+
+// The valid, different entries of a query's selection, in their order.
+template <typename S>
+__device__ __forceinline__ int list_selected(const DecodeArgs& p, const Rows& r, int nb, S& s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t* from = p.blocks + (r.first * p.kv_heads + r.hk) * static_cast<int64_t>(p.select);
+  int32_t mine[MI_ATTN_MAX_SELECT / 256];
+  bool sorted = true;
+#pragma unroll
+  for (int i = 0; i < MI_ATTN_MAX_SELECT / 256; ++i) {
+    const int e = i * 256 + tid;
+    mine[i] = -1;
+    if (e < p.select) {
+      const int b = from[e];
+      mine[i] = b >= 0 && b < nb ? b : -1;
+      s.list[e] = mine[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MI_ATTN_MAX_SELECT / 256; ++i) {
+    const int e = i * 256 + tid;
+    if (e < p.select && e > 0 && mine[i] >= 0 && s.list[e - 1] >= mine[i]) sorted = false;
+    if (e < p.select && e > 0 && mine[i] >= 0 && s.list[e - 1] < 0) sorted = false;  // an ascending row ends in its -1s
+  }
+  const bool clean = __syncthreads_and(sorted);
+  if (!clean) {
+#pragma unroll
+    for (int i = 0; i < MI_ATTN_MAX_SELECT / 256; ++i) {
+      const int e = i * 256 + tid;
+      if (mine[i] >= 0)
+        for (int f = 0; f < e; ++f)
+          if (s.list[f] == mine[i]) { mine[i] = -1; break; }
+    }
+  }
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < MI_ATTN_MAX_SELECT / 256; ++i) {
+    if (i * 256 >= p.select) break;
+    const uint64_t has = __ballot(mine[i] >= 0);
+    if (lane == 0) s.count[wave] = __popcll(has);
+    __syncthreads();
+    int at = base + __popcll(has & ((1ull << lane) - 1));
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) at += s.count[w];
+      base += s.count[w];
+    }
+    if (mine[i] >= 0) s.list[at] = mine[i];
+    __syncthreads();
+  }
+  return base;
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attention_kernel(DecodeArgs p) {
+  constexpr int R = MT * 16;
+  __shared__ __attribute__((aligned(16))) DecodeShared<D> sh;
+  const int64_t item = blockIdx.x / p.splits;
+  const int split = blockIdx.x % p.splits;
+  const Rows rw = rows_of(p, item, R);
+  if (rw.tokens == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const int nb = blocks_seen(p, rw);
+  // entries (blocks) of this chunk; the last chunk takes all that are left
+  int entries = nb;
+  if (p.blocks != nullptr) entries = nb > 0 ? list_selected(p, rw, nb, sh) : 0;
+  const int e0 = split * p.chunk;
+  const int e1 = split == p.splits - 1 ? entries : min(entries, e0 + p.chunk);
+  if (e0 >= e1 && split > 0) {
+    // nothing to add; a selection's chunks are all looked at by the join
+    if (p.blocks != nullptr)
+      for (int row = tid; row < rw.tokens * rw.heads; row += 256) {
+        const int64_t at = (item * p.splits + split) * R + row;
+        p.part_ml[at * 2] = -kInf;
+        p.part_ml[at * 2 + 1] = 0.f;
+      }
+    return;
+  }
+
+  // rows: queries, limits
+  u32x4 q[MT][D / 32];
+  int limit[MT];
+  int least = INT32_MAX;  // the smallest limit of the valid rows
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int row = t * 16 + n, tl = row / rw.heads, h = rw.head0 + row % rw.heads;
+    const bool ok = tl < rw.tokens;
+    const int64_t pos = rw.pos + tl;
+    limit[t] = ok && rw.len > 0 ? static_cast<int>(pos < rw.len ? (pos < 0 ? -1 : pos) : rw.len - 1) : -1;
+    if (ok) least = min(least, limit[t]);
+    const char* from = static_cast<const char*>(p.q) + ((rw.first + (ok ? tl : 0)) * p.q_t + (ok ? h : rw.head0) * p.q_h + g * (D / 4)) * 2;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) q[t][i] = ok ? *reinterpret_cast<const u32x4*>(from + i * 16) : u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+
+  f32x4 acc[MT][D / 16];
+  float m[MT], sum[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    m[t] = -kInf;
+    sum[t] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const float c = p.scale * kLog2e;
+  char* vt = sh.v[wave];
+  const uint32_t vbase = lds_offset(vt);
+  // transposing read: row (n >> 1) of the group's 8 keys, half row n & 1
+  const uint32_t vrow = (n >> 1) < 4 ? 4 * g + (n >> 1) : 16 + 4 * g + (n >> 1) - 4;
+  constexpr int kLoadsK = D / 64;              // 16-byte loads of a lane per 16 keys
+  constexpr int kLoadsV = D / 32;              // of a lane per 32 keys
+  constexpr int kLanesV = D / 16;              // lanes of a row of V
+
+  struct Tile {
+    u32x4 k[2][kLoadsK];
+    u32x4 v[kLoadsV];
+  };
+
+  for (int s0 = e0; s0 < e1; s0 += kSeg) {
+    const int ne = min(kSeg, e1 - s0);
+    __syncthreads();
+    if (tid < ne) {
+      const int b = p.blocks != nullptr ? sh.list[s0 + tid] : s0 + tid;
+      int pg = p.table[rw.seq * p.table_stride + b];
+      if (pg < 0 || pg >= p.num_pages) pg = -1;
+      const int64_t at = static_cast<int64_t>(pg < 0 ? 0 : pg) * p.kv_heads + rw.hk;
+      sh.block[tid] = b;
+      sh.page[tid] = pg;
+      sh.ks[tid] = pg < 0 ? 0.f : p.k_scale[at];
+      sh.vs[tid] = pg < 0 ? 1.f : fminf(fmaxf(p.v_scale[at], kLeast), kMost);
+    }
+    __syncthreads();
+    const int tiles = ((ne << p.lb) + 31) >> 5;
+
+    auto load = [&](int tile, Tile& x) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int a = tile * 32 + h * 16, e = min(a >> p.lb, ne - 1);
+        const int64_t pg = max(0, sh.page[e]);
+        const uint8_t* from = p.k + (((pg * p.kv_heads + rw.hk) << p.lb) + (a & (p.bs - 1)) + n) * D + g * (D / 4);
+#pragma unroll
+        for (int i = 0; i < kLoadsK; ++i) x.k[h][i] = *reinterpret_cast<const u32x4*>(from + i * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoadsV; ++i) {
+        const int row = i * (64 / kLanesV) + lane / kLanesV;
+        const int a = tile * 32 + row, e = min(a >> p.lb, ne - 1);
+        const int64_t pg = max(0, sh.page[e]);
+        const uint8_t* from = p.v + (((pg * p.kv_heads + rw.hk) << p.lb) + (a & (p.bs - 1))) * D + (lane % kLanesV) * 16;
+        x.v[i] = *reinterpret_cast<const u32x4*>(from);
+      }
+    };
+    auto work = [&](int tile, const Tile& x) {
+      // the two 16-key groups: first key, scales, whether they are there
+      int key[2];
+      float ck[2], lv[2], iv[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int a = tile * 32 + h * 16, e = a >> p.lb;
+        const bool there = e < ne && sh.page[min(e, ne - 1)] >= 0;
+        const int ec = min(e, ne - 1);
+        key[h] = there ? (sh.block[ec] << p.lb) + (a & (p.bs - 1)) : INT32_MAX - 64;
+        ck[h] = sh.ks[ec] * c;
+        const float vs = sh.vs[ec];
+        lv[h] = __builtin_amdgcn_logf(vs);
+        iv[h] = 1.f / vs;
+      }
+      const bool whole = max(key[0], key[1]) + 15 <= least;
+      // V to LDS; codes behind the sequence's end (never written, or of a page
+      // that is not there) are set to 0
+#pragma unroll
+      for (int i = 0; i < kLoadsV; ++i) {
+        const int row = i * (64 / kLanesV) + lane / kLanesV;
+        u32x4 w = x.v[i];
+        if (!whole && (row < 16 ? key[0] : key[1]) + (row & 15) >= rw.len) w = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(vt + v_at<D>(row, lane % kLanesV)) = w;
+      }
+      f32x4 s[MT][2];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[t][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kLoadsK; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const u32x4 a = widen<T>(u32x2{x.k[h][i][2 * y], x.k[h][i][2 * y + 1]});
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s[t][h] = T::mfma16(a, q[t][2 * i + y], s[t][h]);
+          }
+      u32x4 pr[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        float top = -kInf;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float y = fmaf(s[t][h][r], ck[h], lv[h]);
+            if (!whole && key[h] + 4 * g + r > limit[t]) y = -kInf;
+            s[t][h][r] = y;
+            top = fmaxf(top, y);
+          }
+        top = quad_max(top);
+        if (__any(top > m[t])) {
+          const float now = fmaxf(m[t], top);
+          const float shrink = now == -kInf ? 1.f : exp2_fast(m[t] - now);
+          m[t] = now;
+          sum[t] *= shrink;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][i][r] *= shrink;
+        }
+        const float base = m[t] == -kInf ? 0.f : m[t];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float w[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[r] = exp2_fast(s[t][h][r] - base);
+          sum[t] = fmaf((w[0] + w[1]) + (w[2] + w[3]), iv[h], sum[t]);
+          pr[t][2 * h] = T::pack(w[0], w[1]);
+          pr[t][2 * h + 1] = T::pack(w[2], w[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t at = vbase + v_at<D>(vrow, i) + (n & 1) * 8;
+        const u32x4 a = widen<T>(lds_read_tr8(at));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t][i] = T::mfma16(a, pr[t], acc[t][i]);
+      }
+    };
+
+    Tile x, y;
+    int tile = wave;
+    if (tile < tiles) load(tile, x);
+    for (; tile < tiles; tile += 8) {
+      if (tile + 4 < tiles) load(tile + 4, y);
+      work(tile, x);
+      if (tile + 4 < tiles) {
+        if (tile + 8 < tiles) load(tile + 8, x);
+        work(tile + 4, y);
+      }
+    }
+  }
+
+  // Join the wavefronts: rows' maxima and sums, then 16 rows at a time.
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    sum[t] = quad_sum(sum[t]);
+    if (g == 0) {
+      sh.ml[wave][t * 16 + n][0] = m[t];
+      sh.ml[wave][t * 16 + n][1] = sum[t];
+    }
+  }
+  __syncthreads();
+  const int rows = rw.tokens * rw.heads;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    if (t * 16 >= rows) break;
+    float top = -kInf;
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, sh.ml[w][t * 16 + n][0]);
+    const float f = top == -kInf ? 0.f : exp2_fast(m[t] - top);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      *reinterpret_cast<f32x4*>(&sh.join[wave][n][i * 16 + 4 * g]) = f32x4{acc[t][i][0] * f, acc[t][i][1] * f, acc[t][i][2] * f, acc[t][i][3] * f};
+    __syncthreads();
+    for (int e = tid; e < 16 * D / 4; e += 256) {
+      const int r = e / (D / 4), d = (e % (D / 4)) * 4, row = t * 16 + r;
+      if (row >= rows) continue;
+      f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+      float mm = -kInf, l = 0.f;
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, sh.ml[w][row][0]);
+      for (int w = 0; w < 4; ++w) {
+        o += *reinterpret_cast<const f32x4*>(&sh.join[w][r][d]);
+        l += sh.ml[w][row][1] * (mm == -kInf ? 0.f : exp2_fast(sh.ml[w][row][0] - mm));
+      }
+      if (p.splits > 1) {
+        const int64_t at = (item * p.splits + split) * R + row;
+        *reinterpret_cast<f32x4*>(p.part + at * D + d) = o;
+        if (d == 0) {
+          p.part_ml[at * 2] = mm;
+          p.part_ml[at * 2 + 1] = l;
+        }
+      } else {
+        const int64_t tok = rw.first + row / rw.heads, h = rw.head0 + row % rw.heads;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        u32x2 w2;
+        w2[0] = T::pack(o[0] * inv, o[1] * inv);
+        w2[1] = T::pack(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<u32x2*>(static_cast<char*>(p.out) + ((tok * p.heads + h) * D + d) * 2) = w2;
+        if (d == 0) p.lse[tok * p.heads + h] = l == 0.f ? -kInf : (mm + __builtin_amdgcn_logf(l)) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the chunks of a workgroup's rows: one wavefront a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_per) {
+  const int lane = threadIdx.x & 63;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t item = index / rows_per;
+  const int row = static_cast<int>(index % rows_per);
+  if (item >= p.slots * p.kv_heads * p.head_chunks) return;
+  const Rows rw = rows_of(p, item, rows_per);
+  if (row >= rw.tokens * rw.heads) return;
+  const int nb = blocks_seen(p, rw);
+  // chunks that were written: all of a selection's, those of a sequence's blocks
+  const int used = p.blocks != nullptr ? p.splits : min(p.splits, max(1, (nb + p.chunk - 1) / p.chunk));
+  const int64_t at = item * p.splits * rows_per + row;
+  float top = -kInf;
+  for (int s = lane; s < used; s += 64) top = fmaxf(top, p.part_ml[(at + static_cast<int64_t>(s) * rows_per) * 2]);
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  float l = 0.f, o[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) o[i] = 0.f;
+  for (int s = 0; s < used; ++s) {
+    const int64_t a = at + static_cast<int64_t>(s) * rows_per;
+    const float mm = p.part_ml[a * 2], ll = p.part_ml[a * 2 + 1];
+    if (ll == 0.f) continue;
+    const float f = exp2_fast(mm - (top == -kInf ? 0.f : top));
+    l += ll * (ll == ll ? f : 1.f);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) o[i] += p.part[a * D + lane * (D / 64) + i] * f;
+  }
+  const int64_t tok = rw.first + row / rw.heads, h = rw.head0 + row % rw.heads;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  char* to = static_cast<char*>(p.out) + ((tok * p.heads + h) * D + lane * (D / 64)) * 2;
+  if constexpr (D == 128) *reinterpret_cast<uint32_t*>(to) = T::pack(o[0] * inv, o[1] * inv);
+  else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(T::pack(o[0] * inv, 0.f));
+  if (lane == 0) p.lse[tok * p.heads + h] = l == 0.f ? -kInf : (top + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <typename T, int D>
+int launch_decode(const DecodeArgs& p, int mt, hipStream_t stream) {
+  const int64_t items = p.slots * p.kv_heads * p.head_chunks;
+  const int64_t grid = items * p.splits;
+  if (grid > INT32_MAX) return MI_ATTN_EINVAL;
+  const dim3 g(static_cast<unsigned>(grid));
+  if (mt == 1) kv8_attention_kernel<T, D, 1><<<g, dim3(256), 0, stream>>>(p);
+  else if (mt == 2) kv8_attention_kernel<T, D, 2><<<g, dim3(256), 0, stream>>>(p);
+  else kv8_attention_kernel<T, D, 4><<<g, dim3(256), 0, stream>>>(p);
+  if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
+  if (p.splits > 1) {
+    const int64_t joins = (items * mt * 16 + 3) / 4;
+    if (joins > INT32_MAX) return MI_ATTN_EINVAL;
+    kv8_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, mt * 16);
+    if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
+  }
+  return MI_ATTN_OK;
+}
+
+struct Plan {
+  int mt, tokens_per, head_chunks, splits, chunk;
+  int64_t slots, items;
+  uint64_t bytes;
+};
+
+// Rows: as many tiles of 16 as the rows that share their keys fill (all new
+// tokens of a sequence where it reads its whole cache; one token's heads where
+// each token selects its own blocks), 64 at most.  Chunks: about four
+// workgroups for each of the 256 compute units, chunks of 128 keys at least
+// and 2048 at most, so that long and short sequences of a batch even out.
+Plan make_plan(const mi_kv8_attention_args* a) {
+  Plan p;
+  const int group = a->heads / a->kv_heads;
+  const bool sparse = a->blocks != nullptr;
+  const int64_t tokens = sparse || a->num_seqs == 0 ? 1 : (a->total_q + a->num_seqs - 1) / a->num_seqs;
+  const int64_t rows = tokens * group;
+  p.mt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  p.tokens_per = sparse || p.mt * 16 < group ? 1 : p.mt * 16 / group;
+  if (a->cu == nullptr) p.tokens_per = 1;
+  p.head_chunks = (group + p.mt * 16 - 1) / (p.mt * 16);
+  p.slots = slots_of(a->total_q, a->num_seqs, p.tokens_per);
+  p.items = p.slots * a->kv_heads * p.head_chunks;
+  int64_t most = (a->max_length + a->block_size - 1) / a->block_size;
+  if (most > a->block_table_cols) most = a->block_table_cols;
+  if (sparse && most > a->select) most = a->select;
+  if (most < 1) most = 1;
+  const int64_t least = 128 / a->block_size < 1 ? 1 : 128 / a->block_size, top = 2048 / a->block_size;
+  const int64_t want = p.items > 0 ? (1024 + p.items - 1) / p.items : 1;  // chunks of an item
+  int64_t chunk = (most + want - 1) / want;
+  chunk = chunk < least ? least : (chunk > top ? top : chunk);
+  p.chunk = static_cast<int>(chunk);
+  p.splits = static_cast<int>((most + chunk - 1) / chunk);
+  p.bytes = p.splits > 1 ? static_cast<uint64_t>(p.items) * p.splits * p.mt * 16 * (a->dim + 2) * 4 : 0;
+  return p;
+}
+
+int check_decode(const mi_kv8_attention_args* a) {
+  if (a == nullptr) return MI_ATTN_EINVAL;
+  if ((a->dtype != MI_ATTN_BF16 && a->dtype != MI_ATTN_FP16) || (a->dim != 64 && a->dim != 128) ||
+      (a->block_size != 16 && a->block_size != 32 && a->block_size != 64 && a->block_size != 128) || a->kv_heads < 1 ||
+      a->heads < a->kv_heads || a->heads % a->kv_heads || a->heads / a->kv_heads > 128 || a->total_q < 0 ||
+      a->total_q > INT32_MAX || a->num_pages < 0 || a->num_pages > INT32_MAX || a->num_seqs < 0 || a->block_table_cols < 0 ||
+      a->block_table_stride < a->block_table_cols || (a->cu == nullptr && a->total_q != a->num_seqs) || a->max_length < 0 ||
+      (static_cast<int64_t>(a->block_table_cols) * a->block_size >= (1 << 30)) || !(a->scale > 0.f) || !(a->scale < kInf) ||
+      a->q_stride_t < 0 || a->q_stride_h < 0 || ((a->q_stride_t | a->q_stride_h) & 7) ||
+      (a->blocks != nullptr && (a->select < 1 || a->select > MI_ATTN_MAX_SELECT)))
+    return MI_ATTN_EINVAL;
+  return MI_ATTN_OK;
+}
+
+}  // namespace
+}  // namespace miattn
+
+using namespace miattn;
+
+MI_ATTN_EXPORT uint64_t kv8_attention_workspace(const mi_kv8_attention_args* args) {
+  return check_decode(args) == MI_ATTN_OK ? make_plan(args).bytes : 0;
+}
+
+MI_ATTN_EXPORT int kv8_attention(const mi_kv8_attention_args* a, hipStream_t stream) {
+  const int st = check_decode(a);
+  if (st != MI_ATTN_OK) return st;
+  const void* wide[] = {a->q, a->k_cache, a->v_cache, a->out, a->workspace};
+  for (const void* x : wide)
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return MI_ATTN_EINVAL;
+  const void* words[] = {a->k_scale, a->v_scale, a->block_table, a->lengths, a->cu, a->blocks, a->lse};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return MI_ATTN_EINVAL;
+  if (a->total_q == 0) return MI_ATTN_OK;
+  if (a->q == nullptr || a->out == nullptr || a->lse == nullptr || (a->num_seqs > 0 && a->lengths == nullptr)) return MI_ATTN_EINVAL;
+  if (a->num_seqs > 0 && a->block_table_cols > 0 && a->block_table == nullptr) return MI_ATTN_EINVAL;
+  if (a->num_pages > 0 && (a->k_cache == nullptr || a->v_cache == nullptr || a->k_scale == nullptr || a->v_scale == nullptr)) return MI_ATTN_EINVAL;
+  const Plan plan = make_plan(a);
+  if (plan.bytes > 0 && (a->workspace == nullptr || a->workspace_bytes < plan.bytes)) return MI_ATTN_EWORKSPACE;
+  DecodeArgs p;
+  p.q = a->q; p.k = static_cast<const uint8_t*>(a->k_cache); p.v = static_cast<const uint8_t*>(a->v_cache);
+  p.k_scale = a->k_scale; p.v_scale = a->v_scale; p.table = a->block_table; p.lengths = a->lengths; p.cu = a->cu;
+  p.blocks = a->blocks; p.out = a->out; p.lse = a->lse;
+  p.part = static_cast<float*>(a->workspace);
+  p.part_ml = p.part == nullptr ? nullptr : p.part + plan.items * plan.splits * plan.mt * 16 * a->dim;
+  p.q_t = a->q_stride_t; p.q_h = a->q_stride_h; p.total_q = a->total_q; p.num_pages = a->num_pages;
+  p.table_stride = a->block_table_stride; p.slots = plan.slots;
+  // without pages nothing can be seen
+  p.table_cols = a->num_pages > 0 ? a->block_table_cols : 0;
+  p.num_seqs = a->num_seqs; p.heads = a->heads; p.kv_heads = a->kv_heads; p.group = a->heads / a->kv_heads;
+  p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
+  p.select = a->select; p.tokens_per = plan.tokens_per; p.head_chunks = plan.head_chunks; p.splits = plan.splits;
+  p.chunk = plan.chunk; p.scale = a->scale;
+  if (a->dtype == MI_ATTN_BF16)
+    return a->dim == 128 ? launch_decode<Bf16, 128>(p, plan.mt, stream) : launch_decode<Bf16, 64>(p, plan.mt, stream);
+  return a->dim == 128 ? launch_decode<Fp16, 128>(p, plan.mt, stream) : launch_decode<Fp16, 64>(p, plan.mt, stream);
+}

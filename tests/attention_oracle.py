@@ -86,3 +86,78 @@ def scores(q, mean_of, bs, max_blocks, placed, hk, first, last, scale=None):
             else:
                 out[row, :, b] = (q[row].double().view(hk, g, d) * m.double()[:, None]).sum(2).amax(1) * scale
     return out, counts
+
+
+def scale_for(most):
+    """The smallest power of two, 2^-60 at least, that brings ``most`` to 448 or less."""
+    s = 2.0 ** -60
+    while most > 448 * s:
+        s *= 2
+    return s
+
+
+def append(k, v, k_cache, v_cache, k_scale, v_scale, table, lengths, bs, cu=None, k_mean=None):
+    """kv8_append on CPU copies, a page and head at a time; caches as float values of the codes."""
+    n = len(lengths)
+    for i in range(n):
+        a, b = (i, i + 1) if cu is None else (int(cu[i]), int(cu[i + 1]))
+        length = int(lengths[i])
+        start = length - (b - a)
+        for j in range(max(start, 0) // bs, -(-length // bs) if b > a else 0):
+            if j >= table.shape[1] or not 0 <= int(table[i, j]) < k_cache.shape[0]:
+                continue
+            page = int(table[i, j])
+            lo, hi = max(0, start - j * bs), min(bs, length - j * bs)
+            for x, cache, scale in ((k, k_cache, k_scale), (v, v_cache, v_scale)):
+                for c in range(x.shape[1]):
+                    new = x[a + j * bs + lo - start:a + j * bs + hi - start, c].double()
+                    finite = new[torch.isfinite(new)].abs()
+                    s = scale_for(finite.max().item() if finite.numel() else 0.0)
+                    old = float(scale[page, c])
+                    if lo > 0:
+                        s = max(s, old)
+                        if s > old:
+                            cache[page, c, :lo] = round8(cache[page, c, :lo].double() * old / s)
+                    cache[page, c, lo:hi] = round8(new / s)
+                    scale[page, c] = s
+            if k_mean is not None:
+                k_mean[page] = (k_cache[page, :, :hi].double().mean(1) * k_scale[page, :, None].double()).to(k_mean.dtype)
+
+
+def round8(x):
+    """Rounded to nearest even e4m3, values behind 448 to it."""
+    return x.clamp(-448, 448).float().to(torch.float8_e4m3fn).float()
+
+
+def cache_attention(q, k_cache, v_cache, k_scale, v_scale, table, lengths, bs, cu=None, blocks=None, scale=None):
+    """(out, lse) of kv8_attention in 64 bits; caches as float values of the codes."""
+    t, h, d = q.shape
+    hk = k_cache.shape[1]
+    g = h // hk
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    out, lse = torch.zeros(t, h, d, dtype=torch.float64), torch.full((t, h), -math.inf, dtype=torch.float64)
+    for i in range(len(lengths)):
+        a, b = (i, i + 1) if cu is None else (int(cu[i]), int(cu[i + 1]))
+        for r in range(a, b):
+            pos = int(lengths[i]) - (b - a) + r - a
+            if pos < 0:
+                continue
+            pos = min(pos, table.shape[1] * bs - 1)
+            for c in range(hk):
+                seen = range(pos // bs + 1)
+                if blocks is not None:
+                    seen = sorted({x for x in blocks[r, c].tolist() if 0 <= x <= pos // bs})
+                ks, vs = [], []
+                for x in seen:
+                    page = int(table[i, x])
+                    if 0 <= page < k_cache.shape[0]:
+                        e = min(bs, pos + 1 - x * bs)
+                        ks.append(k_cache[page, c, :e].double() * float(k_scale[page, c]))
+                        vs.append(v_cache[page, c, :e].double() * float(v_scale[page, c]))
+                if not ks:
+                    continue
+                heads = slice(c * g, (c + 1) * g)
+                s = q[r, heads].double() @ torch.cat(ks).T * scale
+                lse[r, heads] = torch.logsumexp(s, 1)
+                out[r, heads] = torch.softmax(s, 1) @ torch.cat(vs)
+    return out, lse
