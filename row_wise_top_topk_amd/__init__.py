@@ -15,14 +15,15 @@ import threading
 import torch
 
 from . import attention
-from .attention import block_attention, block_means, block_scores, kv8_append, kv8_attention
+from .attention import (block_attention, block_attention_backward, block_means, block_scores, kv8_append,
+                        kv8_attention)
 
 __all__ = [
     "PATH_AUTO", "PATH_LOCAL", "PATH_SPLIT", "PATH_CHUNKS", "PATH_PERSIST", "PLAN_PERSIST",
     "library_path", "load_library", "topk_indices", "workspace_size",
     "plan_describe", "debug_keys", "workspace_error", "status_string",
     "c128a_active_width", "c128a_topk_metadata",
-    "block_means", "block_scores", "block_attention", "kv8_append", "kv8_attention",
+    "block_means", "block_scores", "block_attention", "block_attention_backward", "kv8_append", "kv8_attention",
 ]
 
 PATH_AUTO, PATH_LOCAL, PATH_SPLIT, PATH_CHUNKS, PATH_PERSIST = 0, 1, 2, 3, 4

@@ -25,7 +25,7 @@ import math
 
 import torch
 
-__all__ = ["block_means", "block_scores", "block_attention", "kv8_append", "kv8_attention"]
+__all__ = ["block_means", "block_scores", "block_attention", "block_attention_backward", "kv8_append", "kv8_attention"]
 
 BLOCK_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
@@ -80,6 +80,10 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.block_scores.restype = ctypes.c_int
     lib.block_attention.argtypes = [ctypes.POINTER(_AttentionArgs), _vp]
     lib.block_attention.restype = ctypes.c_int
+    lib.block_attention_workspace.argtypes = [ctypes.POINTER(_AttentionArgs)]
+    lib.block_attention_workspace.restype = ctypes.c_uint64
+    lib.block_attention_backward.argtypes = [ctypes.POINTER(_AttentionArgs), _vp]
+    lib.block_attention_backward.restype = ctypes.c_int
     lib.kv8_append.argtypes = [ctypes.POINTER(_AppendArgs), _vp]
     lib.kv8_append.restype = ctypes.c_int
     lib.kv8_attention.argtypes = [ctypes.POINTER(_DecodeArgs), _vp]
@@ -315,7 +319,14 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
 
     Returns ``(out, lse)``: ``[tokens, heads, dim]`` of q's type, and the
     log-sum of the scaled scores' exponentials, float32 ``[tokens, heads]``.  A
-    query that sees no key, and a row behind the last sequence, has 0 and -inf."""
+    query that sees no key, and a row behind the last sequence, has 0 and -inf.
+
+    Differentiable in q, k and v through autograd (``lse`` is not; ``out=`` is
+    refused then).  Inputs are taken to be finite."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
+        if out is not None:
+            raise ValueError("out cannot be given where a gradient is asked for")
+        return _BlockAttention.apply(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     out = _output(out, q.shape, q.dtype, q.device, "out")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
@@ -323,6 +334,55 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     with torch.cuda.device(q.device):
         _check(_lib().block_attention(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream), "block_attention")
     return out, lse
+
+
+def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                             lse: torch.Tensor, blocks: torch.Tensor, block_size: int, cu_seqlens: torch.Tensor = None,
+                             cu_seqlens_k: torch.Tensor = None, scale: float = None, causal: bool = True):
+    """Gradients ``(dq, dk, dv)`` of ``block_attention`` for the gradient ``dout``
+    of its ``out``; ``out`` and ``lse`` as it returned them, the rest as it was
+    called.  The result is the same from run to run.  With float16 the scores'
+    gradients are held in float16: below about 6e-8 they are lost (scale the
+    loss)."""
+    a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
+    _heads(dout, "dout", q.device, q.dtype, int(q.shape[2]))
+    if dout.shape != q.shape:
+        raise ValueError("dout must have q's shape")
+    _output(out, q.shape, q.dtype, q.device, "out")
+    _output(lse, q.shape[:2], torch.float32, q.device, "lse")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+    a.out, a.lse, a.dout, a.dq, a.dk, a.dv = (_ptr(t) for t in (out, lse, dout, dq, dk, dv))
+    a.dout_stride_t, a.dout_stride_h = _strides(dout)
+    lib = _lib()
+    with torch.cuda.device(q.device):
+        a.workspace_bytes = lib.block_attention_workspace(ctypes.byref(a))
+        workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=q.device)
+        a.workspace = workspace.data_ptr()
+        _check(lib.block_attention_backward(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream),
+               "block_attention_backward")
+    return dq, dk, dv
+
+
+class _BlockAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
+        out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
+        ctx.save_for_backward(q, k, v, out, lse, blocks, cu_seqlens, cu_seqlens_k)
+        ctx.rest = (block_size, scale, causal)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, _):
+        q, k, v, out, lse, blocks, cu_q, cu_k = ctx.saved_tensors
+        block_size, scale, causal = ctx.rest
+        if dout.stride(2) != 1 or dout.data_ptr() % 16 or any(dout.stride(i) % 8 for i in (0, 1)):
+            dout = dout.clone(memory_format=torch.contiguous_format)
+        dq, dk, dv = block_attention_backward(dout, q, k, v, out, lse, blocks, block_size, cu_q, cu_k, scale, causal)
+        need = ctx.needs_input_grad
+        return dq if need[0] else None, dk if need[1] else None, dv if need[2] else None, *(None,) * 6
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, device, hk=None, dim=None):

@@ -1,10 +1,12 @@
-// What the forward and the backward of the block sparse attention share.
+// What the forward and the backward of the block sparse attention share: the
+// arguments, and the walk of a workgroup's rows over the blocks they select.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "attention/mi_block_attention.h"
+#include "attn_device.hpp"
 
 #define MI_ATTN_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -30,5 +32,172 @@ struct Args {
 };
 
 int make_args(const mi_block_attention_args* a, Args& p);
+
+constexpr int kRows = 128;        // rows of a workgroup
+constexpr int kTile = 64;         // keys of a tile
+constexpr int kMaskWords = 2048;  // words of token bits, window of block numbers x words per block
+
+struct Select {
+  uint32_t mask[kMaskWords];
+  uint16_t list[kMaskWords];
+  uint32_t wave_count[4];
+};
+
+// The tokens of one workgroup and how its rows map to them.
+struct Group {
+  int64_t t0, begin, tk0;  // first token; the sequence's first token and first key
+  int32_t tokens;          // tokens of this workgroup
+  int32_t len_k;
+  int32_t shift;           // position of token t: t - begin + shift
+  int32_t blocks;          // blocks that any of its rows can see
+};
+
+__device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
+  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, tq);
+  Group g;
+  g.t0 = at.first;
+  g.begin = at.begin;
+  const int64_t left = at.end - at.first;
+  g.tokens = static_cast<int32_t>(left < 0 ? 0 : (left < tq ? left : tq));
+  g.tk0 = 0;
+  g.len_k = 0;
+  if (at.seq < p.num_seqs) {
+    g.tk0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
+    const int64_t n = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - g.tk0;
+    g.len_k = static_cast<int32_t>(n < 0 ? 0 : n);
+  }
+  g.shift = g.len_k - static_cast<int32_t>(at.end - at.begin);
+  int64_t seen = g.len_k;
+  if (p.causal) {
+    const int64_t last = at.first - at.begin + g.tokens - 1 + g.shift;
+    if (last + 1 < seen) seen = last + 1 < 0 ? 0 : last + 1;
+  }
+  g.blocks = g.tokens > 0 ? static_cast<int32_t>((seen + p.bs - 1) >> p.lb) : 0;
+  return g;
+}
+
+// Marks which tokens select each block of [w0, w0 + width) and lists the blocks
+// that any does, ascending.  Returns their number.  Ends with a barrier.
+__device__ __forceinline__ int list_window(const Args& p, const Group& g, int hk, int w0, int width, int nw, Select& s) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  for (int i = tid; i < width * nw; i += 256) s.mask[i] = 0;
+  __syncthreads();
+  const int most = min(width, g.blocks - w0);
+  const int32_t* rows = p.blocks + (g.t0 * p.kv_heads + hk) * static_cast<int64_t>(p.select);
+  const int64_t stride = static_cast<int64_t>(p.kv_heads) * p.select;
+  const int total = g.tokens * p.select;
+  for (int i = tid; i < total; i += 256) {
+    const int tl = i / p.select;
+    const int b = rows[tl * stride + (i - tl * p.select)] - w0;
+    if (b >= 0 && b < most) atomicOr(&s.mask[b * nw + (tl >> 5)], 1u << (tl & 31));
+  }
+  __syncthreads();
+  // every thread has width / 256 consecutive blocks; counts are summed over
+  // the lanes, then over the wavefronts
+  const int each = (width + 255) >> 8;
+  int mine = 0;
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    uint32_t any = 0;
+    if (b < most)
+      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
+    mine += any != 0;
+  }
+  int sum = mine;
+  const int lane = tid & 63, wave = tid >> 6;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(sum, d);
+    if (lane >= d) sum += up;
+  }
+  if (lane == 63) s.wave_count[wave] = sum;
+  __syncthreads();
+  int at = sum - mine;
+  int count = 0;
+  for (int w = 0; w < 4; ++w) {
+    const int c = s.wave_count[w];
+    if (w < wave) at += c;
+    count += c;
+  }
+  for (int i = 0; i < each; ++i) {
+    const int b = tid * each + i;
+    uint32_t any = 0;
+    if (b < most)
+      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
+    if (any != 0) s.list[at++] = static_cast<uint16_t>(b);
+  }
+  __syncthreads();
+  return count;
+}
+
+// The four 16-key groups of a tile: first key of each in its sequence, or -1.
+struct Keys {
+  int32_t key[4];
+  int32_t id[4];  // place of the block in the window
+};
+
+__device__ __forceinline__ Keys keys_of(const Select& s, int lb, int bs, int w0, int active, int tile) {
+  Keys k;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = tile * kTile + 16 * i;
+    const int e = a >> lb;
+    k.key[i] = -1;
+    k.id[i] = 0;
+    if (e < active) {
+      k.id[i] = __builtin_amdgcn_readfirstlane(s.list[e]);
+      k.key[i] = ((w0 + k.id[i]) << lb) + (a & (bs - 1));
+    }
+  }
+  return k;
+}
+
+// Copies 64 rows of D elements into an LDS tile, straight from memory.
+template <int D>
+__device__ __forceinline__ void stage_tile(void* tile, const char* base, int64_t stride_bytes, const Keys& k, int len_k,
+                                           int wave, int lane) {
+  constexpr int kChunks = D / 8;
+  constexpr int kRowsPer = 64 / kChunks;  // rows of one instruction
+  const int sub = lane / kChunks, chunk = lane % kChunks;
+#pragma unroll
+  for (int j = 0; j < kTile / (4 * kRowsPer); ++j) {
+    const int row0 = (j * 4 + wave) * kRowsPer;
+    const int row = row0 + sub;
+    int key = k.key[0];
+    if (row0 >= 16) key = k.key[1];
+    if (row0 >= 32) key = k.key[2];
+    if (row0 >= 48) key = k.key[3];
+    key += row & 15;
+    key = max(0, min(key, len_k - 1));
+    const char* from = base + key * stride_bytes + ((chunk ^ swizzle<D>(row)) << 4);
+    __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(from), (MI_LDS void*)(static_cast<char*>(tile) + row0 * 2 * D), 16, 0, 0);
+  }
+}
+
+// What a lane's row may see of a tile: for each 16-key group the last visible
+// offset (relative to the group's first key), -1 for none.
+struct Sight {
+  int32_t last[4];
+  bool any;   // some row of the wavefront sees something
+  bool full;  // every valid row sees all 64 keys
+};
+
+__device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw, int word, int bit, int limit, bool valid) {
+  Sight v;
+  bool some = false, all = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.last[i] = -1;
+    if (k.key[i] >= 0 && ((s.mask[k.id[i] * nw + word] >> bit) & 1u)) v.last[i] = limit - k.key[i];
+    some |= v.last[i] >= 0;
+    all &= v.last[i] >= 15;
+  }
+  v.any = __any(valid && some);
+  v.full = __all(!valid || all);
+  return v;
+}
+
+// Every load of this wavefront straight into LDS has arrived.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace miattn

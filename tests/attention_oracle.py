@@ -26,7 +26,9 @@ def visible(blocks_row, bs, keys, pos, causal=True):
 
 
 def attention(q, k, v, blocks, bs, cu_q=None, cu_k=None, scale=None, causal=True, dout=None):
-    """(out, lse) in 64 bits, or (out, lse, dq, dk, dv) with ``dout``.  CPU tensors."""
+    """(out, lse) in 64 bits, or with ``dout`` (out, lse, dq, dk, dv, sizes):
+    ``sizes`` are, for dq, dk and dv, the sums of the absolute terms, where a
+    score's gradient counts with what a rounding of out moves it by.  CPU tensors."""
     t, h, d = q.shape
     hk = k.shape[1]
     g = h // hk
@@ -34,6 +36,7 @@ def attention(q, k, v, blocks, bs, cu_q=None, cu_k=None, scale=None, causal=True
     q, k, v = q.double(), k.double(), v.double()
     out, lse = torch.zeros(t, h, d, dtype=torch.float64), torch.full((t, h), -math.inf, dtype=torch.float64)
     dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    sq, sk, sv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
     for a, b, c, e in spans(t, k.shape[0], cu_q, cu_k):
         for r in range(a, b):
             for hh in range(hk):
@@ -52,7 +55,11 @@ def attention(q, k, v, blocks, bs, cu_q=None, cu_k=None, scale=None, causal=True
                     ds = p * (do @ v[at, hh].T - (do * out[r, heads]).sum(1, keepdim=True)) * scale
                     dq[r, heads] = ds @ k[at, hh]
                     dk[at, hh] += ds.T @ q[r, heads]
-    return (out, lse) if dout is None else (out, lse, dq, dk, dv)
+                    size = ds.abs() + p * (do * out[r, heads]).abs().sum(1, keepdim=True) * scale
+                    sq[r, heads] = size @ k[at, hh].abs()
+                    sk[at, hh] += size.T @ q[r, heads].abs()
+                    sv[at, hh] += p.T @ do.abs()
+    return (out, lse) if dout is None else (out, lse, dq, dk, dv, (sq, sk, sv))
 
 
 def means(k, bs, cu=None):
