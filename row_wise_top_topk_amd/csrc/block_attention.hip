@@ -77,32 +77,47 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
     const int tiles = ((active << p.lb) + kTile - 1) / kTile;
+    if (tiles == 0) continue;
     Keys next = keys_of(sh.sel, p.lb, p.bs, w0, active, 0);
-    if (tiles > 0) {
-      stage_tile<D>(sh.k[0], kbase, p.k_t * 2, next, g.len_k, wave, lane);
-      stage_tile<D>(sh.v[0], vbase, p.v_t * 2, next, g.len_k, wave, lane);
-    }
+    Half<D> kin, vin;
+    kin.load(kbase, p.k_t * 2, next, g.len_k);
+    vin.load(vbase, p.v_t * 2, next, g.len_k);
     for (int tile = 0; tile < tiles; ++tile) {
       const Keys keys = next;
-      wait_loads();
-      __syncthreads();
       const int buf = tile & 1;
+      kin.store(sh.k[buf]);
+      vin.store(sh.v[buf]);
+      __syncthreads();
       if (tile + 1 < tiles) {
         next = keys_of(sh.sel, p.lb, p.bs, w0, active, tile + 1);
-        stage_tile<D>(sh.k[buf ^ 1], kbase, p.k_t * 2, next, g.len_k, wave, lane);
-        stage_tile<D>(sh.v[buf ^ 1], vbase, p.v_t * 2, next, g.len_k, wave, lane);
+        kin.load(kbase, p.k_t * 2, next, g.len_k);
+        vin.load(vbase, p.v_t * 2, next, g.len_k);
       }
       const Sight see = sight_of(sh.sel, keys, nw, tl >> 5 < nw ? tl >> 5 : 0, tl & 31, limit, valid);
       if (!see.any) continue;
       const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
       f32x16 s[2];
+      {
+        u32x4 ka[2][D / 16];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
+          for (int i = 0; i < D / 16; ++i) ka[mt][i] = lds_read16(ks + mt * 32 * 2 * D + (kread ^ (i * 32)));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          s[mt] = T::mfma32(lds_read16(ks + mt * 32 * 2 * D + (kread ^ (i * 32))), q[i], s[mt]);
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) s[mt] = T::mfma32(ka[mt][i], q[i], s[mt]);
+        }
+        // reads of the first 32 keys, then a product and a read of the others in turn
+        __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, D / 16, 0);
       }
       if (!see.full) {
 #pragma unroll
@@ -119,7 +134,9 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[1][r]);
       top = half_max(top);
-      if (__any(top > m)) {
+      // The weights stay relative to an older maximum until it is passed by
+      // 2^8: their sums are divided out at the end, and a weight keeps its bits.
+      if (__any((top - m) * c > 8.f || (m == -kInf && top > m))) {
         const float now = fmaxf(m, top);
         const float shrink = now == -kInf ? 1.f : exp2_fast((m - now) * c);
         m = now;
@@ -139,16 +156,29 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
           sum += x + y;
           pr[mt * 2 + (r >> 3)][(r & 7) >> 1] = T::pack(x, y);
         }
+      {
+        u32x4 va[D / 32][4];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+        for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          const uint32_t r0 = 16 * st + vrow;
-          const uint32_t a0 = vs + tile_at<D>(r0, 4 * i + vchunk) + (li & 1) * 8;
-          const uint32_t a1 = vs + tile_at<D>(r0 + 8, 4 * i + vchunk) + (li & 1) * 8;
-          const u32x2 x = lds_read_tr16(a0), y = lds_read_tr16(a1);
-          acc[i] = T::mfma32(u32x4{x[0], x[1], y[0], y[1]}, pr[st], acc[i]);
+          for (int st = 0; st < 4; ++st) {
+            const uint32_t r0 = 16 * st + vrow;
+            const u32x2 x = lds_read_tr16(vs + tile_at<D>(r0, 4 * i + vchunk) + (li & 1) * 8);
+            const u32x2 y = lds_read_tr16(vs + tile_at<D>(r0 + 8, 4 * i + vchunk) + (li & 1) * 8);
+            va[i][st] = u32x4{x[0], x[1], y[0], y[1]};
+          }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
+        __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8 - 4; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      }
     }
   }
   sum = half_sum(sum);

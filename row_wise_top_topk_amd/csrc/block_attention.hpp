@@ -46,6 +46,7 @@ struct Select {
 // The tokens of one workgroup and how its rows map to them.
 struct Group {
   int64_t t0, begin, tk0;  // first token; the sequence's first token and first key
+  int64_t row0;            // number of its first block among the packed ones
   int32_t tokens;          // tokens of this workgroup
   int32_t len_k;
   int32_t shift;           // position of token t: t - begin + shift
@@ -60,11 +61,13 @@ __device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
   const int64_t left = at.end - at.first;
   g.tokens = static_cast<int32_t>(left < 0 ? 0 : (left < tq ? left : tq));
   g.tk0 = 0;
+  g.row0 = 0;
   g.len_k = 0;
   if (at.seq < p.num_seqs) {
     g.tk0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
     const int64_t n = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - g.tk0;
     g.len_k = static_cast<int32_t>(n < 0 ? 0 : n);
+    g.row0 = g.tk0 / p.bs + at.seq;
   }
   g.shift = g.len_k - static_cast<int32_t>(at.end - at.begin);
   int64_t seen = g.len_k;
@@ -138,41 +141,49 @@ struct Keys {
 
 __device__ __forceinline__ Keys keys_of(const Select& s, int lb, int bs, int w0, int active, int tile) {
   Keys k;
+  int id[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) id[i] = s.list[min((tile * kTile + 16 * i) >> lb, active - 1)];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int a = tile * kTile + 16 * i;
-    const int e = a >> lb;
-    k.key[i] = -1;
-    k.id[i] = 0;
-    if (e < active) {
-      k.id[i] = __builtin_amdgcn_readfirstlane(s.list[e]);
-      k.key[i] = ((w0 + k.id[i]) << lb) + (a & (bs - 1));
-    }
+    k.id[i] = __builtin_amdgcn_readfirstlane(id[i]);
+    k.key[i] = (a >> lb) < active ? ((w0 + k.id[i]) << lb) + (a & (bs - 1)) : -1;
   }
   return k;
 }
 
-// Copies 64 rows of D elements into an LDS tile, straight from memory.
+// Half of a tile on its way from memory to LDS: 64 rows of D elements over 256
+// threads, held in registers while the tile before it is worked on.
 template <int D>
-__device__ __forceinline__ void stage_tile(void* tile, const char* base, int64_t stride_bytes, const Keys& k, int len_k,
-                                           int wave, int lane) {
-  constexpr int kChunks = D / 8;
-  constexpr int kRowsPer = 64 / kChunks;  // rows of one instruction
-  const int sub = lane / kChunks, chunk = lane % kChunks;
+struct Half {
+  static constexpr int kLanes = D / 8;           // threads of a row
+  static constexpr int kRowsAt = 256 / kLanes;   // rows of one step
+  static constexpr int kSteps = kTile / kRowsAt;
+  u32x4 x[kSteps];
+
+  __device__ __forceinline__ void load(const char* base, int64_t stride_bytes, const Keys& k, int len_k) {
+    const int tid = threadIdx.x;
+    const char* from = base + (tid % kLanes) * 16;
 #pragma unroll
-  for (int j = 0; j < kTile / (4 * kRowsPer); ++j) {
-    const int row0 = (j * 4 + wave) * kRowsPer;
-    const int row = row0 + sub;
-    int key = k.key[0];
-    if (row0 >= 16) key = k.key[1];
-    if (row0 >= 32) key = k.key[2];
-    if (row0 >= 48) key = k.key[3];
-    key += row & 15;
-    key = max(0, min(key, len_k - 1));
-    const char* from = base + key * stride_bytes + ((chunk ^ swizzle<D>(row)) << 4);
-    __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(from), (MI_LDS void*)(static_cast<char*>(tile) + row0 * 2 * D), 16, 0, 0);
+    for (int j = 0; j < kSteps; ++j) {
+      int key;
+      if constexpr (kRowsAt == 16) key = k.key[j];
+      else key = tid < 128 ? k.key[2 * j] : k.key[2 * j + 1];
+      key += (tid / kLanes) & 15;
+      key = max(0, min(key, len_k - 1));
+      x[j] = *reinterpret_cast<const u32x4*>(from + static_cast<uint64_t>(static_cast<uint32_t>(key)) * static_cast<uint64_t>(stride_bytes));
+    }
   }
-}
+  __device__ __forceinline__ void store(char* tile) const {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const uint32_t row = j * kRowsAt + tid / kLanes;
+      *reinterpret_cast<u32x4*>(tile + tile_at<D>(row, tid % kLanes)) = x[j];
+    }
+  }
+};
 
 // What a lane's row may see of a tile: for each 16-key group the last visible
 // offset (relative to the group's first key), -1 for none.
@@ -185,10 +196,12 @@ struct Sight {
 __device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw, int word, int bit, int limit, bool valid) {
   Sight v;
   bool some = false, all = true;
+  uint32_t bits[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits[i] = s.mask[k.id[i] * nw + word];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v.last[i] = -1;
-    if (k.key[i] >= 0 && ((s.mask[k.id[i] * nw + word] >> bit) & 1u)) v.last[i] = limit - k.key[i];
+    v.last[i] = k.key[i] >= 0 && ((bits[i] >> bit) & 1u) ? limit - k.key[i] : -1;
     some |= v.last[i] >= 0;
     all &= v.last[i] >= 15;
   }
@@ -196,8 +209,5 @@ __device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw
   v.full = __all(!valid || all);
   return v;
 }
-
-// Every load of this wavefront straight into LDS has arrived.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 }  // namespace miattn

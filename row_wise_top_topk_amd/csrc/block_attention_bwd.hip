@@ -34,7 +34,23 @@ struct BackArgs {
   int64_t words;
   int32_t piece;       // tokens of a piece
   int32_t max_pieces;
+  uint32_t group_magic;  // n / group = n * group_magic >> 32 for n below 2^24, group above 1
 };
+
+// Which tokens of the workgroup selected each listed block, into the bit matrix:
+// tokens t0 .. t0 + 31 of mask word w lie in two words of a block's row.
+__device__ __forceinline__ void mark_tokens(const BackArgs& b, const Group& g, int hk, int w0, int active, int nw, const Select& s) {
+  for (int i = threadIdx.x; i < active * nw; i += 256) {
+    const int id = s.list[i / nw], w = i % nw;
+    const uint32_t x = s.mask[id * nw + w];
+    if (x == 0) continue;
+    const int64_t t = g.t0 + 32 * w;
+    uint32_t* to = b.bits + (hk * b.rows + g.row0 + w0 + id) * b.words + (t >> 5);
+    const int up = static_cast<int>(t & 31);
+    if (x << up) atomicOr(to, x << up);
+    if (up > 0 && (x >> (32 - up))) atomicOr(to + 1, x >> (32 - up));
+  }
+}
 
 // ---- dq ----
 
@@ -110,55 +126,88 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
+    mark_tokens(b, g, hk, w0, active, nw, sh.sel);
     const int tiles = ((active << p.lb) + kTile - 1) / kTile;
+    if (tiles == 0) continue;
     Keys next = keys_of(sh.sel, p.lb, p.bs, w0, active, 0);
-    if (tiles > 0) {
-      stage_tile<D>(sh.k[0], kbase, p.k_t * 2, next, g.len_k, wave, lane);
-      stage_tile<D>(sh.v[0], vbase, p.v_t * 2, next, g.len_k, wave, lane);
-    }
+    Half<D> kin, vin;
+    kin.load(kbase, p.k_t * 2, next, g.len_k);
+    vin.load(vbase, p.v_t * 2, next, g.len_k);
     for (int tile = 0; tile < tiles; ++tile) {
       const Keys keys = next;
-      wait_loads();
-      __syncthreads();
       const int buf = tile & 1;
+      kin.store(sh.k[buf]);
+      vin.store(sh.v[buf]);
+      __syncthreads();
       if (tile + 1 < tiles) {
         next = keys_of(sh.sel, p.lb, p.bs, w0, active, tile + 1);
-        stage_tile<D>(sh.k[buf ^ 1], kbase, p.k_t * 2, next, g.len_k, wave, lane);
-        stage_tile<D>(sh.v[buf ^ 1], vbase, p.v_t * 2, next, g.len_k, wave, lane);
+        kin.load(kbase, p.k_t * 2, next, g.len_k);
+        vin.load(vbase, p.v_t * 2, next, g.len_k);
       }
       const Sight see = sight_of(sh.sel, keys, nw, tl >> 5 < nw ? tl >> 5 : 0, tl & 31, limit, valid);
       if (!see.any) continue;
       const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
-#pragma unroll
+#pragma unroll 1
       for (int mt = 0; mt < 2; ++mt) {
+        const uint32_t off = mt * 32 * 2 * D;
         f32x16 s, dp;
+        {
+          u32x4 ka[D / 16], va[D / 16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+          for (int i = 0; i < D / 16; ++i) ka[i] = lds_read16(ks + off + (kread ^ (i * 32)));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) s = T::mfma32(lds_read16(ks + mt * 32 * 2 * D + (kread ^ (i * 32))), q[i], s);
+          for (int i = 0; i < D / 16; ++i) va[i] = lds_read16(vs + off + (kread ^ (i * 32)));
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) dp = T::mfma32(lds_read16(vs + mt * 32 * 2 * D + (kread ^ (i * 32))), go[i], dp);
+          for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) s = T::mfma32(ka[i], q[i], s);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) dp = T::mfma32(va[i], go[i], dp);
+          // four reads ahead of the products
+          __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+          for (int i = 0; i < D / 8 - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        }
         u32x4 ds[2];
+        const int last0 = mt == 0 ? see.last[0] : see.last[2], last1 = mt == 0 ? see.last[1] : see.last[3];
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
           float w[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int off = 8 * (((r + e) >> 2) & 1) + ((r + e) & 3);
+            const int at = 8 * (((r + e) >> 2) & 1) + ((r + e) & 3);
             w[e] = exp2_fast(fmaf(s[r + e], c, -lse2)) * (dp[r + e] - delta);
-            if (!see.full && off + 4 * half > see.last[mt * 2 + (r >> 3)]) w[e] = 0.f;
+            if (!see.full && at + 4 * half > (r < 8 ? last0 : last1)) w[e] = 0.f;
           }
           ds[r >> 3][(r & 7) >> 1] = T::pack(w[0], w[1]);
         }
+        {
+          u32x4 ka[D / 32][2];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
+          for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint32_t r0 = mt * 32 + 16 * st + trow;
-            const u32x2 x = lds_read_tr16(ks + tile_at<D>(r0, 4 * i + tchunk) + (li & 1) * 8);
-            const u32x2 y = lds_read_tr16(ks + tile_at<D>(r0 + 8, 4 * i + tchunk) + (li & 1) * 8);
-            acc[i] = T::mfma32(u32x4{x[0], x[1], y[0], y[1]}, ds[st], acc[i]);
+            for (int st = 0; st < 2; ++st) {
+              const uint32_t r0 = 16 * st + trow;
+              const u32x2 x = lds_read_tr16(ks + off + tile_at<D>(r0, 4 * i + tchunk) + (li & 1) * 8);
+              const u32x2 y = lds_read_tr16(ks + off + tile_at<D>(r0 + 8, 4 * i + tchunk) + (li & 1) * 8);
+              ka[i][st] = u32x4{x[0], x[1], y[0], y[1]};
+            }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) acc[i] = T::mfma32(ka[i][st], ds[st], acc[i]);
+          __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+          for (int i = 0; i < D / 16 - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
           }
+          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        }
       }
     }
   }
@@ -175,30 +224,11 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
     }
 }
 
-// ---- which tokens selected a block ----
+// ---- the pieces of each block's tokens ----
 
 __global__ void __launch_bounds__(256) clear_bits_kernel(BackArgs b) {
   const int64_t total = b.a.kv_heads * b.rows * b.words;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) b.bits[i] = 0;
-}
-
-// One thread per selected entry.
-__global__ void __launch_bounds__(256) mark_bits_kernel(BackArgs b) {
-  const Args& p = b.a;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.total_q * p.kv_heads * p.select) return;
-  const int64_t tok = i / (static_cast<int64_t>(p.kv_heads) * p.select);
-  const int hk = static_cast<int>((i / p.select) % p.kv_heads);
-  const int blk = p.blocks[i];
-  if (blk < 0) return;
-  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, tok, 1);
-  if (at.seq >= p.num_seqs) return;
-  const int64_t k0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq), k1 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1);
-  const int64_t pos = (k1 - k0) - (at.end - at.begin) + (tok - at.begin);
-  const int64_t from = static_cast<int64_t>(blk) * p.bs;
-  if (from >= k1 - k0 || (p.causal && from > pos)) return;
-  const int64_t row = k0 / p.bs + at.seq + blk;
-  atomicOr(b.bits + (hk * b.rows + row) * b.words + (tok >> 5), 1u << (tok & 31));
 }
 
 // Tokens of each block; one wavefront a block.
@@ -247,16 +277,17 @@ __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
 
 template <int D, int KW>
 struct KvShared {
-  static constexpr int kRowsAt = 32 * (4 / KW < 2 ? 2 : 4 / KW);  // rows staged at a time
+  static constexpr int kSub = KW == 1 ? 1 : 2;           // 32-row tiles of a wavefront at a time
+  static constexpr int kRowsAt = 32 * (4 / KW) * kSub;   // rows staged at a time
   union {
     struct {
-      char q[kRowsAt * 2 * D];
-      char go[kRowsAt * 2 * D];
+      char q[2][kRowsAt * 2 * D];
+      char go[2][kRowsAt * 2 * D];
     };
     float join[4][32][D + 1];
   };
-  float lse2[kRowsAt], delta[kRowsAt];
-  int32_t pos[kRowsAt];
+  float lse2[2][kRowsAt], delta[2][kRowsAt];
+  int32_t pos[2][kRowsAt];
   int32_t list[kPieceRows];
   int32_t wave_count[4];
 };
@@ -264,11 +295,14 @@ struct KvShared {
 // A block's keys: KW wavefronts of 32 keys (of 16 in a block of 16); 4 / KW
 // wavefronts share the keys and take different rows.  The keys and values stay
 // in registers as operands, the rows' queries and output gradients are staged
-// in LDS and read by rows for the scores, transposed for the gradients.
+// in LDS (the next ones wait in registers meanwhile) and read by rows for the
+// scores, transposed for the gradients.  The accumulators leave room for one
+// wavefront a SIMD, so two row tiles are worked on at once: the products of
+// one run beside the exponentials of the other.
 template <typename T, int D, int KW>
 __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b) {
   using Sh = KvShared<D, KW>;
-  constexpr int kRowsAt = Sh::kRowsAt, RW = 4 / KW;
+  constexpr int kRowsAt = Sh::kRowsAt, kSub = Sh::kSub, RW = 4 / KW;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Sh& sh = *reinterpret_cast<Sh*>(smem);
   const Args& p = b.a;
@@ -349,68 +383,91 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
   const float c = p.scale * kLog2e;
-  const int64_t keypos = at.first - at.begin + mykey;  // position of this lane's key
+  const int keypos = static_cast<int>(at.first - at.begin) + mykey;  // position of this lane's key
   const int lastpos = static_cast<int>(at.first - at.begin) + min(keys, key0 + 32) - 1;
   const uint32_t aread = (lane & 31) * (2 * D) + ((half ^ swizzle<D>(lane & 31)) << 4);
   const uint32_t trow = 4 * half + (li >> 2);
   const uint32_t tchunk = dhalf * 2 + ((li & 3) >> 1);
-  const uint32_t qs = lds_offset(sh.q), gs = lds_offset(sh.go);
   const int total = tokens * p.group;
-  constexpr int kChunks = D / 8, kRowsPer = 64 / kChunks;
 
-  for (int r0 = 0; r0 < total; r0 += kRowsAt) {
-    __syncthreads();
-    // stage the rows; those behind the last one repeat it and weigh nothing
+  // rows on their way to LDS: thread t has chunk t % kLanes of the rows
+  // t / kLanes, + kStep, ...  Rows behind the last one repeat it and weigh nothing.
+  constexpr int kLanes = D / 8, kStep = 256 / kLanes, kIn = kRowsAt / kStep;
+  u32x4 qin[kIn], gin[kIn];
+  float lse_in = 0.f, delta_in = 0.f;
+  int pos_in = 0;
+  auto token_of = [&](int r, int& head) {
+    const int t = p.group == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), b.group_magic));
+    head = hk * p.group + r - t * p.group;
+    return static_cast<int64_t>(sh.list[t]);
+  };
+  auto load_rows = [&](int r0) {
 #pragma unroll
-    for (int j = 0; j < kRowsAt / (4 * kRowsPer); ++j) {
-      const int base = (j * 4 + wave) * kRowsPer;
-      const int rr = base + lane / kChunks, chunk = (lane % kChunks) ^ swizzle<D>(rr);
-      const int at_row = min(r0 + rr, total - 1);
-      const int64_t tok = sh.list[at_row / p.group];
-      const int head = hk * p.group + at_row % p.group;
-      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h + chunk * 8) * 2),
-                                       (MI_LDS void*)(sh.q + base * 2 * D), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const MI_GLOBAL void*)(static_cast<const char*>(p.dout) + (tok * p.do_t + head * p.do_h + chunk * 8) * 2),
-                                       (MI_LDS void*)(sh.go + base * 2 * D), 16, 0, 0);
+    for (int j = 0; j < kIn; ++j) {
+      int head;
+      const int64_t tok = token_of(min(r0 + j * kStep + tid / kLanes, total - 1), head);
+      qin[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h + (tid % kLanes) * 8) * 2);
+      gin[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.dout) + (tok * p.do_t + head * p.do_h + (tid % kLanes) * 8) * 2);
     }
     if (tid < kRowsAt) {
-      const int at_row = min(r0 + tid, total - 1);
-      const int64_t tok = sh.list[at_row / p.group];
-      const int64_t i = tok * p.heads + hk * p.group + at_row % p.group;
-      const float l = p.lse[i];
-      sh.lse2[tid] = l == -kInf || r0 + tid >= total ? kInf : l * kLog2e;
-      sh.delta[tid] = b.delta[i];
-      sh.pos[tid] = p.causal ? static_cast<int32_t>(tok + shift) : INT32_MAX;
+      int head;
+      const int64_t tok = token_of(min(r0 + tid, total - 1), head);
+      const float l = p.lse[tok * p.heads + head];
+      lse_in = l == -kInf || r0 + tid >= total ? kInf : l * kLog2e;
+      delta_in = b.delta[tok * p.heads + head];
+      pos_in = p.causal ? static_cast<int32_t>(tok + shift) : INT32_MAX;
     }
-    wait_loads();
+  };
+  if (total > 0) load_rows(0);
+  int buf = 0;
+  for (int r0 = 0; r0 < total; r0 += kRowsAt, buf ^= 1) {
+#pragma unroll
+    for (int j = 0; j < kIn; ++j) {
+      const uint32_t to = tile_at<D>(j * kStep + tid / kLanes, tid % kLanes);
+      *reinterpret_cast<u32x4*>(sh.q[buf] + to) = qin[j];
+      *reinterpret_cast<u32x4*>(sh.go[buf] + to) = gin[j];
+    }
+    if (tid < kRowsAt) {
+      sh.lse2[buf][tid] = lse_in;
+      sh.delta[buf][tid] = delta_in;
+      sh.pos[buf][tid] = pos_in;
+    }
     __syncthreads();
-    for (int sub = rwv; sub < kRowsAt / 32; sub += RW) {
-      if (r0 + sub * 32 >= total) break;
+    if (r0 + kRowsAt < total) load_rows(r0 + kRowsAt);
+    const uint32_t qs = lds_offset(sh.q[buf]), gs = lds_offset(sh.go[buf]);
+    f32x16 s[kSub], dp[kSub];
+    bool masked[kSub];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const int sub = rwv * kSub + u;
       const uint32_t off = sub * 32 * 2 * D;
-      f32x16 s, dp;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
+      for (int r = 0; r < 16; ++r) s[u][r] = dp[u][r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s = T::mfma32(lds_read16(qs + off + (aread ^ (i * 32))), kf[i], s);
+      for (int i = 0; i < D / 16; ++i) s[u] = T::mfma32(lds_read16(qs + off + (aread ^ (i * 32))), kf[i], s[u]);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) dp = T::mfma32(lds_read16(gs + off + (aread ^ (i * 32))), vf[i], dp);
-      const bool masked = __any(sh.pos[sub * 32 + (lane & 31)] < lastpos);
+      for (int i = 0; i < D / 16; ++i) dp[u] = T::mfma32(lds_read16(gs + off + (aread ^ (i * 32))), vf[i], dp[u]);
+      masked[u] = __any(sh.pos[buf][sub * 32 + (lane & 31)] < lastpos);
+    }
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const int sub = rwv * kSub + u;
       u32x4 pw[2], sw[2];
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const int m = sub * 32 + 8 * (r >> 2) + 4 * half;
-        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[m]);
-        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[m]);
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[buf][m]);
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[buf][m]);
         float pr[4], sr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pr[e] = exp2_fast(fmaf(s[r + e], c, -l4[e]));
-          sr[e] = pr[e] * (dp[r + e] - d4[e]);
+          pr[e] = exp2_fast(fmaf(s[u][r + e], c, -l4[e]));
+          sr[e] = pr[e] * (dp[u][r + e] - d4[e]);
         }
-        if (masked) {
+        if (masked[u]) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (sh.pos[m + e] < keypos) pr[e] = sr[e] = 0.f;
+            if (sh.pos[buf][m + e] < keypos) pr[e] = sr[e] = 0.f;
         }
         pw[r >> 3][(r & 7) >> 1] = T::pack(pr[0], pr[1]);
         pw[r >> 3][((r & 7) >> 1) + 1] = T::pack(pr[2], pr[3]);
@@ -418,9 +475,9 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
         sw[r >> 3][((r & 7) >> 1) + 1] = T::pack(sr[2], sr[3]);
       }
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+        for (int i = 0; i < D / 32; ++i) {
           const uint32_t t0 = sub * 32 + 16 * st + trow;
           const uint32_t a0 = tile_at<D>(t0, 4 * i + tchunk) + (li & 1) * 8, a1 = tile_at<D>(t0 + 8, 4 * i + tchunk) + (li & 1) * 8;
           const u32x2 x = lds_read_tr16(gs + a0), y = lds_read_tr16(gs + a1);
@@ -462,7 +519,8 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   }
 }
 
-// Sums the pieces of the blocks that have several: one workgroup a block.
+// Sums the pieces of the blocks that have several, in their order: one workgroup
+// a block and 1024 of its 2 bs D values, eight pieces' loads in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_pieces_kernel(BackArgs b) {
   const Args& p = b.a;
@@ -473,19 +531,15 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(BackArgs b) {
   const Place at = place_of(p.cu_k, p.num_seqs, p.total_k, entry % b.rows, p.bs);
   const int64_t left = at.end - at.first;
   const int keys = static_cast<int>(left < p.bs ? left : p.bs);
-  const int64_t out0 = (at.first * p.kv_heads + hk) * D;
-  for (int e = threadIdx.x; e < 2 * keys * (D / 2); e += 256) {
-    const int side = e / (keys * (D / 2)), f = e % (keys * (D / 2));
-    const int key = f / (D / 2), d = (f % (D / 2)) * 2;
-    float x = 0.f, y = 0.f;
-    for (int i = 0; i < pieces; ++i) {
-      const float* from = b.part + ((static_cast<int64_t>(first + i) * 2 + side) * p.bs + key) * D + d;
-      x += from[0];
-      y += from[1];
-    }
-    char* to = static_cast<char*>(side == 0 ? p.dv : p.dk) + (out0 + static_cast<int64_t>(key) * p.kv_heads * D + d) * 2;
-    *reinterpret_cast<uint32_t*>(to) = T::pack(x, y);
-  }
+  const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+  const int side = e / (p.bs * D), key = e % (p.bs * D) / D, d = e % D;
+  if (key >= keys) return;
+  const float* from = b.part + static_cast<int64_t>(first) * 2 * p.bs * D + e;
+  f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = 0; i < pieces; ++i) x += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(i) * 2 * p.bs * D);
+  char* to = static_cast<char*>(side == 0 ? p.dv : p.dk) + ((at.first + key) * p.kv_heads + hk) * static_cast<int64_t>(2 * D) + d * 2;
+  *reinterpret_cast<u32x2*>(to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
 }
 
 // Sizes of the workspace's parts, 256-byte aligned.
@@ -500,6 +554,7 @@ Layout lay_out(BackArgs& b, int dim) {
   b.rows = slots_of(p.total_k, p.num_seqs, p.bs);
   b.words = (p.total_q + 31) / 32;
   b.piece = kPieceRows / p.group;
+  b.group_magic = static_cast<uint32_t>(((uint64_t{1} << 32) + p.group - 1) / p.group);
   const uint64_t entries = static_cast<uint64_t>(p.kv_heads) * b.rows;
   const uint64_t pairs = static_cast<uint64_t>(p.total_q) * p.select * p.kv_heads;
   const uint64_t pieces = entries + pairs / b.piece;
@@ -531,7 +586,6 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   if (words > 0)
     clear_bits_kernel<<<dim3(static_cast<unsigned>(words / 1024 + 1 < 4096 ? words / 1024 + 1 : 4096)), dim3(256), 0, stream>>>(b);
   if (pairs > 0) {
-    mark_bits_kernel<<<dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, stream>>>(b);
     block_attention_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
   }
   if (p.total_k == 0) return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
@@ -540,7 +594,7 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   const int st = p.bs == 128 ? launch_dkv<T, D, 4>(b, stream) : (p.bs == 64 ? launch_dkv<T, D, 2>(b, stream) : launch_dkv<T, D, 1>(b, stream));
   if (st != MI_ATTN_OK) return st;
-  join_pieces_kernel<T, D><<<dim3(static_cast<unsigned>(entries)), dim3(256), 0, stream>>>(b);
+  join_pieces_kernel<T, D><<<dim3(static_cast<unsigned>(entries), 2 * p.bs * D / 1024), dim3(256), 0, stream>>>(b);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
