@@ -56,6 +56,9 @@ extern "C" {
 /* Largest number of selected blocks per query and key head. */
 #define MI_ATTN_MAX_SELECT 1024
 
+/* Token strides of k and v in attention are below this many elements. */
+#define MI_ATTN_MAX_STRIDE (1 << 23)
+
 /*
  * Mean of the keys of each block, fp32 [rows, HK, D] with
  * rows = total_k / block_size + num_seqs: block b of sequence i is row
@@ -115,7 +118,8 @@ int block_scores(const mi_block_scores_args* args, hipStream_t stream);
  * Attention over the selected blocks (the operation above) and its gradient.
  *
  *   q, k, v, dout  of `dtype`, unit stride along D, strides in elements
- *                  (multiples of 8), 16-byte aligned; D 64 or 128; H a multiple
+ *                  (multiples of 8; token strides of k and v below
+ *                  MI_ATTN_MAX_STRIDE), 16-byte aligned; D 64 or 128; H a multiple
  *                  of HK with H / HK <= 128.
  *   blocks         int32 [total_q, HK, select], contiguous, 1 <= select <=
  *                  MI_ATTN_MAX_SELECT.

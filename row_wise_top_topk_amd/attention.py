@@ -289,6 +289,8 @@ def _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
     total_k, hk = int(k.shape[0]), int(k.shape[1])
+    if total_k > 1 and max(k.stride(0), v.stride(0)) >= 1 << 23:
+        raise ValueError("k and v must have token strides below 2^23 elements")
     _groups(heads, hk)
     if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or not 1 <= blocks.shape[2] <= MAX_SELECT:
         raise ValueError(f"blocks must be an int32 tensor [tokens, kv_heads, selected], selected in [1, {MAX_SELECT}]")

@@ -68,11 +68,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const uint32_t kread = (lane & 31) * (2 * D) + ((half ^ swizzle<D>(lane & 31)) << 4);
-  // transposing read of V: row 4 half + (li >> 2), elements 16 dhalf + 4 (li & 3)
-  const int li = lane & 15, dhalf = (lane >> 4) & 1;
-  const uint32_t vrow = 4 * half + (li >> 2);
-  const uint32_t vchunk = dhalf * 2 + ((li & 3) >> 1);
+  const Reads<D> rd;
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
@@ -102,7 +98,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) ka[mt][i] = lds_read16(ks + mt * 32 * 2 * D + (kread ^ (i * 32)));
+          for (int i = 0; i < D / 16; ++i) ka[mt][i] = rd.row(ks, mt * 32, i);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
@@ -119,7 +115,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
         }
         __builtin_amdgcn_sched_group_barrier(0x008, D / 16, 0);
       }
-      if (!see.full) {
+      if (see.partial) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -128,11 +124,15 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
             if (off + 4 * half > see.last[mt * 2 + (r >> 3)]) s[mt][r] = -kInf;
           }
       }
-      float top = s[0][0];
+      // a row sees all of a 16-key group, nothing of it, or what was just masked
+      float top = -kInf;
 #pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, s[0][r]);
+      for (int i = 0; i < 4; ++i) {
+        float t = s[i >> 1][8 * (i & 1)];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[1][r]);
+        for (int r = 1; r < 8; ++r) t = fmaxf(t, s[i >> 1][8 * (i & 1) + r]);
+        top = fmaxf(top, see.last[i] >= 0 ? t : -kInf);
+      }
       top = half_max(top);
       // The weights stay relative to an older maximum until it is passed by
       // 2^8: their sums are divided out at the end, and a weight keeps its bits.
@@ -148,25 +148,24 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
       }
       const float base = m == -kInf ? 0.f : m * c;
       u32x4 pr[4];
+      float sums[4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int i = 0; i < 4; ++i) {
+        const float from = see.last[i] >= 0 ? base : kInf;
+        float w[8];
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          const float x = exp2_fast(fmaf(s[mt][r], c, -base)), y = exp2_fast(fmaf(s[mt][r + 1], c, -base));
-          sum += x + y;
-          pr[mt * 2 + (r >> 3)][(r & 7) >> 1] = T::pack(x, y);
-        }
+        for (int r = 0; r < 8; ++r) w[r] = exp2_fast(fmaf(s[i >> 1][8 * (i & 1) + r], c, -from));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pr[i][r] = T::pack(w[2 * r], w[2 * r + 1]);
+        sums[i] = ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+      }
+      sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
       {
         u32x4 va[D / 32][4];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            const uint32_t r0 = 16 * st + vrow;
-            const u32x2 x = lds_read_tr16(vs + tile_at<D>(r0, 4 * i + vchunk) + (li & 1) * 8);
-            const u32x2 y = lds_read_tr16(vs + tile_at<D>(r0 + 8, 4 * i + vchunk) + (li & 1) * 8);
-            va[i][st] = u32x4{x[0], x[1], y[0], y[1]};
-          }
+          for (int st = 0; st < 4; ++st) va[i][st] = rd.column(vs, 16 * st, i);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -221,6 +220,7 @@ int make_args(const mi_block_attention_args* a, Args& p) {
   const int64_t strides[] = {a->q_stride_t, a->q_stride_h, a->k_stride_t, a->k_stride_h, a->v_stride_t, a->v_stride_h};
   for (int64_t s : strides)
     if (s < 0 || (s & 7)) return MI_ATTN_EINVAL;
+  if (a->k_stride_t >= MI_ATTN_MAX_STRIDE || a->v_stride_t >= MI_ATTN_MAX_STRIDE) return MI_ATTN_EINVAL;
   const bool some_q = a->total_q > 0, some_k = a->total_k > 0;
   if (some_q && (a->q == nullptr || a->blocks == nullptr || a->out == nullptr || a->lse == nullptr)) return MI_ATTN_EINVAL;
   if (some_k && (a->k == nullptr || a->v == nullptr)) return MI_ATTN_EINVAL;

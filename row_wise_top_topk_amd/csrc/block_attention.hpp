@@ -162,17 +162,20 @@ struct Half {
   static constexpr int kSteps = kTile / kRowsAt;
   u32x4 x[kSteps];
 
+  // base + key * stride of a 16-key group is uniform; a thread adds its row and
+  // chunk in 32 bits.  Rows behind the sequence's last key repeat it.
   __device__ __forceinline__ void load(const char* base, int64_t stride_bytes, const Keys& k, int len_k) {
     const int tid = threadIdx.x;
-    const char* from = base + (tid % kLanes) * 16;
+    const uint32_t chunk = (tid % kLanes) * 16;
+    const int row = (tid / kLanes) & 15;
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
       int key;
       if constexpr (kRowsAt == 16) key = k.key[j];
-      else key = tid < 128 ? k.key[2 * j] : k.key[2 * j + 1];
-      key += (tid / kLanes) & 15;
-      key = max(0, min(key, len_k - 1));
-      x[j] = *reinterpret_cast<const u32x4*>(from + static_cast<uint64_t>(static_cast<uint32_t>(key)) * static_cast<uint64_t>(stride_bytes));
+      else key = __builtin_amdgcn_readfirstlane(tid) < 128 ? k.key[2 * j] : k.key[2 * j + 1];
+      key = max(0, min(key, len_k - 1));  // a group may lie behind the last key of its block
+      const char* from = base + key * stride_bytes;
+      x[j] = *reinterpret_cast<const u32x4*>(from + (__umul24(min(row, len_k - 1 - key), static_cast<uint32_t>(stride_bytes)) + chunk));
     }
   }
   __device__ __forceinline__ void store(char* tile) const {
@@ -186,16 +189,16 @@ struct Half {
 };
 
 // What a lane's row may see of a tile: for each 16-key group the last visible
-// offset (relative to the group's first key), -1 for none.
+// offset (relative to the group's first key), negative for none.
 struct Sight {
   int32_t last[4];
-  bool any;   // some row of the wavefront sees something
-  bool full;  // every valid row sees all 64 keys
+  bool any;      // some row of the wavefront sees something
+  bool partial;  // some row sees a part of a group only
 };
 
 __device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw, int word, int bit, int limit, bool valid) {
   Sight v;
-  bool some = false, all = true;
+  bool some = false, part = false;
   uint32_t bits[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) bits[i] = s.mask[k.id[i] * nw + word];
@@ -203,11 +206,34 @@ __device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw
   for (int i = 0; i < 4; ++i) {
     v.last[i] = k.key[i] >= 0 && ((bits[i] >> bit) & 1u) ? limit - k.key[i] : -1;
     some |= v.last[i] >= 0;
-    all &= v.last[i] >= 15;
+    part |= v.last[i] >= 0 && v.last[i] < 15;
   }
   v.any = __any(valid && some);
-  v.full = __all(!valid || all);
+  v.partial = __any(valid && part);
   return v;
 }
+
+// Where a lane reads a tile in LDS.  By rows: row lane & 31 of 32, 8 elements
+// from 16 i + 8 (lane >> 5) on.  Transposed: rows 4 (lane >> 5) .. + 3 (x) and
+// those 8 behind them (y) of 16, column 32 i + (lane & 31); the rows are the
+// order in which the scores of 32 keys lie in a lane's registers.
+template <int D>
+struct Reads {
+  uint32_t by_row, x, y;
+  __device__ __forceinline__ Reads() {
+    const uint32_t lane = threadIdx.x & 63, half = lane >> 5, li = lane & 15, dhalf = (lane >> 4) & 1;
+    by_row = tile_at<D>(lane & 31, half);
+    const uint32_t row = 4 * half + (li >> 2), chunk = dhalf * 2 + ((li & 3) >> 1);
+    x = tile_at<D>(row, chunk) + (li & 1) * 8;
+    y = tile_at<D>(row + 8, chunk) + (li & 1) * 8;
+  }
+  // operand i of the 32 rows from `rows` on (a multiple of 32)
+  __device__ __forceinline__ u32x4 row(uint32_t tile, int rows, int i) const { return lds_read16((tile + (by_row ^ (i * 32))) + rows * (2 * D)); }
+  // operand of the 16 rows from `rows` on (a multiple of 16), columns 32 i ..
+  __device__ __forceinline__ u32x4 column(uint32_t tile, int rows, int i) const {
+    const u32x2 a = lds_read_tr16((tile + (x ^ (i * 64))) + rows * (2 * D)), b = lds_read_tr16((tile + (y ^ (i * 64))) + rows * (2 * D));
+    return u32x4{a[0], a[1], b[0], b[1]};
+  }
+};
 
 }  // namespace miattn

@@ -119,10 +119,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   const float c = p.scale * kLog2e;
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const uint32_t kread = (lane & 31) * (2 * D) + ((half ^ swizzle<D>(lane & 31)) << 4);
-  const int li = lane & 15, dhalf = (lane >> 4) & 1;
-  const uint32_t trow = 4 * half + (li >> 2);
-  const uint32_t tchunk = dhalf * 2 + ((li & 3) >> 1);
+  const Reads<D> rd;
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
@@ -149,14 +146,14 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
       const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
 #pragma unroll 1
       for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t off = mt * 32 * 2 * D;
+        const uint32_t kt = ks + mt * 32 * 2 * D, vt = vs + mt * 32 * 2 * D;
         f32x16 s, dp;
         {
           u32x4 ka[D / 16], va[D / 16];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) ka[i] = lds_read16(ks + off + (kread ^ (i * 32)));
+          for (int i = 0; i < D / 16; ++i) ka[i] = rd.row(kt, 0, i);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) va[i] = lds_read16(vs + off + (kread ^ (i * 32)));
+          for (int i = 0; i < D / 16; ++i) va[i] = rd.row(vt, 0, i);
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
 #pragma unroll
@@ -173,29 +170,29 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
           __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
         }
         u32x4 ds[2];
-        const int last0 = mt == 0 ? see.last[0] : see.last[2], last1 = mt == 0 ? see.last[1] : see.last[3];
+        const int last[2] = {mt == 0 ? see.last[0] : see.last[2], mt == 0 ? see.last[1] : see.last[3]};
+        if (see.partial) {
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) {
-          float w[2];
+          for (int r = 0; r < 16; ++r)
+            if (8 * ((r >> 2) & 1) + (r & 3) + 4 * half > last[r >> 3]) s[r] = -kInf;
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = 8 * (((r + e) >> 2) & 1) + ((r + e) & 3);
-            w[e] = exp2_fast(fmaf(s[r + e], c, -lse2)) * (dp[r + e] - delta);
-            if (!see.full && at + 4 * half > (r < 8 ? last0 : last1)) w[e] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          const float from = last[i] >= 0 ? lse2 : kInf;
+#pragma unroll
+          for (int r = 0; r < 8; r += 2) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w[e] = exp2_fast(fmaf(s[8 * i + r + e], c, -from)) * (dp[8 * i + r + e] - delta);
+            ds[i][r >> 1] = T::pack(w[0], w[1]);
           }
-          ds[r >> 3][(r & 7) >> 1] = T::pack(w[0], w[1]);
         }
         {
           u32x4 ka[D / 32][2];
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              const uint32_t r0 = 16 * st + trow;
-              const u32x2 x = lds_read_tr16(ks + off + tile_at<D>(r0, 4 * i + tchunk) + (li & 1) * 8);
-              const u32x2 y = lds_read_tr16(ks + off + tile_at<D>(r0 + 8, 4 * i + tchunk) + (li & 1) * 8);
-              ka[i][st] = u32x4{x[0], x[1], y[0], y[1]};
-            }
+            for (int st = 0; st < 2; ++st) ka[i][st] = rd.column(kt, 16 * st, i);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -292,6 +289,80 @@ struct KvShared {
   int32_t wave_count[4];
 };
 
+// Adds the rows first .. first + 32 kSub - 1 of a stage to a wavefront's dk and
+// dv: lane l holds key l & 31 of its 32 and half of the rows.  Masked: rows may
+// stand before keys.
+template <typename T, int D, int kSub, bool kMasked>
+__device__ __forceinline__ void dkv_rows(const u32x4 (&kf)[D / 16], const u32x4 (&vf)[D / 16], uint32_t qs, uint32_t gs, uint32_t first,
+                                         const Reads<D>& rd, const float* lse2, const float* delta, const int32_t* pos, int keypos,
+                                         float c, f32x16 (&dk)[D / 32], f32x16 (&dv)[D / 32]) {
+  const int half = (threadIdx.x & 63) >> 5;
+  qs += first * 2 * D;
+  gs += first * 2 * D;
+  f32x16 s[kSub], dp[kSub];
+  u32x4 pw[kSub][2], sw[kSub][2];
+#pragma unroll
+  for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[u][r] = dp[u][r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s[u] = T::mfma32(rd.row(qs, u * 32, i), kf[i], s[u]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) dp[u] = T::mfma32(rd.row(gs, u * 32, i), vf[i], dp[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const int m = first + u * 32 + 8 * (r >> 2) + 4 * half;
+      const f32x4 l4 = *reinterpret_cast<const f32x4*>(lse2 + m);
+      const f32x4 d4 = *reinterpret_cast<const f32x4*>(delta + m);
+      float pr[4], sr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pr[e] = exp2_fast(fmaf(s[u][r + e], c, -l4[e]));
+        if (kMasked && pos[m + e] < keypos) pr[e] = 0.f;
+        sr[e] = pr[e] * (dp[u][r + e] - d4[e]);
+      }
+      pw[u][r >> 3][(r & 7) >> 1] = T::pack(pr[0], pr[1]);
+      pw[u][r >> 3][((r & 7) >> 1) + 1] = T::pack(pr[2], pr[3]);
+      sw[u][r >> 3][(r & 7) >> 1] = T::pack(sr[0], sr[1]);
+      sw[u][r >> 3][((r & 7) >> 1) + 1] = T::pack(sr[2], sr[3]);
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        dv[i] = T::mfma32(pw[u][st], rd.column(gs, u * 32 + 16 * st, i), dv[i]);
+        dk[i] = T::mfma32(sw[u][st], rd.column(qs, u * 32 + 16 * st, i), dk[i]);
+      }
+  }
+  if constexpr (!kMasked) {
+    // reads ahead of the products; the exponentials of one tile beside the
+    // products of the other
+    constexpr int kProducts = D / 8;  // scores and their gradients of a tile; dv and dk likewise
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int n = 0; n < kSub * kProducts - 6; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (n >= kProducts) __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+    for (int n = 0; n < 6; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < kSub * kProducts; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (n < kProducts) __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+  }
+}
+
 // A block's keys: KW wavefronts of 32 keys (of 16 in a block of 16); 4 / KW
 // wavefronts share the keys and take different rows.  The keys and values stay
 // in registers as operands, the rows' queries and output gradients are staged
@@ -307,7 +378,7 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   Sh& sh = *reinterpret_cast<Sh*>(smem);
   const Args& p = b.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5, li = lane & 15, dhalf = (lane >> 4) & 1;
+  const int half = lane >> 5;
   const int64_t entries = p.kv_heads * b.rows;
   const int piece = blockIdx.x;
   if (piece >= b.first[entries]) return;
@@ -385,9 +456,7 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   const float c = p.scale * kLog2e;
   const int keypos = static_cast<int>(at.first - at.begin) + mykey;  // position of this lane's key
   const int lastpos = static_cast<int>(at.first - at.begin) + min(keys, key0 + 32) - 1;
-  const uint32_t aread = (lane & 31) * (2 * D) + ((half ^ swizzle<D>(lane & 31)) << 4);
-  const uint32_t trow = 4 * half + (li >> 2);
-  const uint32_t tchunk = dhalf * 2 + ((li & 3) >> 1);
+  const Reads<D> rd;
   const int total = tokens * p.group;
 
   // rows on their way to LDS: thread t has chunk t % kLanes of the rows
@@ -435,57 +504,12 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
     __syncthreads();
     if (r0 + kRowsAt < total) load_rows(r0 + kRowsAt);
     const uint32_t qs = lds_offset(sh.q[buf]), gs = lds_offset(sh.go[buf]);
-    f32x16 s[kSub], dp[kSub];
-    bool masked[kSub];
+    const uint32_t first = rwv * kSub * 32;  // this wavefront's rows
+    bool some = false;
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      const int sub = rwv * kSub + u;
-      const uint32_t off = sub * 32 * 2 * D;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[u][r] = dp[u][r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) s[u] = T::mfma32(lds_read16(qs + off + (aread ^ (i * 32))), kf[i], s[u]);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) dp[u] = T::mfma32(lds_read16(gs + off + (aread ^ (i * 32))), vf[i], dp[u]);
-      masked[u] = __any(sh.pos[buf][sub * 32 + (lane & 31)] < lastpos);
-    }
-#pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      const int sub = rwv * kSub + u;
-      u32x4 pw[2], sw[2];
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const int m = sub * 32 + 8 * (r >> 2) + 4 * half;
-        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[buf][m]);
-        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[buf][m]);
-        float pr[4], sr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = exp2_fast(fmaf(s[u][r + e], c, -l4[e]));
-          sr[e] = pr[e] * (dp[u][r + e] - d4[e]);
-        }
-        if (masked[u]) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (sh.pos[buf][m + e] < keypos) pr[e] = sr[e] = 0.f;
-        }
-        pw[r >> 3][(r & 7) >> 1] = T::pack(pr[0], pr[1]);
-        pw[r >> 3][((r & 7) >> 1) + 1] = T::pack(pr[2], pr[3]);
-        sw[r >> 3][(r & 7) >> 1] = T::pack(sr[0], sr[1]);
-        sw[r >> 3][((r & 7) >> 1) + 1] = T::pack(sr[2], sr[3]);
-      }
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t t0 = sub * 32 + 16 * st + trow;
-          const uint32_t a0 = tile_at<D>(t0, 4 * i + tchunk) + (li & 1) * 8, a1 = tile_at<D>(t0 + 8, 4 * i + tchunk) + (li & 1) * 8;
-          const u32x2 x = lds_read_tr16(gs + a0), y = lds_read_tr16(gs + a1);
-          dv[i] = T::mfma32(pw[st], u32x4{x[0], x[1], y[0], y[1]}, dv[i]);
-          const u32x2 z = lds_read_tr16(qs + a0), w = lds_read_tr16(qs + a1);
-          dk[i] = T::mfma32(sw[st], u32x4{z[0], z[1], w[0], w[1]}, dk[i]);
-        }
-    }
+    for (int u = 0; u < kSub; ++u) some |= sh.pos[buf][first + u * 32 + (lane & 31)] < lastpos;
+    if (__any(some)) dkv_rows<T, D, kSub, true>(kf, vf, qs, gs, first, rd, sh.lse2[buf], sh.delta[buf], sh.pos[buf], keypos, c, dk, dv);
+    else dkv_rows<T, D, kSub, false>(kf, vf, qs, gs, first, rd, sh.lse2[buf], sh.delta[buf], sh.pos[buf], keypos, c, dk, dv);
   }
 
   // Join the wavefronts that share keys, values first, then keys.
