@@ -151,4 +151,41 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (those of one
+// column of a 16x16 result): each gets it.
+__device__ __forceinline__ float quad_max(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Where a lane reads a tile in LDS for 16x16x32 products.  By rows: row lane & 15
+// of 16, 8 elements from 32 i + 8 (lane >> 4) on.  Transposed: of 32 rows, rows
+// 4 (lane >> 4) .. + 3 and those 16 behind them, column 16 i + (lane & 15); that
+// is the order in which two results of 16 rows lie in a lane's registers.
+template <int D>
+struct Reads16 {
+  uint32_t by_row, by_column;
+  __device__ __forceinline__ Reads16() {
+    const uint32_t lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+    by_row = tile_at<D>(li, g);
+    by_column = tile_at<D>(4 * g + (li >> 2), (li & 3) >> 1) + (li & 1) * 8;
+  }
+  // operand i of the 16 rows from `rows` on (a multiple of 16)
+  __device__ __forceinline__ u32x4 row(uint32_t tile, int rows, int i) const { return lds_read16((tile + (by_row ^ (i * 64))) + rows * (2 * D)); }
+  // operand of the 32 rows from `rows` on (a multiple of 16), columns 16 i ..
+  __device__ __forceinline__ u32x4 column(uint32_t tile, int rows, int i) const {
+    const uint32_t at = tile + (by_column ^ (i * 32));
+    const u32x2 a = lds_read_tr16(at + rows * (2 * D)), b = lds_read_tr16(at + (rows + 16) * (2 * D));
+    return u32x4{a[0], a[1], b[0], b[1]};
+  }
+};
+
 }  // namespace miattn

@@ -188,6 +188,20 @@ struct Half {
   }
 };
 
+// Tells the scheduler to keep `ahead` products' operand reads (`reads`
+// instructions each) before the product that uses them, for `products` in a row.
+template <int products, int ahead, int reads>
+__device__ __forceinline__ void read_ahead() {
+  constexpr int first = ahead < products ? ahead : products;
+  __builtin_amdgcn_sched_group_barrier(0x100, first * reads, 0);
+#pragma unroll
+  for (int i = 0; i < products - first; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, first, 0);
+}
+
 // What a lane's row may see of a tile: for each 16-key group the last visible
 // offset (relative to the group's first key), negative for none.
 struct Sight {

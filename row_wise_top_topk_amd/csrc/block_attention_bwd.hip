@@ -272,16 +272,17 @@ __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
 
 // ---- dk, dv ----
 
+constexpr int kStage = 32;  // rows of a stage for each group of wavefronts that shares them
+
 template <int D, int KW>
 struct KvShared {
-  static constexpr int kSub = KW == 1 ? 1 : 2;           // 32-row tiles of a wavefront at a time
-  static constexpr int kRowsAt = 32 * (4 / KW) * kSub;   // rows staged at a time
+  static constexpr int kRowsAt = kStage * (4 / KW);  // rows staged at a time
   union {
     struct {
       char q[2][kRowsAt * 2 * D];
       char go[2][kRowsAt * 2 * D];
     };
-    float join[4][32][D + 1];
+    float join[4][16][D + 4];
   };
   float lse2[2][kRowsAt], delta[2][kRowsAt];
   int32_t pos[2][kRowsAt];
@@ -289,98 +290,26 @@ struct KvShared {
   int32_t wave_count[4];
 };
 
-// Adds the rows first .. first + 32 kSub - 1 of a stage to a wavefront's dk and
-// dv: lane l holds key l & 31 of its 32 and half of the rows.  Masked: rows may
-// stand before keys.
-template <typename T, int D, int kSub, bool kMasked>
-__device__ __forceinline__ void dkv_rows(const u32x4 (&kf)[D / 16], const u32x4 (&vf)[D / 16], uint32_t qs, uint32_t gs, uint32_t first,
-                                         const Reads<D>& rd, const float* lse2, const float* delta, const int32_t* pos, int keypos,
-                                         float c, f32x16 (&dk)[D / 32], f32x16 (&dv)[D / 32]) {
-  const int half = (threadIdx.x & 63) >> 5;
-  qs += first * 2 * D;
-  gs += first * 2 * D;
-  f32x16 s[kSub], dp[kSub];
-  u32x4 pw[kSub][2], sw[kSub][2];
-#pragma unroll
-  for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) s[u][r] = dp[u][r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) s[u] = T::mfma32(rd.row(qs, u * 32, i), kf[i], s[u]);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) dp[u] = T::mfma32(rd.row(gs, u * 32, i), vf[i], dp[u]);
-  }
-#pragma unroll
-  for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const int m = first + u * 32 + 8 * (r >> 2) + 4 * half;
-      const f32x4 l4 = *reinterpret_cast<const f32x4*>(lse2 + m);
-      const f32x4 d4 = *reinterpret_cast<const f32x4*>(delta + m);
-      float pr[4], sr[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        pr[e] = exp2_fast(fmaf(s[u][r + e], c, -l4[e]));
-        if (kMasked && pos[m + e] < keypos) pr[e] = 0.f;
-        sr[e] = pr[e] * (dp[u][r + e] - d4[e]);
-      }
-      pw[u][r >> 3][(r & 7) >> 1] = T::pack(pr[0], pr[1]);
-      pw[u][r >> 3][((r & 7) >> 1) + 1] = T::pack(pr[2], pr[3]);
-      sw[u][r >> 3][(r & 7) >> 1] = T::pack(sr[0], sr[1]);
-      sw[u][r >> 3][((r & 7) >> 1) + 1] = T::pack(sr[2], sr[3]);
-    }
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        dv[i] = T::mfma32(pw[u][st], rd.column(gs, u * 32 + 16 * st, i), dv[i]);
-        dk[i] = T::mfma32(sw[u][st], rd.column(qs, u * 32 + 16 * st, i), dk[i]);
-      }
-  }
-  if constexpr (!kMasked) {
-    // reads ahead of the products; the exponentials of one tile beside the
-    // products of the other
-    constexpr int kProducts = D / 8;  // scores and their gradients of a tile; dv and dk likewise
-    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-#pragma unroll
-    for (int n = 0; n < kSub * kProducts - 6; ++n) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (n >= kProducts) __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
-#pragma unroll
-    for (int n = 0; n < 6; ++n) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-    }
-#pragma unroll
-    for (int n = 0; n < kSub * kProducts; ++n) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      if (n < kProducts) __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    }
-  }
-}
-
-// A block's keys: KW wavefronts of 32 keys (of 16 in a block of 16); 4 / KW
-// wavefronts share the keys and take different rows.  The keys and values stay
-// in registers as operands, the rows' queries and output gradients are staged
-// in LDS (the next ones wait in registers meanwhile) and read by rows for the
-// scores, transposed for the gradients.  The accumulators leave room for one
-// wavefront a SIMD, so two row tiles are worked on at once: the products of
-// one run beside the exponentials of the other.
+// KW wavefronts of 16 keys; 4 / KW of them share the keys and take different
+// rows; a block of 128 keys is two workgroups'.  The keys and values stay in
+// registers as operands, the rows' queries and output gradients are staged in
+// LDS (the next ones wait in registers meanwhile) and read by rows for the
+// scores, transposed for the gradients.  16 keys rather than 32 a wavefront:
+// with 32 the accumulators leave one wavefront a SIMD, and its waits show
+// (measured on 8192 tokens, 32/2 heads, 16 blocks of 64: 690 us).
 template <typename T, int D, int KW>
-__global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b) {
+__global__ void __launch_bounds__(256, 3) block_attention_dkv_kernel(BackArgs b) {
   using Sh = KvShared<D, KW>;
-  constexpr int kRowsAt = Sh::kRowsAt, kSub = Sh::kSub, RW = 4 / KW;
+  constexpr int kRowsAt = Sh::kRowsAt, RW = 4 / KW;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Sh& sh = *reinterpret_cast<Sh*>(smem);
   const Args& p = b.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5;
+  const int quad = lane >> 4;
   const int64_t entries = p.kv_heads * b.rows;
-  const int piece = blockIdx.x;
+  const int parts = p.bs > 64 ? 2 : 1;  // workgroups of a piece
+  const int piece = blockIdx.x / parts;
+  const int key_first = (blockIdx.x % parts) * 64;  // this workgroup's first key within the block
   if (piece >= b.first[entries]) return;
   int64_t lo = 0, hi = entries - 1;  // the last entry whose first piece is not behind this one
   while (lo < hi) {
@@ -393,7 +322,7 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   const Place at = place_of(p.cu_k, p.num_seqs, p.total_k, row, p.bs);
   const int64_t left = at.end - at.first;
   const int keys = static_cast<int>(left < 0 ? 0 : (left < p.bs ? left : p.bs));
-  if (keys == 0) return;
+  if (keys <= key_first) return;
   const int pieces = b.first[entry + 1] - b.first[entry];
   const int part = piece - b.first[entry];
   const int count = b.counts[entry];
@@ -435,28 +364,26 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   }
 
   const int kw = wave % KW, rwv = wave / KW;
-  const int key0 = kw * 32;  // first key of this wavefront within the block
-  const int mykey = key0 + (lane & 31);
+  const int key0 = key_first + kw * 16;  // first key of this wavefront within the block
+  const int mykey = key0 + (lane & 15);
   const bool haskey = mykey < keys;
-  u32x4 kf[D / 16], vf[D / 16];
+  u32x4 kf[D / 32], vf[D / 32];
   {
-    const char* kfrom = static_cast<const char*>(p.k) + ((at.first + (haskey ? mykey : 0)) * p.k_t + hk * p.k_h) * 2 + half * 16;
-    const char* vfrom = static_cast<const char*>(p.v) + ((at.first + (haskey ? mykey : 0)) * p.v_t + hk * p.v_h) * 2 + half * 16;
+    const char* kfrom = static_cast<const char*>(p.k) + ((at.first + (haskey ? mykey : 0)) * p.k_t + hk * p.k_h) * 2 + quad * 16;
+    const char* vfrom = static_cast<const char*>(p.v) + ((at.first + (haskey ? mykey : 0)) * p.v_t + hk * p.v_h) * 2 + quad * 16;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      kf[i] = haskey ? *reinterpret_cast<const u32x4*>(kfrom + i * 32) : u32x4{0, 0, 0, 0};
-      vf[i] = haskey ? *reinterpret_cast<const u32x4*>(vfrom + i * 32) : u32x4{0, 0, 0, 0};
+    for (int i = 0; i < D / 32; ++i) {
+      kf[i] = haskey ? *reinterpret_cast<const u32x4*>(kfrom + i * 64) : u32x4{0, 0, 0, 0};
+      vf[i] = haskey ? *reinterpret_cast<const u32x4*>(vfrom + i * 64) : u32x4{0, 0, 0, 0};
     }
   }
-  f32x16 dk[D / 32], dv[D / 32];
+  f32x4 dk[D / 16], dv[D / 16];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) dk[i][r] = dv[i][r] = 0.f;
+  for (int i = 0; i < D / 16; ++i) dk[i] = dv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float c = p.scale * kLog2e;
   const int keypos = static_cast<int>(at.first - at.begin) + mykey;  // position of this lane's key
-  const int lastpos = static_cast<int>(at.first - at.begin) + min(keys, key0 + 32) - 1;
-  const Reads<D> rd;
+  const int lastpos = static_cast<int>(at.first - at.begin) + min(keys, key0 + 16) - 1;
+  const Reads16<D> rd;
   const int total = tokens * p.group;
 
   // rows on their way to LDS: thread t has chunk t % kLanes of the rows
@@ -468,22 +395,27 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
   auto token_of = [&](int r, int& head) {
     const int t = p.group == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), b.group_magic));
     head = hk * p.group + r - t * p.group;
-    return static_cast<int64_t>(sh.list[t]);
+    return static_cast<uint32_t>(sh.list[t]);
   };
+  const char* qbase = static_cast<const char*>(p.q) + (tid % kLanes) * 16;
+  const char* gbase = static_cast<const char*>(p.dout) + (tid % kLanes) * 16;
+  const uint64_t qt = p.q_t * 2, gt = p.do_t * 2;
+  const uint32_t qh = static_cast<uint32_t>(p.q_h * 2), gh = static_cast<uint32_t>(p.do_h * 2);
   auto load_rows = [&](int r0) {
 #pragma unroll
     for (int j = 0; j < kIn; ++j) {
       int head;
-      const int64_t tok = token_of(min(r0 + j * kStep + tid / kLanes, total - 1), head);
-      qin[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h + (tid % kLanes) * 8) * 2);
-      gin[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.dout) + (tok * p.do_t + head * p.do_h + (tid % kLanes) * 8) * 2);
+      const uint32_t tok = token_of(min(r0 + j * kStep + tid / kLanes, total - 1), head);
+      qin[j] = *reinterpret_cast<const u32x4*>(qbase + (tok * qt + static_cast<uint64_t>(static_cast<uint32_t>(head)) * qh));
+      gin[j] = *reinterpret_cast<const u32x4*>(gbase + (tok * gt + static_cast<uint64_t>(static_cast<uint32_t>(head)) * gh));
     }
     if (tid < kRowsAt) {
       int head;
-      const int64_t tok = token_of(min(r0 + tid, total - 1), head);
-      const float l = p.lse[tok * p.heads + head];
+      const uint32_t tok = token_of(min(r0 + tid, total - 1), head);
+      const int64_t at_row = static_cast<int64_t>(tok) * p.heads + head;
+      const float l = p.lse[at_row];
       lse_in = l == -kInf || r0 + tid >= total ? kInf : l * kLog2e;
-      delta_in = b.delta[tok * p.heads + head];
+      delta_in = b.delta[at_row];
       pos_in = p.causal ? static_cast<int32_t>(tok + shift) : INT32_MAX;
     }
   };
@@ -504,40 +436,69 @@ __global__ void __launch_bounds__(256, 1) block_attention_dkv_kernel(BackArgs b)
     __syncthreads();
     if (r0 + kRowsAt < total) load_rows(r0 + kRowsAt);
     const uint32_t qs = lds_offset(sh.q[buf]), gs = lds_offset(sh.go[buf]);
-    const uint32_t first = rwv * kSub * 32;  // this wavefront's rows
-    bool some = false;
+    const int first = rwv * kStage;  // this wavefront's rows
+    const bool masked = __any(sh.pos[buf][first + (lane & 31)] < lastpos);
+    f32x4 s[2], dp[2];
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) some |= sh.pos[buf][first + u * 32 + (lane & 31)] < lastpos;
-    if (__any(some)) dkv_rows<T, D, kSub, true>(kf, vf, qs, gs, first, rd, sh.lse2[buf], sh.delta[buf], sh.pos[buf], keypos, c, dk, dv);
-    else dkv_rows<T, D, kSub, false>(kf, vf, qs, gs, first, rd, sh.lse2[buf], sh.delta[buf], sh.pos[buf], keypos, c, dk, dv);
+    for (int t = 0; t < 2; ++t) {
+      s[t] = dp[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) s[t] = T::mfma16(rd.row(qs, first + 16 * t, i), kf[i], s[t]);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) dp[t] = T::mfma16(rd.row(gs, first + 16 * t, i), vf[i], dp[t]);
+    }
+    read_ahead<D / 8, 6, 1>();
+    u32x4 pw, sw;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r0 = first + 16 * t + 4 * quad;
+      const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[buf][r0]);
+      const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[buf][r0]);
+      float pr[4], sr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(fmaf(s[t][e], c, -l4[e]));
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (sh.pos[buf][r0 + e] < keypos) pr[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sr[e] = pr[e] * (dp[t][e] - d4[e]);
+      pw[2 * t] = T::pack(pr[0], pr[1]);
+      pw[2 * t + 1] = T::pack(pr[2], pr[3]);
+      sw[2 * t] = T::pack(sr[0], sr[1]);
+      sw[2 * t + 1] = T::pack(sr[2], sr[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      dv[i] = T::mfma16(pw, rd.column(gs, first, i), dv[i]);
+      dk[i] = T::mfma16(sw, rd.column(qs, first, i), dk[i]);
+    }
+    read_ahead<D / 8, 4, 2>();
   }
 
-  // Join the wavefronts that share keys, values first, then keys.
+  // Join the wavefronts that share keys, values first, then keys: lane l holds
+  // column l & 15 of 16 and keys 4 (l >> 4) + r.
   const int64_t out0 = (at.first * p.kv_heads + hk) * D;
+  const int here = min(keys - key_first, KW * 16);
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        sh.join[wave][8 * (r >> 2) + 4 * half + (r & 3)][i * 32 + (lane & 31)] = side == 0 ? dv[i][r] : dk[i][r] * p.scale;
+      for (int r = 0; r < 4; ++r) sh.join[wave][4 * quad + r][i * 16 + (lane & 15)] = side == 0 ? dv[i][r] : dk[i][r] * p.scale;
     __syncthreads();
-    for (int e = tid; e < keys * (D / 2); e += 256) {
-      const int key = e / (D / 2), d = (e % (D / 2)) * 2;
-      float x = 0.f, y = 0.f;
+    for (int e = tid; e < here * (D / 4); e += 256) {
+      const int key = e / (D / 4), d = (e % (D / 4)) * 4;
+      f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < RW; ++w) {
-        x += sh.join[w * KW + key / 32][key % 32][d];
-        y += sh.join[w * KW + key / 32][key % 32][d + 1];
-      }
+      for (int w = 0; w < RW; ++w) x += *reinterpret_cast<const f32x4*>(&sh.join[w * KW + key / 16][key % 16][d]);
       if (pieces == 1) {
-        char* to = static_cast<char*>(side == 0 ? p.dv : p.dk) + (out0 + static_cast<int64_t>(key) * p.kv_heads * D + d) * 2;
-        *reinterpret_cast<uint32_t*>(to) = T::pack(x, y);
+        char* to = static_cast<char*>(side == 0 ? p.dv : p.dk) + (out0 + static_cast<int64_t>(key_first + key) * p.kv_heads * D + d) * 2;
+        *reinterpret_cast<u32x2*>(to) = u32x2{T::pack(x[0], x[1]), T::pack(x[2], x[3])};
       } else {
-        float* to = b.part + ((static_cast<int64_t>(piece) * 2 + side) * p.bs + key) * D + d;
-        to[0] = x;
-        to[1] = y;
+        *reinterpret_cast<f32x4*>(b.part + ((static_cast<int64_t>(piece) * 2 + side) * p.bs + key_first + key) * D + d) = x;
       }
     }
   }
@@ -582,7 +543,7 @@ Layout lay_out(BackArgs& b, int dim) {
   const uint64_t entries = static_cast<uint64_t>(p.kv_heads) * b.rows;
   const uint64_t pairs = static_cast<uint64_t>(p.total_q) * p.select * p.kv_heads;
   const uint64_t pieces = entries + pairs / b.piece;
-  b.max_pieces = pieces > INT32_MAX ? -1 : static_cast<int32_t>(pieces);
+  b.max_pieces = pieces > INT32_MAX / 2 ? -1 : static_cast<int32_t>(pieces);
   Layout l;
   l.delta = 0;
   l.bits = up256(static_cast<uint64_t>(p.total_q) * p.heads * 4);
@@ -595,7 +556,7 @@ Layout lay_out(BackArgs& b, int dim) {
 
 template <typename T, int D, int KW>
 int launch_dkv(const BackArgs& b, hipStream_t stream) {
-  block_attention_dkv_kernel<T, D, KW><<<dim3(static_cast<unsigned>(b.max_pieces)), dim3(256), sizeof(KvShared<D, KW>), stream>>>(b);
+  block_attention_dkv_kernel<T, D, KW><<<dim3(static_cast<unsigned>(b.max_pieces) * (b.a.bs > 64 ? 2u : 1u)), dim3(256), sizeof(KvShared<D, KW>), stream>>>(b);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
@@ -616,7 +577,7 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   count_bits_kernel<<<dim3(static_cast<unsigned>((entries + 3) / 4)), dim3(256), 0, stream>>>(b);
   number_pieces_kernel<<<dim3(1), dim3(1024), 0, stream>>>(b);
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
-  const int st = p.bs == 128 ? launch_dkv<T, D, 4>(b, stream) : (p.bs == 64 ? launch_dkv<T, D, 2>(b, stream) : launch_dkv<T, D, 1>(b, stream));
+  const int st = p.bs >= 64 ? launch_dkv<T, D, 4>(b, stream) : (p.bs == 32 ? launch_dkv<T, D, 2>(b, stream) : launch_dkv<T, D, 1>(b, stream));
   if (st != MI_ATTN_OK) return st;
   join_pieces_kernel<T, D><<<dim3(static_cast<unsigned>(entries), 2 * p.bs * D / 1024), dim3(256), 0, stream>>>(b);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;

@@ -104,16 +104,6 @@ __device__ __forceinline__ u32x4 widen(u32x2 c) {  // 8 codes, exactly
   return r;
 }
 
-// Maximum and sum over the four lanes that hold one row (16 lanes apart).
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return half_max(x);
-}
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return half_sum(x);
-}
-
 template <int D>
 struct DecodeShared {
   union {
