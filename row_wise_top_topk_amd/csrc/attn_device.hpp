@@ -91,13 +91,15 @@ __device__ __forceinline__ u32x2 lds_read_tr8(uint32_t at) {
 }
 
 // A tile of rows of D 16-bit elements in LDS: 16-byte chunks, chunk c of row r
-// at place c ^ swizzle(r).  The swizzle takes rows four apart to neighbouring
-// chunks and rows within a group of four to different quarters of a row, so
-// that both the row reads (16 lanes, 16 rows, one chunk) and the transposing
-// reads (32 lanes, 4 rows, 4 chunks) touch every bank once.
+// at place c ^ swizzle(r).  The swizzle takes rows within a group of four to
+// different quarters of a row and rows four apart to different halves of a
+// quarter, so that the row reads (16 lanes, 16 rows, one chunk) and the
+// transposing reads (32 lanes: 4 rows of 4 chunks, or 8 rows of 2) touch every
+// bank once.
 template <int D>
 __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-  return D == 128 ? ((row & 3u) << 2) | ((row >> 2) & 3u) : (((row >> 1) & 1u) << 2) | ((row >> 2) & 3u);
+  const uint32_t low = ((row >> 1) & 2u) | ((row >> 3) & 1u);
+  return D == 128 ? ((row & 3u) << 2) | low : (((row >> 1) & 1u) << 2) | low;
 }
 
 template <int D>

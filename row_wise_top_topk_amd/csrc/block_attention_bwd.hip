@@ -29,6 +29,7 @@ struct BackArgs {
   uint32_t* bits;      // [kv_heads][rows][words]
   int32_t* first;      // [kv_heads * rows + 1]: first piece of each block
   int32_t* counts;     // [kv_heads * rows]: tokens of each block
+  int32_t* owner;      // [piece]: its block
   float* part;         // [piece][2][bs][D]
   int64_t rows;        // blocks of all sequences, and those of the keys behind them
   int64_t words;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(256) count_bits_kernel(BackArgs b) {
 }
 
 // Pieces of each block (one at least, for the zeros of a block that nobody
-// selected) and their running number; one workgroup.
+// selected), their running number and whose they are; one workgroup.
 __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
   __shared__ int32_t s_wave[16];
   __shared__ int32_t s_base;
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
     int at = s_base + sum - n;
     for (int w = 0; w < wave; ++w) at += s_wave[w];
     if (e < total) b.first[e] = at;
+    for (int i = 0; i < n; ++i) b.owner[at + i] = static_cast<int32_t>(e);
     __syncthreads();
     if (tid == 1023) s_base = at + n;
     __syncthreads();
@@ -272,11 +274,14 @@ __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
 
 // ---- dk, dv ----
 
-constexpr int kStage = 32;  // rows of a stage for each group of wavefronts that shares them
+// Rows of a stage for each group of wavefronts that shares them: the more, the
+// more of the loads' time is covered (64: 410 us, 32: 600, on the case below).
+template <int KW>
+constexpr int kStage = KW == 4 ? 64 : 32;
 
 template <int D, int KW>
 struct KvShared {
-  static constexpr int kRowsAt = kStage * (4 / KW);  // rows staged at a time
+  static constexpr int kRowsAt = kStage<KW> * (4 / KW);  // rows staged at a time
   union {
     struct {
       char q[2][kRowsAt * 2 * D];
@@ -298,7 +303,7 @@ struct KvShared {
 // with 32 the accumulators leave one wavefront a SIMD, and its waits show
 // (measured on 8192 tokens, 32/2 heads, 16 blocks of 64: 690 us).
 template <typename T, int D, int KW>
-__global__ void __launch_bounds__(256, 3) block_attention_dkv_kernel(BackArgs b) {
+__global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b) {
   using Sh = KvShared<D, KW>;
   constexpr int kRowsAt = Sh::kRowsAt, RW = 4 / KW;
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -311,12 +316,7 @@ __global__ void __launch_bounds__(256, 3) block_attention_dkv_kernel(BackArgs b)
   const int piece = blockIdx.x / parts;
   const int key_first = (blockIdx.x % parts) * 64;  // this workgroup's first key within the block
   if (piece >= b.first[entries]) return;
-  int64_t lo = 0, hi = entries - 1;  // the last entry whose first piece is not behind this one
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (b.first[mid] <= piece) lo = mid; else hi = mid - 1;
-  }
-  const int64_t entry = lo;
+  const int64_t entry = b.owner[piece];
   const int hk = static_cast<int>(entry / b.rows);
   const int64_t row = entry % b.rows;
   const Place at = place_of(p.cu_k, p.num_seqs, p.total_k, row, p.bs);
@@ -436,45 +436,48 @@ __global__ void __launch_bounds__(256, 3) block_attention_dkv_kernel(BackArgs b)
     __syncthreads();
     if (r0 + kRowsAt < total) load_rows(r0 + kRowsAt);
     const uint32_t qs = lds_offset(sh.q[buf]), gs = lds_offset(sh.go[buf]);
-    const int first = rwv * kStage;  // this wavefront's rows
-    const bool masked = __any(sh.pos[buf][first + (lane & 31)] < lastpos);
-    f32x4 s[2], dp[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t] = dp[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int sub = 0; sub < kStage<KW>; sub += 32) {
+      const int first = rwv * kStage<KW> + sub;  // this wavefront's rows
+      const bool masked = __any(sh.pos[buf][first + (lane & 31)] < lastpos);
+      f32x4 s[2], dp[2];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) s[t] = T::mfma16(rd.row(qs, first + 16 * t, i), kf[i], s[t]);
+      for (int t = 0; t < 2; ++t) {
+        s[t] = dp[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) dp[t] = T::mfma16(rd.row(gs, first + 16 * t, i), vf[i], dp[t]);
-    }
-    read_ahead<D / 8, 6, 1>();
-    u32x4 pw, sw;
+        for (int i = 0; i < D / 32; ++i) s[t] = T::mfma16(rd.row(qs, first + 16 * t, i), kf[i], s[t]);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r0 = first + 16 * t + 4 * quad;
-      const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[buf][r0]);
-      const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[buf][r0]);
-      float pr[4], sr[4];
+        for (int i = 0; i < D / 32; ++i) dp[t] = T::mfma16(rd.row(gs, first + 16 * t, i), vf[i], dp[t]);
+      }
+      read_ahead<D / 8, 6, 1>();
+      u32x4 pw, sw;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(fmaf(s[t][e], c, -l4[e]));
-      if (masked) {
+      for (int t = 0; t < 2; ++t) {
+        const int r0 = first + 16 * t + 4 * quad;
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(&sh.lse2[buf][r0]);
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(&sh.delta[buf][r0]);
+        float pr[4], sr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (sh.pos[buf][r0 + e] < keypos) pr[e] = 0.f;
+        for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(fmaf(s[t][e], c, -l4[e]));
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (sh.pos[buf][r0 + e] < keypos) pr[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sr[e] = pr[e] * (dp[t][e] - d4[e]);
+        pw[2 * t] = T::pack(pr[0], pr[1]);
+        pw[2 * t + 1] = T::pack(pr[2], pr[3]);
+        sw[2 * t] = T::pack(sr[0], sr[1]);
+        sw[2 * t + 1] = T::pack(sr[2], sr[3]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sr[e] = pr[e] * (dp[t][e] - d4[e]);
-      pw[2 * t] = T::pack(pr[0], pr[1]);
-      pw[2 * t + 1] = T::pack(pr[2], pr[3]);
-      sw[2 * t] = T::pack(sr[0], sr[1]);
-      sw[2 * t + 1] = T::pack(sr[2], sr[3]);
+      for (int i = 0; i < D / 16; ++i) {
+        dv[i] = T::mfma16(pw, rd.column(gs, first, i), dv[i]);
+        dk[i] = T::mfma16(sw, rd.column(qs, first, i), dk[i]);
+      }
+      read_ahead<D / 8, 4, 2>();
     }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      dv[i] = T::mfma16(pw, rd.column(gs, first, i), dv[i]);
-      dk[i] = T::mfma16(sw, rd.column(qs, first, i), dk[i]);
-    }
-    read_ahead<D / 8, 4, 2>();
   }
 
   // Join the wavefronts that share keys, values first, then keys: lane l holds
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(BackArgs b) {
 
 // Sizes of the workspace's parts, 256-byte aligned.
 struct Layout {
-  uint64_t delta, bits, first, counts, part, bytes;
+  uint64_t delta, bits, first, counts, owner, part, bytes;
 };
 
 uint64_t up256(uint64_t n) { return (n + 255) & ~uint64_t{255}; }
@@ -549,7 +552,8 @@ Layout lay_out(BackArgs& b, int dim) {
   l.bits = up256(static_cast<uint64_t>(p.total_q) * p.heads * 4);
   l.first = l.bits + up256(entries * b.words * 4);
   l.counts = l.first + up256((entries + 1) * 4);
-  l.part = l.counts + up256(entries * 4);
+  l.owner = l.counts + up256(entries * 4);
+  l.part = l.owner + up256(pieces * 4);
   l.bytes = l.part + pieces * 2 * p.bs * dim * 4;
   return l;
 }
@@ -613,6 +617,7 @@ MI_ATTN_EXPORT int block_attention_backward(const mi_block_attention_args* args,
   b.bits = reinterpret_cast<uint32_t*>(ws + l.bits);
   b.first = reinterpret_cast<int32_t*>(ws + l.first);
   b.counts = reinterpret_cast<int32_t*>(ws + l.counts);
+  b.owner = reinterpret_cast<int32_t*>(ws + l.owner);
   b.part = reinterpret_cast<float*>(ws + l.part);
   if (args->dtype == MI_ATTN_BF16)
     return args->dim == 128 ? launch_backward<Bf16, 128>(b, stream) : launch_backward<Bf16, 64>(b, stream);
