@@ -38,6 +38,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 
+template <int n>
+struct Int {
+  static constexpr int value = n;
+};
+
 struct Bf16 {
   static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -128,18 +133,25 @@ __device__ __forceinline__ int64_t cu_at(const int32_t* cu, int num, int64_t tot
   return c < 0 ? 0 : (c > total ? total : c);
 }
 
+// For a slot that is the same in the whole wavefront: 64 sequences are looked
+// at together, so a search costs two loads one after the other, not one for
+// each halving.
 __device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per) {
   const int64_t extra = per == 1 ? 0 : 1;
-  int lo = 0, hi = num;  // the last i with first slot <= slot
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_at(cu, num, total, mid) / per + mid * extra <= slot) lo = mid; else hi = mid - 1;
+  const int lane = static_cast<int>(__lane_id());
+  int seq = -1;  // the last i with first slot <= slot
+  for (int i0 = 0; i0 <= num; i0 += 64) {
+    const int i = i0 + lane;
+    const bool before = i <= num && cu_at(cu, num, total, i) / per + i * extra <= slot;
+    const int n = __popcll(__ballot(before));
+    seq += n;
+    if (n < 64) break;
   }
   Place r;
-  r.seq = lo;
-  r.begin = cu_at(cu, num, total, lo);
-  r.end = cu_at(cu, num, total, lo + 1);
-  r.first = r.begin + (slot - (r.begin / per + lo * extra)) * per;
+  r.seq = __builtin_amdgcn_readfirstlane(seq < 0 ? 0 : seq);
+  r.begin = cu_at(cu, num, total, r.seq);
+  r.end = cu_at(cu, num, total, r.seq + 1);
+  r.first = r.begin + (slot - (r.begin / per + r.seq * extra)) * per;
   return r;
 }
 

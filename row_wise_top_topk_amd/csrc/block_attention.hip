@@ -26,7 +26,7 @@ struct Shared {
   Select sel;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem);
@@ -68,37 +68,42 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const Reads<D> rd;
+  const Reads<D> rd(lds_offset(sh.k[0]));
+  constexpr int kBuf = kTile * 2 * D;  // from one buffer to the other; the values lie two behind the keys
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
     const int tiles = ((active << p.lb) + kTile - 1) / kTile;
     if (tiles == 0) continue;
-    Keys next = keys_of(sh.sel, p.lb, p.bs, w0, active, 0);
+    // Keys of the tile in LDS, of the one on its way and of the one behind it;
+    // what a row sees of a tile is worked out one tile ahead.
+    Keys<kWide> next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 0);
     Half<D> kin, vin;
     kin.load(kbase, p.k_t * 2, next, g.len_k);
     vin.load(vbase, p.v_t * 2, next, g.len_k);
-    for (int tile = 0; tile < tiles; ++tile) {
-      const Keys keys = next;
-      const int buf = tile & 1;
+    const int word = tl >> 5 < nw ? tl >> 5 : 0;
+    Sight ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+    next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 1);
+    auto step = [&](auto which, int tile) {
+      constexpr int buf = decltype(which)::value;
       kin.store(sh.k[buf]);
       vin.store(sh.v[buf]);
       __syncthreads();
+      const Sight see = ahead;
       if (tile + 1 < tiles) {
-        next = keys_of(sh.sel, p.lb, p.bs, w0, active, tile + 1);
         kin.load(kbase, p.k_t * 2, next, g.len_k);
         vin.load(vbase, p.v_t * 2, next, g.len_k);
+        ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+        next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 2);
       }
-      const Sight see = sight_of(sh.sel, keys, nw, tl >> 5 < nw ? tl >> 5 : 0, tl & 31, limit, valid);
-      if (!see.any) continue;
-      const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
+      if (!see.any) return;
       f32x16 s[2];
       {
         u32x4 ka[2][D / 16];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) ka[mt][i] = rd.row(ks, mt * 32, i);
+          for (int i = 0; i < D / 16; ++i) ka[mt][i] = rd.row(buf * kBuf, mt * 32, i);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
         float t = s[i >> 1][8 * (i & 1)];
 #pragma unroll
         for (int r = 1; r < 8; ++r) t = fmaxf(t, s[i >> 1][8 * (i & 1) + r]);
-        top = fmaxf(top, see.last[i] >= 0 ? t : -kInf);
+        top = fmaxf(top, sees<kWide>(see, i) ? t : -kInf);
       }
       top = half_max(top);
       // The weights stay relative to an older maximum until it is passed by
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
       float sums[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float from = see.last[i] >= 0 ? base : kInf;
+        const float from = sees<kWide>(see, i) ? base : kInf;
         float w[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) w[r] = exp2_fast(fmaf(s[i >> 1][8 * (i & 1) + r], c, -from));
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int st = 0; st < 4; ++st) va[i][st] = rd.column(vs, 16 * st, i);
+          for (int st = 0; st < 4; ++st) va[i][st] = rd.column((2 + buf) * kBuf, 16 * st, i);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -178,6 +183,10 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
         }
         __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
       }
+    };
+    for (int tile = 0; tile < tiles; tile += 2) {
+      step(Int<0>{}, tile);
+      if (tile + 1 < tiles) step(Int<1>{}, tile + 1);
     }
   }
   sum = half_sum(sum);
@@ -196,11 +205,11 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
   if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : m * p.scale + __logf(sum);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWide>
 int launch(const Args& p, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads;
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
-  block_attention_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(Shared<T, D>), stream>>>(p);
+  block_attention_kernel<T, D, kWide><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(Shared<T, D>), stream>>>(p);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
@@ -239,6 +248,7 @@ int make_args(const mi_block_attention_args* a, Args& p) {
   p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
   p.select = a->select; p.causal = a->causal != 0; p.scale = a->scale;
   p.tokens_per = kRows / p.group;
+  p.select_magic = static_cast<uint32_t>(((uint64_t{1} << 32) + p.select - 1) / p.select);
   p.slots = slots_of(p.total_q, p.num_seqs, p.tokens_per);
   return MI_ATTN_OK;
 }
@@ -251,6 +261,10 @@ MI_ATTN_EXPORT int block_attention(const mi_block_attention_args* args, hipStrea
   Args p;
   const int st = make_args(args, p);
   if (st != MI_ATTN_OK || p.total_q == 0) return st;
-  if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128>(p, stream) : launch<Bf16, 64>(p, stream);
-  return args->dim == 128 ? launch<Fp16, 128>(p, stream) : launch<Fp16, 64>(p, stream);
+  if (p.lb >= 6) {
+    if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128, true>(p, stream) : launch<Bf16, 64, true>(p, stream);
+    return args->dim == 128 ? launch<Fp16, 128, true>(p, stream) : launch<Fp16, 64, true>(p, stream);
+  }
+  if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128, false>(p, stream) : launch<Bf16, 64, false>(p, stream);
+  return args->dim == 128 ? launch<Fp16, 128, false>(p, stream) : launch<Fp16, 64, false>(p, stream);
 }

@@ -28,19 +28,21 @@ struct Args {
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, do_t, do_h;
   int64_t total_q, total_k, slots;
   int32_t num_seqs, heads, kv_heads, group, bs, lb, select, causal, tokens_per;
+  uint32_t select_magic;  // n / select = n * select_magic >> 32 for the entries of a workgroup, select above 1
   float scale;
 };
 
 int make_args(const mi_block_attention_args* a, Args& p);
 
-constexpr int kRows = 128;        // rows of a workgroup
+constexpr int kRows = 128;        // rows of a workgroup: 32 for each of four wavefronts
+constexpr int kThreads = 256;
 constexpr int kTile = 64;         // keys of a tile
 constexpr int kMaskWords = 2048;  // words of token bits, window of block numbers x words per block
 
 struct Select {
   uint32_t mask[kMaskWords];
   uint16_t list[kMaskWords];
-  uint32_t wave_count[4];
+  uint32_t wave_count[kThreads / 64];
 };
 
 // The tokens of one workgroup and how its rows map to them.
@@ -82,73 +84,86 @@ __device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
 // Marks which tokens select each block of [w0, w0 + width) and lists the blocks
 // that any does, ascending.  Returns their number.  Ends with a barrier.
 __device__ __forceinline__ int list_window(const Args& p, const Group& g, int hk, int w0, int width, int nw, Select& s) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  for (int i = tid; i < width * nw; i += 256) s.mask[i] = 0;
-  __syncthreads();
+  constexpr int kWaves = kThreads / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int most = min(width, g.blocks - w0);
   const int32_t* rows = p.blocks + (g.t0 * p.kv_heads + hk) * static_cast<int64_t>(p.select);
   const int64_t stride = static_cast<int64_t>(p.kv_heads) * p.select;
   const int total = g.tokens * p.select;
-  for (int i = tid; i < total; i += 256) {
-    const int tl = i / p.select;
-    const int b = rows[tl * stride + (i - tl * p.select)] - w0;
+  // entry i belongs to token i / select; the first of a thread's entries is on
+  // its way while the words are cleared
+  auto entry = [&](int i, int& tl) {
+    tl = static_cast<int>(__umulhi(static_cast<uint32_t>(i), p.select_magic));
+    if (p.select == 1) tl = i;
+    return rows[tl * stride + (i - tl * p.select)] - w0;
+  };
+  int tl = 0, b = tid < total ? entry(tid, tl) : -1;
+  __syncthreads();
+  for (int i = tid; i < most * nw; i += kThreads) s.mask[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < total; i += kThreads) {
+    if (i != tid) b = entry(i, tl);
     if (b >= 0 && b < most) atomicOr(&s.mask[b * nw + (tl >> 5)], 1u << (tl & 31));
   }
   __syncthreads();
-  // every thread has width / 256 consecutive blocks; counts are summed over
-  // the lanes, then over the wavefronts
-  const int each = (width + 255) >> 8;
+  // a wavefront lists a quarter of the window, 64 blocks at a time: counts
+  // first, then the places
+  const int share = ((most + 64 * kWaves - 1) / (64 * kWaves)) * 64;
+  const int from = min(most, wave * share), to = min(most, from + share);
+  auto taken = [&](int i) {
+    uint32_t any = 0;
+    if (i < to)
+      for (int w = 0; w < nw; ++w) any |= s.mask[i * nw + w];
+    return __ballot(any != 0);
+  };
   int mine = 0;
-  for (int i = 0; i < each; ++i) {
-    const int b = tid * each + i;
-    uint32_t any = 0;
-    if (b < most)
-      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
-    mine += any != 0;
-  }
-  int sum = mine;
-  const int lane = tid & 63, wave = tid >> 6;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(sum, d);
-    if (lane >= d) sum += up;
-  }
-  if (lane == 63) s.wave_count[wave] = sum;
+  for (int i = from; i < to; i += 64) mine += __popcll(taken(i + lane));
+  if (lane == 0) s.wave_count[wave] = mine;
   __syncthreads();
-  int at = sum - mine;
-  int count = 0;
-  for (int w = 0; w < 4; ++w) {
-    const int c = s.wave_count[w];
-    if (w < wave) at += c;
-    count += c;
+  int at = 0, count = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int n = s.wave_count[w];
+    if (w < wave) at += n;
+    count += n;
   }
-  for (int i = 0; i < each; ++i) {
-    const int b = tid * each + i;
-    uint32_t any = 0;
-    if (b < most)
-      for (int w = 0; w < nw; ++w) any |= s.mask[b * nw + w];
-    if (any != 0) s.list[at++] = static_cast<uint16_t>(b);
+  for (int i = from; i < to; i += 64) {
+    const uint64_t has = taken(i + lane);
+    if ((has >> lane) & 1) s.list[at + __popcll(has & ((1ull << lane) - 1))] = static_cast<uint16_t>(i + lane);
+    at += __popcll(has);
   }
   __syncthreads();
-  return count;
+  return __builtin_amdgcn_readfirstlane(count);
 }
 
 // The four 16-key groups of a tile: first key of each in its sequence, or -1.
+// Wide: blocks of 64 keys or more, so that all four are of one block.
+template <bool kWide>
 struct Keys {
+  static constexpr int kIds = kWide ? 1 : 4;
   int32_t key[4];
-  int32_t id[4];  // place of the block in the window
+  int32_t id[kIds];  // place of the block in the window
 };
 
-__device__ __forceinline__ Keys keys_of(const Select& s, int lb, int bs, int w0, int active, int tile) {
-  Keys k;
-  int id[4];
+template <bool kWide>
+__device__ __forceinline__ Keys<kWide> keys_of(const Select& s, int lb, int bs, int w0, int active, int tile) {
+  Keys<kWide> k;
+  if constexpr (kWide) {
+    const int a = tile * kTile;
+    k.id[0] = __builtin_amdgcn_readfirstlane(s.list[min(a >> lb, active - 1)]);
+    const int key = ((w0 + k.id[0]) << lb) + (a & (bs - 1));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) id[i] = s.list[min((tile * kTile + 16 * i) >> lb, active - 1)];
+    for (int i = 0; i < 4; ++i) k.key[i] = key + 16 * i;
+  } else {
+    int id[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int a = tile * kTile + 16 * i;
-    k.id[i] = __builtin_amdgcn_readfirstlane(id[i]);
-    k.key[i] = (a >> lb) < active ? ((w0 + k.id[i]) << lb) + (a & (bs - 1)) : -1;
+    for (int i = 0; i < 4; ++i) id[i] = s.list[min((tile * kTile + 16 * i) >> lb, active - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = tile * kTile + 16 * i;
+      k.id[i] = __builtin_amdgcn_readfirstlane(id[i]);
+      k.key[i] = (a >> lb) < active ? ((w0 + k.id[i]) << lb) + (a & (bs - 1)) : -1;
+    }
   }
   return k;
 }
@@ -164,7 +179,8 @@ struct Half {
 
   // base + key * stride of a 16-key group is uniform; a thread adds its row and
   // chunk in 32 bits.  Rows behind the sequence's last key repeat it.
-  __device__ __forceinline__ void load(const char* base, int64_t stride_bytes, const Keys& k, int len_k) {
+  template <bool kWide>
+  __device__ __forceinline__ void load(const char* base, int64_t stride_bytes, const Keys<kWide>& k, int len_k) {
     const int tid = threadIdx.x;
     const uint32_t chunk = (tid % kLanes) * 16;
     const int row = (tid / kLanes) & 15;
@@ -210,42 +226,67 @@ struct Sight {
   bool partial;  // some row sees a part of a group only
 };
 
-__device__ __forceinline__ Sight sight_of(const Select& s, const Keys& k, int nw, int word, int bit, int limit, bool valid) {
+template <bool kWide>
+__device__ __forceinline__ Sight sight_of(const Select& s, const Keys<kWide>& k, int nw, int word, int bit, int limit, bool valid) {
   Sight v;
-  bool some = false, part = false;
-  uint32_t bits[4];
+  if constexpr (kWide) {
+    const uint32_t bits = s.mask[k.id[0] * nw + word];
+    const int last = (bits >> bit) & 1u ? limit - k.key[0] : -64;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bits[i] = s.mask[k.id[i] * nw + word];
+    for (int i = 0; i < 4; ++i) v.last[i] = last - 16 * i;
+    v.any = __any(valid && last >= 0);
+    v.partial = __any(valid && last >= 0 && last < 63);
+  } else {
+    bool some = false, part = false;
+    uint32_t bits[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v.last[i] = k.key[i] >= 0 && ((bits[i] >> bit) & 1u) ? limit - k.key[i] : -1;
-    some |= v.last[i] >= 0;
-    part |= v.last[i] >= 0 && v.last[i] < 15;
+    for (int i = 0; i < 4; ++i) bits[i] = s.mask[k.id[i] * nw + word];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v.last[i] = k.key[i] >= 0 && ((bits[i] >> bit) & 1u) ? limit - k.key[i] : -1;
+      some |= v.last[i] >= 0;
+      part |= v.last[i] >= 0 && v.last[i] < 15;
+    }
+    v.any = __any(valid && some);
+    v.partial = __any(valid && part);
   }
-  v.any = __any(valid && some);
-  v.partial = __any(valid && part);
   return v;
 }
+
+// Whether a row sees group i, where what it sees a part of has been masked: with
+// one block the first group stands for all.
+template <bool kWide>
+__device__ __forceinline__ bool sees(const Sight& v, int i) { return v.last[kWide ? 0 : i] >= 0; }
 
 // Where a lane reads a tile in LDS.  By rows: row lane & 31 of 32, 8 elements
 // from 16 i + 8 (lane >> 5) on.  Transposed: rows 4 (lane >> 5) .. + 3 (x) and
 // those 8 behind them (y) of 16, column 32 i + (lane & 31); the rows are the
 // order in which the scores of 32 keys lie in a lane's registers.
+// The addresses are those of a tile at `base`; other tiles and rows are constants
+// away, which the instructions add.
 template <int D>
 struct Reads {
-  uint32_t by_row, x, y;
-  __device__ __forceinline__ Reads() {
+  uint32_t r[D / 16], x[D / 32], y[D / 32];
+  __device__ __forceinline__ explicit Reads(uint32_t base) {
     const uint32_t lane = threadIdx.x & 63, half = lane >> 5, li = lane & 15, dhalf = (lane >> 4) & 1;
-    by_row = tile_at<D>(lane & 31, half);
     const uint32_t row = 4 * half + (li >> 2), chunk = dhalf * 2 + ((li & 3) >> 1);
-    x = tile_at<D>(row, chunk) + (li & 1) * 8;
-    y = tile_at<D>(row + 8, chunk) + (li & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) r[i] = keep(base + (tile_at<D>(lane & 31, half) ^ (i * 32)));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      x[i] = keep(base + ((tile_at<D>(row, chunk) + (li & 1) * 8) ^ (i * 64)));
+      y[i] = keep(base + ((tile_at<D>(row + 8, chunk) + (li & 1) * 8) ^ (i * 64)));
+    }
   }
-  // operand i of the 32 rows from `rows` on (a multiple of 32)
-  __device__ __forceinline__ u32x4 row(uint32_t tile, int rows, int i) const { return lds_read16((tile + (by_row ^ (i * 32))) + rows * (2 * D)); }
+  static __device__ __forceinline__ uint32_t keep(uint32_t v) {  // in a register, not worked out again
+    asm volatile("" : "+v"(v));
+    return v;
+  }
+  // operand i of the 32 rows from `rows` on (a multiple of 32) of the tile `at` bytes on
+  __device__ __forceinline__ u32x4 row(int at, int rows, int i) const { return lds_read16(r[i] + (at + rows * 2 * D)); }
   // operand of the 16 rows from `rows` on (a multiple of 16), columns 32 i ..
-  __device__ __forceinline__ u32x4 column(uint32_t tile, int rows, int i) const {
-    const u32x2 a = lds_read_tr16((tile + (x ^ (i * 64))) + rows * (2 * D)), b = lds_read_tr16((tile + (y ^ (i * 64))) + rows * (2 * D));
+  __device__ __forceinline__ u32x4 column(int at, int rows, int i) const {
+    const u32x2 a = lds_read_tr16(x[i] + (at + rows * 2 * D)), b = lds_read_tr16(y[i] + (at + rows * 2 * D));
     return u32x4{a[0], a[1], b[0], b[1]};
   }
 };

@@ -62,7 +62,7 @@ struct QShared {
   Select sel;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kWide>
 __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   QShared<T, D>& sh = *reinterpret_cast<QShared<T, D>*>(smem);
@@ -120,41 +120,45 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   const float c = p.scale * kLog2e;
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const Reads<D> rd;
+  const Reads<D> rd(lds_offset(sh.k[0]));
+  constexpr int kBuf = kTile * 2 * D;  // from one buffer to the other; the values lie two behind the keys
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
     mark_tokens(b, g, hk, w0, active, nw, sh.sel);
     const int tiles = ((active << p.lb) + kTile - 1) / kTile;
     if (tiles == 0) continue;
-    Keys next = keys_of(sh.sel, p.lb, p.bs, w0, active, 0);
+    // Keys of the tile in LDS, of the one on its way and of the one behind it;
+    // what a row sees of a tile is worked out one tile ahead.
+    Keys<kWide> next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 0);
     Half<D> kin, vin;
     kin.load(kbase, p.k_t * 2, next, g.len_k);
     vin.load(vbase, p.v_t * 2, next, g.len_k);
-    for (int tile = 0; tile < tiles; ++tile) {
-      const Keys keys = next;
-      const int buf = tile & 1;
+    const int word = tl >> 5 < nw ? tl >> 5 : 0;
+    Sight ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+    next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 1);
+    auto step = [&](auto which, int tile) {
+      constexpr int buf = decltype(which)::value;
       kin.store(sh.k[buf]);
       vin.store(sh.v[buf]);
       __syncthreads();
+      const Sight see = ahead;
       if (tile + 1 < tiles) {
-        next = keys_of(sh.sel, p.lb, p.bs, w0, active, tile + 1);
         kin.load(kbase, p.k_t * 2, next, g.len_k);
         vin.load(vbase, p.v_t * 2, next, g.len_k);
+        ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+        next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 2);
       }
-      const Sight see = sight_of(sh.sel, keys, nw, tl >> 5 < nw ? tl >> 5 : 0, tl & 31, limit, valid);
-      if (!see.any) continue;
-      const uint32_t ks = lds_offset(sh.k[buf]), vs = lds_offset(sh.v[buf]);
-#pragma unroll 1
+      if (!see.any) return;
+#pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t kt = ks + mt * 32 * 2 * D, vt = vs + mt * 32 * 2 * D;
         f32x16 s, dp;
         {
           u32x4 ka[D / 16], va[D / 16];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) ka[i] = rd.row(kt, 0, i);
+          for (int i = 0; i < D / 16; ++i) ka[i] = rd.row(buf * kBuf, mt * 32, i);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) va[i] = rd.row(vt, 0, i);
+          for (int i = 0; i < D / 16; ++i) va[i] = rd.row((2 + buf) * kBuf, mt * 32, i);
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.f;
 #pragma unroll
@@ -171,15 +175,14 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
           __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
         }
         u32x4 ds[2];
-        const int last[2] = {mt == 0 ? see.last[0] : see.last[2], mt == 0 ? see.last[1] : see.last[3]};
         if (see.partial) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (8 * ((r >> 2) & 1) + (r & 3) + 4 * half > last[r >> 3]) s[r] = -kInf;
+            if (8 * ((r >> 2) & 1) + (r & 3) + 4 * half > see.last[2 * mt + (r >> 3)]) s[r] = -kInf;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float from = last[i] >= 0 ? lse2 : kInf;
+          const float from = sees<kWide>(see, 2 * mt + i) ? lse2 : kInf;
 #pragma unroll
           for (int r = 0; r < 8; r += 2) {
             float w[2];
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int st = 0; st < 2; ++st) ka[i][st] = rd.column(kt, 16 * st, i);
+            for (int st = 0; st < 2; ++st) ka[i][st] = rd.column(buf * kBuf, mt * 32 + 16 * st, i);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -207,6 +210,10 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
           __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
         }
       }
+    };
+    for (int tile = 0; tile < tiles; tile += 2) {
+      step(Int<0>{}, tile);
+      if (tile + 1 < tiles) step(Int<1>{}, tile + 1);
     }
   }
   if (!valid) return;
@@ -575,7 +582,8 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   if (words > 0)
     clear_bits_kernel<<<dim3(static_cast<unsigned>(words / 1024 + 1 < 4096 ? words / 1024 + 1 : 4096)), dim3(256), 0, stream>>>(b);
   if (pairs > 0) {
-    block_attention_dq_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
+    if (p.lb >= 6) block_attention_dq_kernel<T, D, true><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
+    else block_attention_dq_kernel<T, D, false><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
   }
   if (p.total_k == 0) return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
   count_bits_kernel<<<dim3(static_cast<unsigned>((entries + 3) / 4)), dim3(256), 0, stream>>>(b);

@@ -34,7 +34,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) block_means_kernel(MeanArgs p) {
   constexpr int kChunks = D / 8, kKeys = 64 / kChunks;
   const int lane = threadIdx.x & 63;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = item / p.kv_heads;
   const int hk = static_cast<int>(item % p.kv_heads);
   if (row >= p.rows) return;

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attentio
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_per) {
   const int lane = threadIdx.x & 63;
-  const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t item = index / rows_per;
   const int row = static_cast<int>(index % rows_per);
   if (item >= p.slots * p.kv_heads * p.head_chunks) return;
