@@ -27,7 +27,7 @@ struct Shared {
 };
 
 template <typename T, int D, bool kWide>
-__global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
+__global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(Args p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem);
   const int hk = blockIdx.x % p.kv_heads;
@@ -75,28 +75,41 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
     const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
     const int tiles = ((active << p.lb) + kTile - 1) / kTile;
     if (tiles == 0) continue;
-    // Keys of the tile in LDS, of the one on its way and of the one behind it;
-    // what a row sees of a tile is worked out one tile ahead.
+    // While a tile is worked on, the next one goes to the other buffer and the
+    // one behind it is on its way to registers; what a row sees of a tile is
+    // worked out one tile ahead.  The copies are spread over the step, between
+    // the products and the exponentials: in one place they wait for each other
+    // (a step of 4061 cycles held 1177 of that, measured).  Behind the last
+    // tile they copy it again.
+    const int word = tl >> 5 < nw ? tl >> 5 : 0;
     Keys<kWide> next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 0);
     Half<D> kin, vin;
     kin.load(kbase, p.k_t * 2, next, g.len_k);
     vin.load(vbase, p.v_t * 2, next, g.len_k);
-    const int word = tl >> 5 < nw ? tl >> 5 : 0;
     Sight ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+    kin.store(sh.k[0]);
+    vin.store(sh.v[0]);
     next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 1);
+    kin.load(kbase, p.k_t * 2, next, g.len_k);
+    vin.load(vbase, p.v_t * 2, next, g.len_k);
+    Keys<kWide> after = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 2);
+    __syncthreads();
     auto step = [&](auto which, int tile) {
       constexpr int buf = decltype(which)::value;
-      kin.store(sh.k[buf]);
-      vin.store(sh.v[buf]);
-      __syncthreads();
       const Sight see = ahead;
-      if (tile + 1 < tiles) {
-        kin.load(kbase, p.k_t * 2, next, g.len_k);
-        vin.load(vbase, p.v_t * 2, next, g.len_k);
+      auto look_ahead = [&] {
         ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
-        next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 2);
+        next = after;
+        after = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 3);
+      };
+      if (!see.any) {
+        kin.store(sh.k[buf ^ 1]);
+        vin.store(sh.v[buf ^ 1]);
+        kin.load(kbase, p.k_t * 2, after, g.len_k);
+        vin.load(vbase, p.v_t * 2, after, g.len_k);
+        look_ahead();
+        return;
       }
-      if (!see.any) return;
       f32x16 s[2];
       {
         u32x4 ka[2][D / 16];
@@ -111,14 +124,21 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) s[mt] = T::mfma32(ka[mt][i], q[i], s[mt]);
         }
-        // reads of the first 32 keys, then a product and a read of the others in turn
+        kin.store(sh.k[buf ^ 1]);
+        vin.store(sh.v[buf ^ 1]);
+        // reads of the first 32 keys, then a product and a read of the others in
+        // turn, then a product and a write
         __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, D / 16, 0);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        }
       }
       if (see.partial) {
 #pragma unroll
@@ -151,6 +171,8 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[i][r] *= shrink;
       }
+      kin.load(kbase, p.k_t * 2, after, g.len_k);
+      vin.load(vbase, p.v_t * 2, after, g.len_k);
       const float base = m == -kInf ? 0.f : m * c;
       u32x4 pr[4];
       float sums[4];
@@ -175,18 +197,22 @@ __global__ void __launch_bounds__(256, 2) block_attention_kernel(Args p) {
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
-        __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
-        for (int i = 0; i < D / 8 - 4; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        for (int i = 0; i < D / 16; ++i) {  // the loads between the exponentials
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 128 / (D / 16), 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        read_ahead<D / 8, 4, 2>();
       }
+      look_ahead();
     };
     for (int tile = 0; tile < tiles; tile += 2) {
       step(Int<0>{}, tile);
-      if (tile + 1 < tiles) step(Int<1>{}, tile + 1);
+      __syncthreads();
+      if (tile + 1 < tiles) {
+        step(Int<1>{}, tile + 1);
+        __syncthreads();
+      }
     }
   }
   sum = half_sum(sum);
