@@ -125,9 +125,13 @@ int block_scores(const mi_block_scores_args* args, hipStream_t stream);
  *                  MI_ATTN_MAX_SELECT.
  *   out, dq        [total_q, H, D] contiguous; dk, dv [total_k, HK, D]
  *                  contiguous; lse fp32 [total_q, H].
+ *   rest           NULL, or like out: what the rounding of out leaves out.  The
+ *                  forward computes out more exactly then; the backward takes it
+ *                  in where it is given (bf16: dq 3 times nearer to the exact
+ *                  one).
  *   scale          positive and finite.
- * block_attention_backward() takes out and lse as block_attention() gave them
- * and a workspace of block_attention_workspace() bytes (16-byte aligned).
+ * block_attention_backward() takes out, rest and lse as block_attention()
+ * gave them and a workspace of block_attention_workspace() bytes (16-byte aligned).
  */
 typedef struct mi_block_attention_args {
   const void* q;
@@ -137,6 +141,7 @@ typedef struct mi_block_attention_args {
   const int32_t* cu_q;
   const int32_t* cu_k;
   void* out;
+  void* rest;
   float* lse;
   const void* dout;
   void* dq;

@@ -45,8 +45,8 @@ class _ScoreArgs(ctypes.Structure):
 
 
 class _AttentionArgs(ctypes.Structure):
-    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "blocks", "cu_q", "cu_k", "out", "lse", "dout", "dq", "dk", "dv",
-                                    "workspace")]
+    _fields_ = ([(n, _vp) for n in ("q", "k", "v", "blocks", "cu_q", "cu_k", "out", "rest", "lse", "dout", "dq", "dk",
+                                    "dv", "workspace")]
                 + [("workspace_bytes", ctypes.c_uint64)]
                 + [(n, _i64) for n in ("q_stride_t", "q_stride_h", "k_stride_t", "k_stride_h", "v_stride_t", "v_stride_h",
                                        "dout_stride_t", "dout_stride_h", "total_q", "total_k")]
@@ -309,7 +309,7 @@ def _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale
 
 def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: torch.Tensor, block_size: int,
                     cu_seqlens: torch.Tensor = None, cu_seqlens_k: torch.Tensor = None, scale: float = None,
-                    causal: bool = True, out: torch.Tensor = None):
+                    causal: bool = True, out: torch.Tensor = None, rest: torch.Tensor = None):
     """Attention of each query over the key blocks that it selects.
 
     ``q`` ``[tokens, heads, dim]``, ``k`` and ``v`` ``[keys, kv_heads, dim]``
@@ -323,16 +323,20 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     log-sum of the scaled scores' exponentials, float32 ``[tokens, heads]``.  A
     query that sees no key, and a row behind the last sequence, has 0 and -inf.
 
-    Differentiable in q, k and v through autograd (``lse`` is not; ``out=`` is
-    refused then).  Inputs are taken to be finite."""
+    Differentiable in q, k and v through autograd (``lse`` is not; ``out=`` and
+    ``rest=`` are refused then).  A caller of ``block_attention_backward`` gives
+    ``rest`` (like ``out``), which receives what the rounding of ``out`` leaves
+    out."""
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
-        if out is not None:
-            raise ValueError("out cannot be given where a gradient is asked for")
+        if out is not None or rest is not None:
+            raise ValueError("out and rest cannot be given where a gradient is asked for")
         return _BlockAttention.apply(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     out = _output(out, q.shape, q.dtype, q.device, "out")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    a.out, a.lse = out.data_ptr(), lse.data_ptr()
+    if rest is not None:
+        _output(rest, q.shape, q.dtype, q.device, "rest")
+    a.out, a.rest, a.lse = out.data_ptr(), _ptr(rest), lse.data_ptr()
     with torch.cuda.device(q.device):
         _check(_lib().block_attention(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream), "block_attention")
     return out, lse
@@ -340,10 +344,12 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
 
 def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                              lse: torch.Tensor, blocks: torch.Tensor, block_size: int, cu_seqlens: torch.Tensor = None,
-                             cu_seqlens_k: torch.Tensor = None, scale: float = None, causal: bool = True):
+                             cu_seqlens_k: torch.Tensor = None, scale: float = None, causal: bool = True,
+                             rest: torch.Tensor = None):
     """Gradients ``(dq, dk, dv)`` of ``block_attention`` for the gradient ``dout``
     of its ``out``; ``out`` and ``lse`` as it returned them, the rest as it was
-    called.  The result is the same from run to run.  With float16 the scores'
+    called; ``rest`` as ``block_attention`` filled it in (without it dq loses
+    precision).  The result is the same from run to run.  With float16 the scores'
     gradients are held in float16: below about 6e-8 they are lost (scale the
     loss)."""
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
@@ -352,9 +358,11 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
         raise ValueError("dout must have q's shape")
     _output(out, q.shape, q.dtype, q.device, "out")
     _output(lse, q.shape[:2], torch.float32, q.device, "lse")
+    if rest is not None:
+        _output(rest, q.shape, q.dtype, q.device, "rest")
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
-    a.out, a.lse, a.dout, a.dq, a.dk, a.dv = (_ptr(t) for t in (out, lse, dout, dq, dk, dv))
+    a.out, a.rest, a.lse, a.dout, a.dq, a.dk, a.dv = (_ptr(t) for t in (out, rest, lse, dout, dq, dk, dv))
     a.dout_stride_t, a.dout_stride_h = _strides(dout)
     lib = _lib()
     with torch.cuda.device(q.device):
@@ -369,8 +377,9 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
 class _BlockAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
-        out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
-        ctx.save_for_backward(q, k, v, out, lse, blocks, cu_seqlens, cu_seqlens_k)
+        rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal, rest=rest)
+        ctx.save_for_backward(q, k, v, out, rest, lse, blocks, cu_seqlens, cu_seqlens_k)
         ctx.rest = (block_size, scale, causal)
         ctx.mark_non_differentiable(lse)
         return out, lse
@@ -378,11 +387,11 @@ class _BlockAttention(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout, _):
-        q, k, v, out, lse, blocks, cu_q, cu_k = ctx.saved_tensors
+        q, k, v, out, rest, lse, blocks, cu_q, cu_k = ctx.saved_tensors
         block_size, scale, causal = ctx.rest
         if dout.stride(2) != 1 or dout.data_ptr() % 16 or any(dout.stride(i) % 8 for i in (0, 1)):
             dout = dout.clone(memory_format=torch.contiguous_format)
-        dq, dk, dv = block_attention_backward(dout, q, k, v, out, lse, blocks, block_size, cu_q, cu_k, scale, causal)
+        dq, dk, dv = block_attention_backward(dout, q, k, v, out, lse, blocks, block_size, cu_q, cu_k, scale, causal, rest)
         need = ctx.needs_input_grad
         return dq if need[0] else None, dk if need[1] else None, dv if need[2] else None, *(None,) * 6
 

@@ -26,7 +26,10 @@ struct Shared {
   Select sel;
 };
 
-template <typename T, int D, bool kWide>
+// With kRest the weights of the second product have two terms (16 bits of 24)
+// and the part of out that its own rounding leaves out is stored too: the
+// gradient subtracts dout . out from terms that it nearly cancels.
+template <typename T, int D, bool kWide, bool kRest>
 __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(Args p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem);
@@ -185,6 +188,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
 #pragma unroll
         for (int r = 0; r < 4; ++r) pr[i][r] = T::pack(w[2 * r], w[2 * r + 1]);
         sums[i] = ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        if constexpr (kRest) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) s[i >> 1][8 * (i & 1) + r] = w[r];
+        }
       }
       sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
       {
@@ -197,12 +204,25 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
+        if constexpr (kRest) {
+          // the second terms read V again: its operands do not fit beside them
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // the loads between the exponentials
-          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 128 / (D / 16), 0);
+          for (int st = 0; st < 4; ++st) {
+            u32x4 low;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              low[r] = T::pack(s[st >> 1][8 * (st & 1) + 2 * r] - T::lo(pr[st][r]), s[st >> 1][8 * (st & 1) + 2 * r + 1] - T::hi(pr[st][r]));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] = T::mfma32(rd.column((2 + buf) * kBuf, 16 * st, i), low, acc[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {  // the loads between the exponentials
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 128 / (D / 16), 0);
+          }
+          read_ahead<D / 8, 4, 2>();
         }
-        read_ahead<D / 8, 4, 2>();
       }
       look_ahead();
     };
@@ -218,7 +238,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
   sum = half_sum(sum);
   if (!valid) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  char* to = static_cast<char*>(p.out) + (tok * p.heads + head) * (2 * D) + half * 8;
+  const int64_t to_at = (tok * p.heads + head) * (2 * D) + half * 8;
+  char* to = static_cast<char*>(p.out) + to_at;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -227,15 +248,29 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       w[0] = T::pack(acc[i][r] * inv, acc[i][r + 1] * inv);
       w[1] = T::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv);
       *reinterpret_cast<u32x2*>(to + i * 64 + (r >> 2) * 16) = w;
+      if constexpr (kRest) {
+        u32x2 z;
+        z[0] = T::pack(acc[i][r] * inv - T::lo(w[0]), acc[i][r + 1] * inv - T::hi(w[0]));
+        z[1] = T::pack(acc[i][r + 2] * inv - T::lo(w[1]), acc[i][r + 3] * inv - T::hi(w[1]));
+        *reinterpret_cast<u32x2*>(static_cast<char*>(p.rest) + to_at + i * 64 + (r >> 2) * 16) = z;
+      }
     }
   if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : m * p.scale + __logf(sum);
 }
 
-template <typename T, int D, bool kWide>
+template <typename T, int D>
 int launch(const Args& p, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads;
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
-  block_attention_kernel<T, D, kWide><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(Shared<T, D>), stream>>>(p);
+  const dim3 g(static_cast<unsigned>(grid)), b(256);
+  const size_t lds = sizeof(Shared<T, D>);
+  if (p.lb >= 6) {
+    if (p.rest != nullptr) block_attention_kernel<T, D, true, true><<<g, b, lds, stream>>>(p);
+    else block_attention_kernel<T, D, true, false><<<g, b, lds, stream>>>(p);
+  } else {
+    if (p.rest != nullptr) block_attention_kernel<T, D, false, true><<<g, b, lds, stream>>>(p);
+    else block_attention_kernel<T, D, false, false><<<g, b, lds, stream>>>(p);
+  }
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
@@ -259,14 +294,14 @@ int make_args(const mi_block_attention_args* a, Args& p) {
   const bool some_q = a->total_q > 0, some_k = a->total_k > 0;
   if (some_q && (a->q == nullptr || a->blocks == nullptr || a->out == nullptr || a->lse == nullptr)) return MI_ATTN_EINVAL;
   if (some_k && (a->k == nullptr || a->v == nullptr)) return MI_ATTN_EINVAL;
-  const void* wide[] = {a->q, a->k, a->v, a->out};
+  const void* wide[] = {a->q, a->k, a->v, a->out, a->rest};
   for (const void* x : wide)
     if (reinterpret_cast<uintptr_t>(x) & 15u) return MI_ATTN_EINVAL;
   const void* words[] = {a->blocks, a->cu_q, a->cu_k, a->lse};
   for (const void* x : words)
     if (reinterpret_cast<uintptr_t>(x) & 3u) return MI_ATTN_EINVAL;
   p.q = a->q; p.k = a->k; p.v = a->v; p.blocks = a->blocks; p.cu_q = a->cu_q; p.cu_k = a->cu_k;
-  p.out = a->out; p.lse = a->lse; p.dout = a->dout; p.dq = a->dq; p.dk = a->dk; p.dv = a->dv;
+  p.out = a->out; p.rest = a->rest; p.lse = a->lse; p.dout = a->dout; p.dq = a->dq; p.dk = a->dk; p.dv = a->dv;
   p.q_t = a->q_stride_t; p.q_h = a->q_stride_h; p.k_t = a->k_stride_t; p.k_h = a->k_stride_h;
   p.v_t = a->v_stride_t; p.v_h = a->v_stride_h; p.do_t = a->dout_stride_t; p.do_h = a->dout_stride_h;
   p.total_q = a->total_q; p.total_k = a->total_k;
@@ -287,10 +322,6 @@ MI_ATTN_EXPORT int block_attention(const mi_block_attention_args* args, hipStrea
   Args p;
   const int st = make_args(args, p);
   if (st != MI_ATTN_OK || p.total_q == 0) return st;
-  if (p.lb >= 6) {
-    if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128, true>(p, stream) : launch<Bf16, 64, true>(p, stream);
-    return args->dim == 128 ? launch<Fp16, 128, true>(p, stream) : launch<Fp16, 64, true>(p, stream);
-  }
-  if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128, false>(p, stream) : launch<Bf16, 64, false>(p, stream);
-  return args->dim == 128 ? launch<Fp16, 128, false>(p, stream) : launch<Fp16, 64, false>(p, stream);
+  if (args->dtype == MI_ATTN_BF16) return args->dim == 128 ? launch<Bf16, 128>(p, stream) : launch<Bf16, 64>(p, stream);
+  return args->dim == 128 ? launch<Fp16, 128>(p, stream) : launch<Fp16, 64>(p, stream);
 }

@@ -20,6 +20,7 @@ struct Args {
   const int32_t* cu_q;
   const int32_t* cu_k;
   void* out;
+  void* rest;
   float* lse;
   const void* dout;
   void* dq;

@@ -3,6 +3,10 @@
 //   p_j = exp(scale q.k_j - lse),  delta = dout . out,  ds_j = p_j (dout.v_j - delta)
 //   dq = scale sum_j ds_j k_j,  dk_j = scale sum_q ds_j q,  dv_j = sum_q p_j dout
 //
+// The ds_j of a row add up to 0, so what keys have in common cancels in dq and
+// roundings show: there ds is multiplied as two 16-bit terms, and delta takes
+// out with what its rounding left out.  dk and dv round p and ds once.
+//
 // dq goes over the rows as the forward does.  dk and dv go over the key blocks:
 // a bit matrix [key head][block][token] says which tokens selected a block
 // (atomic OR, so its content does not depend on their order), a block's tokens
@@ -88,7 +92,9 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   {
     const char* from = static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h) * 2 + half * 16;
     const char* gfrom = static_cast<const char*>(p.dout) + (tok * p.do_t + head * p.do_h) * 2 + half * 16;
-    const char* ofrom = static_cast<const char*>(p.out) + (tok * p.heads + head) * (2 * D) + half * 16;
+    const int64_t o_at = (tok * p.heads + head) * (2 * D) + half * 16;
+    const char* ofrom = static_cast<const char*>(p.out) + o_at;
+    const char* rfrom = p.rest == nullptr ? nullptr : static_cast<const char*>(p.rest) + o_at;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       q[i] = go[i] = u32x4{0, 0, 0, 0};
@@ -100,6 +106,14 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
         for (int e = 0; e < 4; ++e) {
           delta = fmaf(T::lo(go[i][e]), T::lo(o[e]), delta);
           delta = fmaf(T::hi(go[i][e]), T::hi(o[e]), delta);
+        }
+        if (rfrom != nullptr) {
+          const u32x4 z = *reinterpret_cast<const u32x4*>(rfrom + i * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            delta = fmaf(T::lo(go[i][e]), T::lo(z[e]), delta);
+            delta = fmaf(T::hi(go[i][e]), T::hi(z[e]), delta);
+          }
         }
       }
     }
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
           }
           __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
         }
-        u32x4 ds[2];
+        u32x4 ds[2], low[2];
         if (see.partial) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
@@ -189,6 +203,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
 #pragma unroll
             for (int e = 0; e < 2; ++e) w[e] = exp2_fast(fmaf(s[8 * i + r + e], c, -from)) * (dp[8 * i + r + e] - delta);
             ds[i][r >> 1] = T::pack(w[0], w[1]);
+            low[i][r >> 1] = T::pack(w[0] - T::lo(ds[i][r >> 1]), w[1] - T::hi(ds[i][r >> 1]));
           }
         }
         {
@@ -200,14 +215,17 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int st = 0; st < 2; ++st) acc[i] = T::mfma32(ka[i][st], ds[st], acc[i]);
+            for (int st = 0; st < 2; ++st) {
+              acc[i] = T::mfma32(ka[i][st], ds[st], acc[i]);
+              acc[i] = T::mfma32(ka[i][st], low[st], acc[i]);
+            }
           __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
           for (int i = 0; i < D / 16 - 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
           }
-          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
         }
       }
     };
