@@ -92,37 +92,52 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.kv8_attention_workspace.restype = ctypes.c_uint64
 
 
+_loaded = None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _lib():
-    from . import load_library
-    return load_library()
+    global _loaded
+    if _loaded is None:
+        from . import load_library
+        _loaded = load_library()
+    return _loaded
 
 
-def _check(status: int, what: str) -> None:
+def _run(device, what: str, fn, *args) -> None:
+    """``fn(*args, stream)`` on ``device`` and its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         raise RuntimeError(f"{what} failed: {_STATUS.get(status, 'unknown status')} (status {status})")
 
 
-def _heads(t, what: str, device=None, dtype=None, dim=None) -> None:
-    """A [tokens, heads, dim] operand as the kernels read it."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype not in _DTYPES:
+def _heads(t, what: str, device=None, dtype=None, dim=None):
+    """Checks a [tokens, heads, dim] operand; returns its shape and (token, head) strides, 0 for an axis of one entry."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3:
         raise ValueError(f"{what} must be a 3-D bfloat16 or float16 tensor [tokens, heads, dim]")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a GPU")
     if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{what} must have the others' type and device")
-    if t.shape[2] not in HEAD_DIMS or (dim is not None and t.shape[2] != dim):
+    tokens, heads, d = t.shape
+    if d not in HEAD_DIMS or (dim is not None and d != dim):
         raise ValueError(f"{what} must have a head dimension in {HEAD_DIMS}, the same for all")
-    if t.shape[1] < 1:
+    if heads < 1:
         raise ValueError(f"{what} must have at least one head")
-    if t.numel() and (t.stride(2) != 1 or t.data_ptr() % 16
-                      or any(t.shape[i] > 1 and (t.stride(i) % 8 or t.stride(i) < 0) for i in (0, 1))):
+    st, sh, sd = t.stride()
+    if tokens <= 1:
+        st = 0
+    if heads <= 1:
+        sh = 0
+    if tokens and (sd != 1 or st % 8 or sh % 8 or st < 0 or sh < 0 or t.data_ptr() % 16):
         raise ValueError(f"{what} must have unit stride along its last axis, 16-byte-aligned data and other strides "
                          "that are multiples of 8 elements")
-
-
-def _strides(t):
-    """(token, head) strides; of an axis of one entry, 0."""
-    return (int(t.stride(0)) if t.shape[0] > 1 else 0, int(t.stride(1)) if t.shape[1] > 1 else 0)
+    return tokens, heads, d, st, sh
 
 
 def _ints(t, what: str, device, dims: int, shape=None) -> None:
@@ -156,8 +171,8 @@ def _table(t, device):
     if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2 or t.device != device
             or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
         raise ValueError("block_table must be a 2-D int32 tensor on the others' device with unit stride along its last axis")
-    n, cols = int(t.shape[0]), int(t.shape[1])
-    return n, cols, int(t.stride(0)) if n > 1 else cols
+    n, cols = t.shape
+    return n, cols, t.stride(0) if n > 1 else cols
 
 
 def _block_size(block_size) -> int:
@@ -200,14 +215,12 @@ def block_means(k: torch.Tensor, block_size: int, cu_seqlens: torch.Tensor = Non
     i is row ``cu_seqlens[i] // block_size + i + b``; rows that are no block
     are 0."""
     bs = _block_size(block_size)
-    _heads(k, "k")
-    total, hk, dim = (int(x) for x in k.shape)
-    cu, _, n = _sequences(cu_seqlens, None, k.device, total, total)
-    out = _output(out, (total // bs + n, hk, dim), torch.float32, k.device, "out")
-    st, sh = _strides(k)
-    with torch.cuda.device(k.device):
-        _check(_lib().block_means(_DTYPES[k.dtype], k.data_ptr(), st, sh, total, hk, dim, bs, _ptr(cu), n,
-                                  out.data_ptr(), torch.cuda.current_stream(k.device).cuda_stream), "block_means")
+    total, hk, dim, st, sh = _heads(k, "k")
+    device = k.device
+    cu, _, n = _sequences(cu_seqlens, None, device, total, total)
+    out = _output(out, (total // bs + n, hk, dim), torch.float32, device, "out")
+    _run(device, "block_means", _lib().block_means, _DTYPES[k.dtype], k.data_ptr(), st, sh, total, hk, dim, bs, _ptr(cu), n,
+         out.data_ptr())
     return out
 
 
@@ -235,9 +248,9 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     the pages gives its block -inf.  Rows behind the last sequence are -inf
     with count 0."""
     bs = _block_size(block_size)
-    _heads(q, "q")
+    a = _ScoreArgs()
+    total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
     device = q.device
-    total, heads, dim = (int(x) for x in q.shape)
     if (not isinstance(means, torch.Tensor) or means.dtype != torch.float32 or means.dim() != 3 or means.device != device
             or not means.is_contiguous() or means.shape[2] != dim or means.shape[1] < 1):
         raise ValueError("means must be a contiguous float32 tensor [rows, kv_heads, dim] on q's device")
@@ -248,7 +261,6 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     max_blocks, first, last = int(max_blocks), int(first), int(last)
     if max_blocks < 1 or max_blocks >= 1 << 22 or first < 0 or last < 0:
         raise ValueError("max_blocks must be in [1, 2^22), first and last not negative")
-    a = _ScoreArgs()
     if block_table is not None:
         if lengths is None or cu_seqlens_k is not None:
             raise ValueError("the paged form takes block_table and lengths, without cu_seqlens_k")
@@ -271,36 +283,31 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     counts = torch.empty((total, hk), dtype=torch.int32, device=device)
     a.q, a.means, a.cu_q, a.cu_k = q.data_ptr(), means.data_ptr(), _ptr(cu_q), _ptr(cu_k)
     a.lengths, a.block_table, a.scores, a.counts = _ptr(lengths), _ptr(block_table), scores.data_ptr(), counts.data_ptr()
-    a.q_stride_t, a.q_stride_h = _strides(q)
     a.total_q, a.total_k, a.mean_rows = total, total, int(means.shape[0])
     a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
     a.max_blocks, a.first, a.last, a.scale = max_blocks, first, last, _scale(scale, dim)
-    with torch.cuda.device(device):
-        _check(_lib().block_scores(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "block_scores")
+    _run(device, "block_scores", _lib().block_scores, ctypes.byref(a))
     return scores, counts
 
 
 def _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
     bs = _block_size(block_size)
-    _heads(q, "q")
-    total, heads, dim = (int(x) for x in q.shape)
-    _heads(k, "k", q.device, q.dtype, dim)
-    _heads(v, "v", q.device, q.dtype, dim)
+    a = _AttentionArgs()
+    total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
+    device = q.device
+    total_k, hk, _, a.k_stride_t, a.k_stride_h = _heads(k, "k", device, q.dtype, dim)
+    _, _, _, a.v_stride_t, a.v_stride_h = _heads(v, "v", device, q.dtype, dim)
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    total_k, hk = int(k.shape[0]), int(k.shape[1])
-    if total_k > 1 and max(k.stride(0), v.stride(0)) >= 1 << 23:
+    if a.k_stride_t >= 1 << 23 or a.v_stride_t >= 1 << 23:
         raise ValueError("k and v must have token strides below 2^23 elements")
     _groups(heads, hk)
     if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or not 1 <= blocks.shape[2] <= MAX_SELECT:
         raise ValueError(f"blocks must be an int32 tensor [tokens, kv_heads, selected], selected in [1, {MAX_SELECT}]")
-    _ints(blocks, "blocks", q.device, 3, (total, hk, blocks.shape[2]))
-    cu_q, cu_k, n = _sequences(cu_seqlens, cu_seqlens_k, q.device, total, total_k)
-    a = _AttentionArgs()
-    a.q, a.k, a.v, a.blocks, a.cu_q, a.cu_k = (_ptr(t) for t in (q, k, v, blocks, cu_q, cu_k))
-    a.q_stride_t, a.q_stride_h = _strides(q)
-    a.k_stride_t, a.k_stride_h = _strides(k)
-    a.v_stride_t, a.v_stride_h = _strides(v)
+    _ints(blocks, "blocks", device, 3, (total, hk, blocks.shape[2]))
+    cu_q, cu_k, n = _sequences(cu_seqlens, cu_seqlens_k, device, total, total_k)
+    a.q, a.k, a.v, a.blocks = q.data_ptr(), k.data_ptr(), v.data_ptr(), blocks.data_ptr()
+    a.cu_q, a.cu_k = _ptr(cu_q), _ptr(cu_k)
     a.total_q, a.total_k = total, total_k
     a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
     a.select, a.causal, a.scale = int(blocks.shape[2]), int(bool(causal)), _scale(scale, dim)
@@ -337,8 +344,7 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     if rest is not None:
         _output(rest, q.shape, q.dtype, q.device, "rest")
     a.out, a.rest, a.lse = out.data_ptr(), _ptr(rest), lse.data_ptr()
-    with torch.cuda.device(q.device):
-        _check(_lib().block_attention(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream), "block_attention")
+    _run(q.device, "block_attention", _lib().block_attention, ctypes.byref(a))
     return out, lse
 
 
@@ -353,7 +359,7 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     gradients are held in float16: below about 6e-8 they are lost (scale the
     loss)."""
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
-    _heads(dout, "dout", q.device, q.dtype, int(q.shape[2]))
+    _, _, _, a.dout_stride_t, a.dout_stride_h = _heads(dout, "dout", q.device, q.dtype, q.shape[2])
     if dout.shape != q.shape:
         raise ValueError("dout must have q's shape")
     _output(out, q.shape, q.dtype, q.device, "out")
@@ -363,14 +369,11 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
     a.out, a.rest, a.lse, a.dout, a.dq, a.dk, a.dv = (_ptr(t) for t in (out, rest, lse, dout, dq, dk, dv))
-    a.dout_stride_t, a.dout_stride_h = _strides(dout)
     lib = _lib()
-    with torch.cuda.device(q.device):
-        a.workspace_bytes = lib.block_attention_workspace(ctypes.byref(a))
-        workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=q.device)
-        a.workspace = workspace.data_ptr()
-        _check(lib.block_attention_backward(ctypes.byref(a), torch.cuda.current_stream(q.device).cuda_stream),
-               "block_attention_backward")
+    a.workspace_bytes = lib.block_attention_workspace(ctypes.byref(a))
+    workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=q.device)
+    a.workspace = workspace.data_ptr()
+    _run(q.device, "block_attention_backward", lib.block_attention_backward, ctypes.byref(a))
     return dq, dk, dv
 
 
@@ -403,7 +406,7 @@ def _cache(k_cache, v_cache, k_scale, v_scale, device, hk=None, dim=None):
                 or not t.is_contiguous() or t.shape != k_cache.shape or (t.numel() and t.data_ptr() % 16)):
             raise ValueError(f"{what} must be a contiguous float8_e4m3fn tensor [pages, kv_heads, block_size, dim] on the "
                              "others' device, 16-byte aligned, k_cache and v_cache of one shape")
-    pages, heads, bs, d = (int(x) for x in k_cache.shape)
+    pages, heads, bs, d = k_cache.shape
     _block_size(bs)
     if d not in HEAD_DIMS or heads < 1 or (hk is not None and heads != hk) or (dim is not None and d != dim):
         raise ValueError(f"the cache must have the others' heads and head dimension, one of {HEAD_DIMS}")
@@ -440,26 +443,23 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache:
     Pages outside the cache store nothing; no two sequences may store into one
     page.  ``k_mean`` (float32 ``[pages, kv_heads, dim]``) receives the mean of
     the keys of each page that got tokens: the ``means`` of ``block_scores``."""
-    _heads(k, "k")
+    a = _AppendArgs()
+    total, hk, dim, a.k_stride_t, a.k_stride_h = _heads(k, "k")
     device = k.device
-    _heads(v, "v", device, k.dtype, int(k.shape[2]))
+    _, _, _, a.v_stride_t, a.v_stride_h = _heads(v, "v", device, k.dtype, dim)
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    total, hk, dim = (int(x) for x in k.shape)
     pages, _, bs, _ = _cache(k_cache, v_cache, k_scale, v_scale, device, hk, dim)
-    a = _AppendArgs()
     n, a.block_table_cols, a.block_table_stride = _table(block_table, device)
     _cache_sequences(cu_seqlens, lengths, n, total, device)
     if k_mean is not None:
         _output(k_mean, (pages, hk, dim), torch.float32, device, "k_mean")
-    (a.k, a.v, a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.k_mean, a.block_table, a.lengths, a.cu) = (
-        _ptr(t) for t in (k, v, k_cache, v_cache, k_scale, v_scale, k_mean, block_table, lengths, cu_seqlens))
-    a.k_stride_t, a.k_stride_h = _strides(k)
-    a.v_stride_t, a.v_stride_h = _strides(v)
+    a.k, a.v, a.k_cache, a.v_cache = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    a.k_scale, a.v_scale, a.k_mean = k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_mean)
+    a.block_table, a.lengths, a.cu = block_table.data_ptr(), lengths.data_ptr(), _ptr(cu_seqlens)
     a.total, a.num_pages, a.num_seqs = total, pages, n
     a.dtype, a.kv_heads, a.dim, a.block_size = _DTYPES[k.dtype], hk, dim, bs
-    with torch.cuda.device(device):
-        _check(_lib().kv8_append(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "kv8_append")
+    _run(device, "kv8_append", _lib().kv8_append, ctypes.byref(a))
 
 
 def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -477,12 +477,11 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     how the work is split.
 
     Returns ``(out, lse)`` as ``block_attention`` does."""
-    _heads(q, "q")
+    a = _DecodeArgs()
+    total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
     device = q.device
-    total, heads, dim = (int(x) for x in q.shape)
     pages, hk, bs, _ = _cache(k_cache, v_cache, k_scale, v_scale, device, None, dim)
     _groups(heads, hk)
-    a = _DecodeArgs()
     n, a.block_table_cols, a.block_table_stride = _table(block_table, device)
     _cache_sequences(cu_seqlens, lengths, n, total, device)
     if a.block_table_cols * bs >= 1 << 30:
@@ -496,17 +495,16 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         raise ValueError("max_length must not be negative")
     out = _output(out, q.shape, q.dtype, device, "out")
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
-    a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.block_table, a.lengths, a.cu, a.blocks, a.out, a.lse = (
-        _ptr(t) for t in (q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens, blocks, out, lse))
-    a.q_stride_t, a.q_stride_h = _strides(q)
+    a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    a.k_scale, a.v_scale, a.block_table = k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr()
+    a.lengths, a.cu, a.blocks, a.out, a.lse = lengths.data_ptr(), _ptr(cu_seqlens), _ptr(blocks), out.data_ptr(), lse.data_ptr()
     a.total_q, a.num_pages, a.max_length, a.num_seqs = total, pages, max_length, n
     a.dtype, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], heads, hk, dim, bs
     a.select, a.scale = 0 if blocks is None else int(blocks.shape[2]), _scale(scale, dim)
     lib = _lib()
-    with torch.cuda.device(device):
-        a.workspace_bytes = lib.kv8_attention_workspace(ctypes.byref(a))
-        if a.workspace_bytes:
-            workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
-            a.workspace = workspace.data_ptr()
-        _check(lib.kv8_attention(ctypes.byref(a), torch.cuda.current_stream(device).cuda_stream), "kv8_attention")
+    a.workspace_bytes = lib.kv8_attention_workspace(ctypes.byref(a))
+    if a.workspace_bytes:
+        workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
+        a.workspace = workspace.data_ptr()
+    _run(device, "kv8_attention", lib.kv8_attention, ctypes.byref(a))
     return out, lse
