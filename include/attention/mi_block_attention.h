@@ -80,7 +80,7 @@ int block_means(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stri
  * position up to the query's; counts[t][c] is the number of those.  The first
  * `first` of them and the last `last` of them are forced: their score is +inf.
  * Scores from counts[t][c] on are -inf.  Rows of queries without blocks, and
- * rows behind the last sequence, are -inf with count 0.  A NaN among a
+ * rows behind the last sequence, are -inf with count 0. 
  * block's products makes its score NaN.
  *
  * The means are those of block_means() (block_table NULL; cu_k as there), or

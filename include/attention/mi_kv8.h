@@ -42,7 +42,8 @@ extern "C" {
  * that quotient rounded to nearest even.  A page that a call finds empty (its
  * first token is new) takes the scale of the new tokens.  In a page that holds
  * tokens the scale can only grow: if the new tokens need a larger one, the
- * codes that are there are rounded again under it.  Infinite values become
+ * codes that are there are rounded again under it; a scale that is no power of
+ * two grows to the next one.  Infinite values become
  * +-448 * scale, NaN stays NaN.  No two sequences of a call may store into one
  * page.
  *

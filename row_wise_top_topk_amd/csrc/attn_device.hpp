@@ -126,32 +126,34 @@ struct Place {
   int64_t begin;
 };
 
-__device__ __forceinline__ int64_t cu_at(const int32_t* cu, int num, int64_t total, int i) {
+// (totals are below 2^31: 32-bit arithmetic, 64-bit division is slow)
+__device__ __forceinline__ int32_t cu_at(const int32_t* cu, int num, int64_t total64, int i) {
+  const int32_t total = static_cast<int32_t>(total64);
   if (i > num) return total;
-  if (cu == nullptr) return num == 1 ? (i == 0 ? 0 : total) : (i < total ? i : total);
-  const int64_t c = cu[i];
-  return c < 0 ? 0 : (c > total ? total : c);
+  if (cu == nullptr) return num == 1 ? (i == 0 ? 0 : total) : min(i, total);
+  return max(0, min(cu[i], total));
 }
 
 // For a slot that is the same in the whole wavefront: 64 sequences are looked
 // at together, so a search costs two loads one after the other, not one for
 // each halving.
 __device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per) {
-  const int64_t extra = per == 1 ? 0 : 1;
+  const uint32_t extra = per == 1 ? 0 : 1, wide = static_cast<uint32_t>(per);
   const int lane = static_cast<int>(__lane_id());
   int seq = -1;  // the last i with first slot <= slot
   for (int i0 = 0; i0 <= num; i0 += 64) {
     const int i = i0 + lane;
-    const bool before = i <= num && cu_at(cu, num, total, i) / per + i * extra <= slot;
+    const bool before = i <= num && static_cast<uint32_t>(cu_at(cu, num, total, i)) / wide + i * extra <= static_cast<uint32_t>(slot);
     const int n = __popcll(__ballot(before));
     seq += n;
     if (n < 64) break;
   }
   Place r;
   r.seq = __builtin_amdgcn_readfirstlane(seq < 0 ? 0 : seq);
-  r.begin = cu_at(cu, num, total, r.seq);
-  r.end = cu_at(cu, num, total, r.seq + 1);
-  r.first = r.begin + (slot - (r.begin / per + r.seq * extra)) * per;
+  const uint32_t begin = __builtin_amdgcn_readfirstlane(cu_at(cu, num, total, r.seq));
+  r.begin = begin;
+  r.end = __builtin_amdgcn_readfirstlane(cu_at(cu, num, total, r.seq + 1));
+  r.first = r.begin + (slot - (begin / wide + r.seq * extra)) * per;
   return r;
 }
 

@@ -34,7 +34,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) block_means_kernel(MeanArgs p) {
   constexpr int kChunks = D / 8, kKeys = 64 / kChunks;
   const int lane = threadIdx.x & 63;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = item / p.kv_heads;
   const int hk = static_cast<int>(item % p.kv_heads);
   if (row >= p.rows) return;
@@ -77,24 +77,20 @@ struct ScoreArgs {
   float* scores;
   int32_t* counts;
   int64_t q_t, q_h, total_q, total_k, mean_rows, table_stride, slots;
-  int32_t num_seqs, heads, kv_heads, group, bs, max_blocks, first, last, tokens_per, chunk;
+  int32_t num_seqs, heads, kv_heads, group, bs, lb, max_blocks, first, last, tokens_per, chunk;
   float scale;
 };
 
-// Splits 8 floats into bf16 terms: x = t0 + t1 + t2 up to 2^-24 of x.  An
-// infinite or NaN x stays in the first term.
+// Splits 8 floats into bf16 terms: x = t0 + t1 + t2 up to 2^-24 of x.
 __device__ __forceinline__ void split3(const float* x, u32x4* t) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float a = x[2 * e], b = x[2 * e + 1];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const uint32_t w = Bf16::pack(a, b);
-      t[i][e] = w;
-      a -= Bf16::lo(w);
-      b -= Bf16::hi(w);
-      a = a == a ? a : 0.f;
-      b = b == b ? b : 0.f;
+      t[i][e] = Bf16::pack(a, b);
+      a -= Bf16::lo(t[i][e]);
+      b -= Bf16::hi(t[i][e]);
     }
   }
 }
@@ -104,9 +100,7 @@ __device__ __forceinline__ void split2(const float* x, u32x4* t) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t w = Fp16::pack(x[2 * e], x[2 * e + 1]);
-    float a = (x[2 * e] - Fp16::lo(w)) * 2048.f, b = (x[2 * e + 1] - Fp16::hi(w)) * 2048.f;
-    a = a == a ? a : 0.f;
-    b = b == b ? b : 0.f;
+    const float a = (x[2 * e] - Fp16::lo(w)) * 2048.f, b = (x[2 * e + 1] - Fp16::hi(w)) * 2048.f;
     t[0][e] = w;
     t[1][e] = Fp16::pack(a, b);
   }
@@ -123,7 +117,7 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
   constexpr int kPad = 20;
   __shared__ float s_best[4][RT * 16 * kPad];
   const int hk = blockIdx.x % p.kv_heads;
-  const int64_t slot = blockIdx.x / p.kv_heads;
+  const int64_t slot = static_cast<int>(blockIdx.x / p.kv_heads);
   const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, p.tokens_per);
   const int64_t left = at.end - at.first;
   const int tokens = static_cast<int>(left < 0 ? 0 : (left < p.tokens_per ? left : p.tokens_per));
@@ -135,7 +129,7 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
     } else {
       const int64_t k0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
       len = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - k0;
-      base = k0 / p.bs + at.seq;
+      base = (k0 >> p.lb) + at.seq;
     }
     if (len < 0) len = 0;
   }
@@ -144,15 +138,15 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
   auto count_of = [&](int tl) {
     const int64_t pos = pos0 + tl;
     if (at.seq >= p.num_seqs || len == 0 || pos < 0) return 0;
-    const int64_t n = pos / p.bs + 1;
+    const int64_t n = (pos >> p.lb) + 1;
     return static_cast<int>(n < p.max_blocks ? n : p.max_blocks);
   };
   const int seen = count_of(tokens - 1);  // positions ascend
   if (blockIdx.y == 0)
     for (int tl = threadIdx.x; tl < tokens; tl += 256) p.counts[(at.first + tl) * p.kv_heads + hk] = count_of(tl);
 
-  u32x4 q[RT][D / 32];
   const int kg = lane >> 4;
+  u32x4 q[RT][D / 32];
   if (seen > 0) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -261,6 +255,7 @@ int launch_scores(const ScoreArgs& p0, bool few, hipStream_t stream) {
   if (grid > INT32_MAX || chunks > 65535) return MI_ATTN_EINVAL;
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(chunks));
   if (few) block_scores_kernel<T, D, 1><<<g, dim3(256), 0, stream>>>(p);
+  else if (p.group <= 64) block_scores_kernel<T, D, 4><<<g, dim3(256), 0, stream>>>(p);
   else block_scores_kernel<T, D, 8><<<g, dim3(256), 0, stream>>>(p);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
@@ -284,7 +279,7 @@ MI_ATTN_EXPORT int block_means(int32_t dtype, const void* k, int64_t k_stride_t,
   if (p.rows == 0) return MI_ATTN_OK;
   if (means == nullptr || (total_k > 0 && k == nullptr)) return MI_ATTN_EINVAL;
   const int64_t grid = (p.rows * kv_heads + 3) / 4;
-  if (grid > INT32_MAX) return MI_ATTN_EINVAL;
+  if (grid > INT32_MAX / 4) return MI_ATTN_EINVAL;
   const dim3 g(static_cast<unsigned>(grid));
   if (dtype == MI_ATTN_BF16) {
     if (dim == 128) block_means_kernel<Bf16, 128><<<g, dim3(256), 0, stream>>>(p);
@@ -320,11 +315,12 @@ MI_ATTN_EXPORT int block_scores(const mi_block_scores_args* a, hipStream_t strea
   p.scores = a->scores; p.counts = a->counts; p.q_t = a->q_stride_t; p.q_h = a->q_stride_h;
   p.total_q = a->total_q; p.total_k = a->cu_k == nullptr ? a->total_k : INT32_MAX; p.mean_rows = a->mean_rows; p.table_stride = a->block_table_stride;
   p.num_seqs = a->num_seqs; p.heads = a->heads; p.kv_heads = a->kv_heads; p.group = a->heads / a->kv_heads;
-  p.bs = a->block_size; p.max_blocks = a->max_blocks; p.first = a->first; p.last = a->last; p.scale = a->scale;
+  p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size)); p.max_blocks = a->max_blocks; p.first = a->first; p.last = a->last; p.scale = a->scale;
   // Few rows for each sequence (a decode batch): tiles of 16 rows, and the
-  // blocks are split over workgroups; many: tiles of 128 rows.
+  // blocks are split over workgroups; many: tiles of 64 rows, or of 128 where a
+  // group needs them.
   const bool few = a->total_q * p.group <= static_cast<int64_t>(a->num_seqs) * 16 && p.group <= 16;
-  p.tokens_per = (few ? 16 : 128) / p.group;
+  p.tokens_per = (few ? 16 : (p.group <= 64 ? 64 : 128)) / p.group;
   if (a->cu_q == nullptr && paged) p.tokens_per = 1;  // one query a sequence
   p.slots = slots_of(p.total_q, p.num_seqs, p.tokens_per);
   p.chunk = few ? 128 : 1024;

@@ -52,10 +52,10 @@ struct Rows {
   int len;                 // keys of the sequence that the table can hold
 };
 
-__device__ __forceinline__ Rows rows_of(const DecodeArgs& p, int64_t item, int rows) {
+__device__ __forceinline__ Rows rows_of(const DecodeArgs& p, uint32_t item, int rows) {
   Rows r;
   const int hc = static_cast<int>(item % p.head_chunks);
-  const int64_t rest = item / p.head_chunks;
+  const uint32_t rest = item / p.head_chunks;
   r.hk = static_cast<int>(rest % p.kv_heads);
   const Place at = place_of(p.cu, p.num_seqs, p.total_q, rest / p.kv_heads, p.tokens_per);
   r.seq = at.seq;
@@ -175,7 +175,7 @@ template <typename T, int D, int MT>
 __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attention_kernel(DecodeArgs p) {
   constexpr int R = MT * 16;
   __shared__ __attribute__((aligned(16))) DecodeShared<D> sh;
-  const int64_t item = blockIdx.x / p.splits;
+  const int64_t item = static_cast<int>(blockIdx.x / p.splits);
   const int split = blockIdx.x % p.splits;
   const Rows rw = rows_of(p, item, R);
   if (rw.tokens == 0) return;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attentio
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_per) {
   const int lane = threadIdx.x & 63;
-  const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t index = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t item = index / rows_per;
   const int row = static_cast<int>(index % rows_per);
   if (item >= p.slots * p.kv_heads * p.head_chunks) return;
@@ -440,18 +440,38 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_pe
   float top = -kInf;
   for (int s = lane; s < used; s += 64) top = fmaxf(top, p.part_ml[(at + static_cast<int64_t>(s) * rows_per) * 2]);
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float from = top == -kInf ? 0.f : top;
   float l = 0.f, o[D / 64];
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) o[i] = 0.f;
-  for (int s = 0; s < used; ++s) {
-    const int64_t a = at + static_cast<int64_t>(s) * rows_per;
-    const float mm = p.part_ml[a * 2], ll = p.part_ml[a * 2 + 1];
-    if (ll == 0.f) continue;
-    const float f = exp2_fast(mm - (top == -kInf ? 0.f : top));
-    l += ll * (ll == ll ? f : 1.f);
+  // 64 chunks at a time: a lane works out the weight of one, then all add the
+  // chunks' values, eight loads in flight.  A chunk that added nothing may not
+  // have written any.
+  for (int s0 = 0; s0 < used; s0 += 64) {
+    const int n = min(64, used - s0);
+    float f = 0.f;
+    if (lane < n) {
+      const int64_t a = at + static_cast<int64_t>(s0 + lane) * rows_per;
+      const float ll = p.part_ml[a * 2 + 1];
+      f = ll == 0.f ? 0.f : exp2_fast(p.part_ml[a * 2] - from);
+      l += ll * (ll == ll ? f : 1.f);
+    }
+    const float* values = p.part + (at + static_cast<int64_t>(s0) * rows_per) * D + lane * (D / 64);
+    for (int s = 0; s < n; s += 8) {
+      float x[8][D / 64];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) o[i] += p.part[a * D + lane * (D / 64) + i] * f;
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) x[u][i] = values[static_cast<int64_t>(min(s + u, n - 1)) * rows_per * D + i];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s + u));  // 0 from n on
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) o[i] += fs == 0.f ? 0.f : x[u][i] * fs;
+      }
+    }
   }
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
   const int64_t tok = rw.first + row / rw.heads, h = rw.head0 + row % rw.heads;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   char* to = static_cast<char*>(p.out) + ((tok * p.heads + h) * D + lane * (D / 64)) * 2;
@@ -472,7 +492,7 @@ int launch_decode(const DecodeArgs& p, int mt, hipStream_t stream) {
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   if (p.splits > 1) {
     const int64_t joins = (items * mt * 16 + 3) / 4;
-    if (joins > INT32_MAX) return MI_ATTN_EINVAL;
+    if (joins > INT32_MAX / 4) return MI_ATTN_EINVAL;
     kv8_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, mt * 16);
     if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   }
@@ -489,7 +509,7 @@ struct Plan {
 // tokens of a sequence where it reads its whole cache; one token's heads where
 // each token selects its own blocks), 64 at most.  Chunks: about four
 // workgroups for each of the 256 compute units, chunks of 128 keys at least
-// and 2048 at most, so that long and short sequences of a batch even out.
+// and 4096 at most, so that long and short sequences of a batch even out.
 Plan make_plan(const mi_kv8_attention_args* a) {
   Plan p;
   const int group = a->heads / a->kv_heads;
@@ -506,7 +526,7 @@ Plan make_plan(const mi_kv8_attention_args* a) {
   if (most > a->block_table_cols) most = a->block_table_cols;
   if (sparse && most > a->select) most = a->select;
   if (most < 1) most = 1;
-  const int64_t least = 128 / a->block_size < 1 ? 1 : 128 / a->block_size, top = 2048 / a->block_size;
+  const int64_t least = 128 / a->block_size < 1 ? 1 : 128 / a->block_size, top = 4096 / a->block_size;
   const int64_t want = p.items > 0 ? (1024 + p.items - 1) / p.items : 1;  // chunks of an item
   int64_t chunk = (most + want - 1) / want;
   chunk = chunk < least ? least : (chunk > top ? top : chunk);

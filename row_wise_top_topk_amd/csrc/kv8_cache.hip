@@ -26,7 +26,8 @@ struct AppendArgs {
   const int32_t* cu;
   int64_t x_t[2], x_h[2];
   int64_t total, num_pages, table_stride;
-  int32_t table_cols, num_seqs, kv_heads, bs;
+  int32_t table_cols, num_seqs, kv_heads;
+  uint32_t bs, lb;
 };
 
 // The smallest power of two that brings `most` to 448 or less: with
@@ -62,9 +63,10 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
   __shared__ float s_most[4];
   __shared__ float s_sum[4][D];
   const int side = blockIdx.x & 1;
-  const int64_t item = blockIdx.x >> 1;
+  const uint32_t item = blockIdx.x >> 1;
   const int hk = static_cast<int>(item % p.kv_heads);
-  const int64_t slot = item / p.kv_heads;
+  const uint32_t slot = item / p.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 
   // sequence i owns the slots [cu[i] / bs + 2 i, cu[i + 1] / bs + 2 i + 2): n
   // tokens from any place of a page touch ceil(n / bs) + 1 pages at most
@@ -75,29 +77,32 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
     from = slot;
     n = 1;
   } else {
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu_at(p.cu, p.num_seqs, p.total, mid) / p.bs + 2 * static_cast<int64_t>(mid) <= slot) lo = mid; else hi = mid - 1;
+    int before = 0;  // sequences whose first slot is not behind this one, 64 at a time
+    for (int i0 = 0; i0 < p.num_seqs; i0 += 64) {
+      const int i = i0 + lane;
+      const bool yes = i < p.num_seqs && static_cast<uint32_t>(cu_at(p.cu, p.num_seqs, p.total, i)) / p.bs + 2u * i <= slot;
+      const int some = __popcll(__ballot(yes));
+      before += some;
+      if (some < 64) break;
     }
-    seq = lo;
-    from = cu_at(p.cu, p.num_seqs, p.total, lo);
-    n = cu_at(p.cu, p.num_seqs, p.total, lo + 1) - from;
-    j = slot - (from / p.bs + 2 * static_cast<int64_t>(lo));
+    seq = __builtin_amdgcn_readfirstlane(before > 0 ? before - 1 : 0);
+    from = cu_at(p.cu, p.num_seqs, p.total, seq);
+    n = cu_at(p.cu, p.num_seqs, p.total, seq + 1) - from;
+    j = slot - (static_cast<uint32_t>(from) / p.bs + 2u * seq);
   }
   if (n <= 0) return;
   const int64_t len = p.lengths[seq], start = len - n;
   if (len <= 0) return;
-  j += (start < 0 ? 0 : start) / p.bs;
-  if (j * p.bs >= len || j >= p.table_cols) return;
+  j += (start < 0 ? 0 : start) >> p.lb;
+  if ((j << p.lb) >= len || j >= p.table_cols) return;
   const int64_t page = p.table[seq * p.table_stride + j];
   if (page < 0 || page >= p.num_pages) return;
-  const int held = static_cast<int>(start - j * p.bs < 0 ? 0 : start - j * p.bs);  // rows that were there
-  const int there = static_cast<int>(len - j * p.bs < p.bs ? len - j * p.bs : p.bs);
+  const int64_t first = j << p.lb;
+  const int held = static_cast<int>(start < first ? 0 : start - first);  // rows that were there
+  const int there = static_cast<int>(len - first < p.bs ? len - first : p.bs);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int chunk = tid % kChunks, row0 = tid / kChunks;
-  const char* x = static_cast<const char*>(p.x[side]) + ((from + j * p.bs - start) * p.x_t[side] + hk * p.x_h[side] + chunk * 8) * 2;
+  const char* x = static_cast<const char*>(p.x[side]) + ((from + first - start) * p.x_t[side] + hk * p.x_h[side] + chunk * 8) * 2;
   float* scale_at = p.scale[side] + page * p.kv_heads + hk;
   float old = *scale_at;  // read by all before the barrier, written by one behind it
   u32x4 in[kSteps];
@@ -124,12 +129,12 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
   float scale = scale_for(most);
   if (held == 0) old = scale;
   if (!(old > 0.f && old < kInf)) old = scale_for(0.f);
-  scale = fmaxf(scale, old);
+  // a scale that somebody else left there is taken up to a power of two
+  const uint32_t bits = __float_as_uint(old);
+  scale = fmaxf(scale, __uint_as_float((bits + 0x7fffffu) & 0x7f800000u));
   const bool grows = scale > old;
   const bool wants_mean = side == 0 && p.mean != nullptr;
   uint8_t* cache = p.cache[side] + ((page * p.kv_heads + hk) * p.bs) * D + chunk * 8;
-  // x / scale: by the reciprocal where that is exact
-  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
   const float inv = 1.f / scale, shrink = old / scale;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float a = T::lo(in[s][2 * h]), b = T::hi(in[s][2 * h]), c = T::lo(in[s][2 * h + 1]), d = T::hi(in[s][2 * h + 1]);
-        w[h] = exact ? codes4(a * inv, b * inv, c * inv, d * inv) : codes4(a / scale, b / scale, c / scale, d / scale);
+        w[h] = codes4(a * inv, b * inv, c * inv, d * inv);
       }
       *at = w;
     } else {
@@ -214,6 +219,7 @@ MI_ATTN_EXPORT int kv8_append(const mi_kv8_append_args* a, hipStream_t stream) {
   p.x_t[0] = a->k_stride_t; p.x_h[0] = a->k_stride_h; p.x_t[1] = a->v_stride_t; p.x_h[1] = a->v_stride_h;
   p.total = a->total; p.num_pages = a->num_pages; p.table_stride = a->block_table_stride; p.table_cols = a->block_table_cols;
   p.num_seqs = a->num_seqs; p.kv_heads = a->kv_heads; p.bs = a->block_size;
+  p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
   const int64_t slots = a->cu == nullptr ? a->num_seqs : a->total / a->block_size + 2 * static_cast<int64_t>(a->num_seqs);
   const int64_t grid = slots * a->kv_heads * 2;
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
