@@ -135,26 +135,44 @@ __device__ __forceinline__ int32_t cu_at(const int32_t* cu, int num, int64_t tot
 }
 
 // For a slot that is the same in the whole wavefront: 64 sequences are looked
-// at together, so a search costs two loads one after the other, not one for
-// each halving.
-__device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per) {
+// at together, and what belongs to them is loaded beside them, so that a search
+// costs about one load's time.  also(i) is loaded for sequence i; what it gave
+// for the one found, and for the next, come back in x0 and x1.
+template <typename F>
+__device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per, F also, int32_t& x0, int32_t& x1) {
   const uint32_t extra = per == 1 ? 0 : 1, wide = static_cast<uint32_t>(per);
   const int lane = static_cast<int>(__lane_id());
-  int seq = -1;  // the last i with first slot <= slot
+  int seq = -1, first = 0;  // the last i with first slot <= slot; the first of the 64 looked at
+  int32_t c = 0, x = 0;
   for (int i0 = 0; i0 <= num; i0 += 64) {
     const int i = i0 + lane;
-    const bool before = i <= num && static_cast<uint32_t>(cu_at(cu, num, total, i)) / wide + i * extra <= static_cast<uint32_t>(slot);
+    first = i0;
+    c = cu_at(cu, num, total, i);
+    x = also(i);
+    const bool before = i <= num && static_cast<uint32_t>(c) / wide + i * extra <= static_cast<uint32_t>(slot);
     const int n = __popcll(__ballot(before));
     seq += n;
     if (n < 64) break;
   }
   Place r;
   r.seq = __builtin_amdgcn_readfirstlane(seq < 0 ? 0 : seq);
-  const uint32_t begin = __builtin_amdgcn_readfirstlane(cu_at(cu, num, total, r.seq));
+  // the sequence lies among the last 64 looked at, or just before them
+  auto pick = [&](int32_t mine, int i, auto value) {
+    return i >= first && i < first + 64 ? __builtin_amdgcn_readlane(mine, i - first) : __builtin_amdgcn_readfirstlane(value(i));
+  };
+  auto at = [&](int i) { return cu_at(cu, num, total, i); };
+  const uint32_t begin = pick(c, r.seq, at);
   r.begin = begin;
-  r.end = __builtin_amdgcn_readfirstlane(cu_at(cu, num, total, r.seq + 1));
+  r.end = pick(c, r.seq + 1, at);
+  x0 = pick(x, r.seq, also);
+  x1 = pick(x, r.seq + 1, also);
   r.first = r.begin + (slot - (begin / wide + r.seq * extra)) * per;
   return r;
+}
+
+__device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per) {
+  int32_t x0, x1;
+  return place_of(cu, num, total, slot, per, [](int) { return 0; }, x0, x1);
 }
 
 // Maximum and sum over a lane and its partner in the other half wavefront.

@@ -57,7 +57,8 @@ struct Group {
 };
 
 __device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
-  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, tq);
+  int32_t k0, k1;
+  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, tq, [&](int i) { return cu_at(p.cu_k, p.num_seqs, p.total_k, i); }, k0, k1);
   Group g;
   g.t0 = at.first;
   g.begin = at.begin;
@@ -67,10 +68,9 @@ __device__ __forceinline__ Group group_of(const Args& p, int64_t slot, int tq) {
   g.row0 = 0;
   g.len_k = 0;
   if (at.seq < p.num_seqs) {
-    g.tk0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
-    const int64_t n = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - g.tk0;
-    g.len_k = static_cast<int32_t>(n < 0 ? 0 : n);
-    g.row0 = g.tk0 / p.bs + at.seq;
+    g.tk0 = k0;
+    g.len_k = k1 < k0 ? 0 : k1 - k0;
+    g.row0 = (k0 >> p.lb) + at.seq;
   }
   g.shift = g.len_k - static_cast<int32_t>(at.end - at.begin);
   int64_t seen = g.len_k;

@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b)
   const int64_t entry = b.owner[piece];
   const int hk = static_cast<int>(entry / b.rows);
   const int64_t row = entry % b.rows;
-  const Place at = place_of(p.cu_k, p.num_seqs, p.total_k, row, p.bs);
+  int32_t q0, q1;  // the sequence's queries
+  const Place at = place_of(p.cu_k, p.num_seqs, p.total_k, row, p.bs, [&](int i) { return cu_at(p.cu_q, p.num_seqs, p.total_q, i); }, q0, q1);
   const int64_t left = at.end - at.first;
   const int keys = static_cast<int>(left < 0 ? 0 : (left < p.bs ? left : p.bs));
   if (keys <= key_first) return;
@@ -354,10 +355,10 @@ __global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b)
   const int tokens = max(0, min(b.piece, count - part * b.piece));
 
   // the piece's tokens: those of rank [part * piece, ..) in the block's bits
-  int64_t q0 = 0, q1 = 0, shift = 0;
-  if (at.seq < p.num_seqs) {
-    q0 = cu_at(p.cu_q, p.num_seqs, p.total_q, at.seq);
-    q1 = cu_at(p.cu_q, p.num_seqs, p.total_q, at.seq + 1);
+  int64_t shift = 0;
+  if (at.seq >= p.num_seqs) {
+    q0 = q1 = 0;
+  } else {
     shift = (at.end - at.begin) - (q1 - q0) - q0;  // position of token t: t + shift
   }
   if (tokens > 0) {

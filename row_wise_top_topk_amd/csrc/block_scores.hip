@@ -118,18 +118,21 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
   __shared__ float s_best[4][RT * 16 * kPad];
   const int hk = blockIdx.x % p.kv_heads;
   const int64_t slot = static_cast<int>(blockIdx.x / p.kv_heads);
-  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, p.tokens_per);
+  int32_t x0, x1;
+  const Place at = place_of(p.cu_q, p.num_seqs, p.total_q, slot, p.tokens_per, [&](int i) {
+    if (p.table == nullptr) return cu_at(p.cu_k, p.num_seqs, p.total_k, i);
+    return i < p.num_seqs ? p.lengths[i] : 0;
+  }, x0, x1);
   const int64_t left = at.end - at.first;
   const int tokens = static_cast<int>(left < 0 ? 0 : (left < p.tokens_per ? left : p.tokens_per));
   if (tokens == 0) return;
   int64_t len = 0, base = 0;
   if (at.seq < p.num_seqs) {
     if (p.table != nullptr) {
-      len = p.lengths[at.seq];
+      len = x0;
     } else {
-      const int64_t k0 = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq);
-      len = cu_at(p.cu_k, p.num_seqs, p.total_k, at.seq + 1) - k0;
-      base = (k0 >> p.lb) + at.seq;
+      len = x1 - x0;
+      base = (x0 >> p.lb) + at.seq;
     }
     if (len < 0) len = 0;
   }

@@ -57,7 +57,9 @@ __device__ __forceinline__ Rows rows_of(const DecodeArgs& p, uint32_t item, int 
   const int hc = static_cast<int>(item % p.head_chunks);
   const uint32_t rest = item / p.head_chunks;
   r.hk = static_cast<int>(rest % p.kv_heads);
-  const Place at = place_of(p.cu, p.num_seqs, p.total_q, rest / p.kv_heads, p.tokens_per);
+  int32_t len, none;
+  const Place at = place_of(p.cu, p.num_seqs, p.total_q, rest / p.kv_heads, p.tokens_per,
+                            [&](int i) { return i < p.num_seqs ? p.lengths[i] : 0; }, len, none);
   r.seq = at.seq;
   r.first = at.first;
   const int64_t left = at.end - at.first;
@@ -68,7 +70,7 @@ __device__ __forceinline__ Rows rows_of(const DecodeArgs& p, uint32_t item, int 
   r.len = 0;
   r.pos = -1;
   if (at.seq < p.num_seqs && r.tokens > 0) {
-    const int64_t len = p.lengths[at.seq], most = static_cast<int64_t>(p.table_cols) << p.lb;
+    const int64_t most = static_cast<int64_t>(p.table_cols) << p.lb;
     r.pos = len - (at.end - at.begin) + (at.first - at.begin);
     r.len = static_cast<int>(len < 0 ? 0 : (len < most ? len : most));
   }

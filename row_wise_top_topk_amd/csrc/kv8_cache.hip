@@ -56,7 +56,7 @@ __device__ __forceinline__ f32x4 values4(uint32_t w) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
+__global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs p) {
   constexpr int kChunks = D / 8;            // 8 elements each
   constexpr int kRowsPer = 256 / kChunks;   // rows of the page in one step
   constexpr int kSteps = 128 / kRowsPer;    // of a page of 128 rows
@@ -71,27 +71,40 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(AppendArgs p) {
   // sequence i owns the slots [cu[i] / bs + 2 i, cu[i + 1] / bs + 2 i + 2): n
   // tokens from any place of a page touch ceil(n / bs) + 1 pages at most
   int seq = 0;
-  int64_t from = 0, n = 0, j = 0;
+  int64_t from = 0, n = 0, j = 0, len = 0;
   if (p.cu == nullptr) {
     seq = static_cast<int>(slot);
     from = slot;
     n = 1;
+    len = p.lengths[seq];
   } else {
-    int before = 0;  // sequences whose first slot is not behind this one, 64 at a time
+    int before = 0, last = 0;
+    int32_t c = 0, next = 0, mine = 0;  // sequences whose first slot is not behind this one, 64 at a time
     for (int i0 = 0; i0 < p.num_seqs; i0 += 64) {
       const int i = i0 + lane;
-      const bool yes = i < p.num_seqs && static_cast<uint32_t>(cu_at(p.cu, p.num_seqs, p.total, i)) / p.bs + 2u * i <= slot;
+      last = i0;
+      c = cu_at(p.cu, p.num_seqs, p.total, i);
+      next = cu_at(p.cu, p.num_seqs, p.total, i + 1);
+      mine = i < p.num_seqs ? p.lengths[i] : 0;
+      const bool yes = i < p.num_seqs && (static_cast<uint32_t>(c) >> p.lb) + 2u * i <= slot;
       const int some = __popcll(__ballot(yes));
       before += some;
       if (some < 64) break;
     }
     seq = __builtin_amdgcn_readfirstlane(before > 0 ? before - 1 : 0);
-    from = cu_at(p.cu, p.num_seqs, p.total, seq);
-    n = cu_at(p.cu, p.num_seqs, p.total, seq + 1) - from;
-    j = slot - (static_cast<uint32_t>(from) / p.bs + 2u * seq);
+    if (seq >= last) {
+      from = __builtin_amdgcn_readlane(c, seq - last);
+      n = __builtin_amdgcn_readlane(next, seq - last) - from;
+      len = __builtin_amdgcn_readlane(mine, seq - last);
+    } else {  // the last of the 64 before
+      from = cu_at(p.cu, p.num_seqs, p.total, seq);
+      n = cu_at(p.cu, p.num_seqs, p.total, seq + 1) - from;
+      len = p.lengths[seq];
+    }
+    j = slot - ((static_cast<uint32_t>(from) >> p.lb) + 2u * seq);
   }
   if (n <= 0) return;
-  const int64_t len = p.lengths[seq], start = len - n;
+  const int64_t start = len - n;
   if (len <= 0) return;
   j += (start < 0 ? 0 : start) >> p.lb;
   if ((j << p.lb) >= len || j >= p.table_cols) return;
