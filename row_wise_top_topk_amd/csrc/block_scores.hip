@@ -115,7 +115,8 @@ template <typename T, int D, int RT>
 __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
   constexpr bool kHalf = __is_same(T, Fp16);
   constexpr int kPad = 20;
-  __shared__ float s_best[4][RT * 16 * kPad];
+  __shared__ __attribute__((aligned(16))) float s_best[4][RT * 16 * kPad];
+  __shared__ __attribute__((aligned(1024))) char s_q[RT * 32 * D];
   const int hk = blockIdx.x % p.kv_heads;
   const int64_t slot = static_cast<int>(blockIdx.x / p.kv_heads);
   int32_t x0, x1;
@@ -149,17 +150,27 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
     for (int tl = threadIdx.x; tl < tokens; tl += 256) p.counts[(at.first + tl) * p.kv_heads + hk] = count_of(tl);
 
   const int kg = lane >> 4;
+  // the rows' queries go through LDS: read once and whole for the four
+  // wavefronts, which all need all of them (read by each from memory: 55 us
+  // instead of 42 for 8192 tokens of 32 heads)
   u32x4 q[RT][D / 32];
   if (seen > 0) {
+    constexpr int kLanes = D / 8;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = t * 16 + (lane & 15), tl = row / p.group;
-      const bool ok = tl < tokens;
-      const char* from = static_cast<const char*>(p.q) +
-          ((at.first + (ok ? tl : 0)) * p.q_t + (hk * p.group + row % p.group) * p.q_h + kg * 8) * 2;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) q[t][i] = ok ? *reinterpret_cast<const u32x4*>(from + i * 64) : u32x4{0, 0, 0, 0};
+    for (int e = threadIdx.x; e < RT * 16 * kLanes; e += 256) {
+      const int row = e / kLanes, tl = row / p.group;
+      u32x4 x = {0, 0, 0, 0};
+      if (tl < tokens)
+        x = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) +
+            ((at.first + tl) * p.q_t + (hk * p.group + row % p.group) * p.q_h + (e % kLanes) * 8) * 2);
+      *reinterpret_cast<u32x4*>(s_q + tile_at<D>(row, e % kLanes)) = x;
     }
+    __syncthreads();
+    const uint32_t from = lds_offset(s_q) + tile_at<D>(lane & 15, kg);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) q[t][i] = lds_read16((from ^ (i * 64)) + t * 32 * D);
   }
   float* best = s_best[wave];
   const int end = min(p.max_blocks, (static_cast<int>(blockIdx.y) + 1) * p.chunk);
