@@ -23,6 +23,8 @@
  *   out[t][h] = sum_j p_j v_j,  p_j = exp(scale q.k_j - lse),
  *   lse[t][h] = log sum_j exp(scale q.k_j)     over the visible keys j.
  *
+ * Infinities and NaN count where they are visible and nowhere else (the
+ * workgroups that meet any go over their keys a second time, one by one).
  * A query without visible keys, and a row behind the last sequence, has out 0
  * and lse -inf, and its gradient is 0.  Keys that no query sees, and keys
  * behind the last sequence, have gradient 0.
@@ -80,7 +82,7 @@ int block_means(int32_t dtype, const void* k, int64_t k_stride_t, int64_t k_stri
  * position up to the query's; counts[t][c] is the number of those.  The first
  * `first` of them and the last `last` of them are forced: their score is +inf.
  * Scores from counts[t][c] on are -inf.  Rows of queries without blocks, and
- * rows behind the last sequence, are -inf with count 0. 
+ * rows behind the last sequence, are -inf with count 0.  A NaN among a
  * block's products makes its score NaN.
  *
  * The means are those of block_means() (block_table NULL; cu_k as there), or

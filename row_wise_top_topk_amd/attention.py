@@ -385,11 +385,14 @@ class _BlockAttention(torch.autograd.Function):
         ctx.save_for_backward(q, k, v, out, rest, lse, blocks, cu_seqlens, cu_seqlens_k)
         ctx.rest = (block_size, scale, causal)
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
         return out, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout, _):
+        if dout is None:
+            return (None,) * 9
         q, k, v, out, rest, lse, blocks, cu_q, cu_k = ctx.saved_tensors
         block_size, scale, causal = ctx.rest
         if dout.stride(2) != 1 or dout.data_ptr() % 16 or any(dout.stride(i) % 8 for i in (0, 1)):

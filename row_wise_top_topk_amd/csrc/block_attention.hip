@@ -26,6 +26,103 @@ struct Shared {
   Select sel;
 };
 
+// A row's output, divided by the sum of its weights: lane half `half` has the
+// columns 32 i + 8 (r / 4) + 4 half + r % 4 in acc[i][r].
+template <typename T, int D, bool kRest>
+__device__ __forceinline__ void store_row(const Args& p, int64_t tok, int head, int half, const f32x16 (&acc)[D / 32], float m, float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t to_at = (tok * p.heads + head) * (2 * D) + half * 8;
+  char* to = static_cast<char*>(p.out) + to_at;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      u32x2 w;
+      w[0] = T::pack(acc[i][r] * inv, acc[i][r + 1] * inv);
+      w[1] = T::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv);
+      *reinterpret_cast<u32x2*>(to + i * 64 + (r >> 2) * 16) = w;
+      if constexpr (kRest) {
+        u32x2 z;
+        z[0] = T::pack(acc[i][r] * inv - T::lo(w[0]), acc[i][r + 1] * inv - T::hi(w[0]));
+        z[1] = T::pack(acc[i][r + 2] * inv - T::lo(w[1]), acc[i][r + 3] * inv - T::hi(w[1]));
+        *reinterpret_cast<u32x2*>(static_cast<char*>(p.rest) + to_at + i * 64 + (r >> 2) * 16) = z;
+      }
+    }
+  if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : (m == kInf ? kInf : m * p.scale + __logf(sum));
+}
+
+// The rows of the workgroup once more, key by key, with what a row does not see
+// left out of its arithmetic: for the rare workgroup whose results are not
+// finite.
+template <typename T, int D, bool kRest>
+__device__ __forceinline__ void one_by_one(const Args& p, Select& sel) {
+  const int hk = blockIdx.x % p.kv_heads;
+  const int64_t slot = p.slots - 1 - static_cast<int64_t>(blockIdx.x / p.kv_heads);
+  const int tq = p.tokens_per;
+  const Group g = group_of(p, slot, tq);
+  const int lane = threadIdx.x & 63, half = lane >> 5, row = (threadIdx.x >> 6) * 32 + (lane & 31);
+  const int tl = row / p.group, head = hk * p.group + row % p.group;
+  const bool valid = tl < g.tokens;
+  const int64_t tok = g.t0 + (valid ? tl : 0), pos = tok - g.begin + g.shift;
+  const int64_t limit = p.causal && pos < g.len_k ? pos : g.len_k - 1;
+  const char* q = static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h) * 2 + half * 16;
+  const char* kbase = static_cast<const char*>(p.k) + (g.tk0 * p.k_t + hk * p.k_h) * 2 + half * 16;
+  const char* vbase = static_cast<const char*>(p.v) + (g.tk0 * p.v_t + hk * p.v_h) * 2 + half * 8;
+  const float c = p.scale * kLog2e;
+  f32x16 acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+  float m = -kInf, sum = 0.f;
+  const int nw = (tq + 31) >> 5, width = kMaskWords / nw, word = tl >> 5 < nw ? tl >> 5 : 0;
+  for (int w0 = 0; w0 < g.blocks; w0 += width) {
+    const int active = list_window(p, g, hk, w0, width, nw, sel);
+    for (int e = 0; e < active; ++e) {
+      const int id = sel.list[e];
+      const bool mine = valid && ((sel.mask[id * nw + word] >> (tl & 31)) & 1u);
+      if (!__any(mine)) continue;
+      const int from = (w0 + id) << p.lb, to = min(from + p.bs, g.len_k);
+      for (int key = from; key < to; ++key) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const u32x4 a = *reinterpret_cast<const u32x4*>(kbase + key * (p.k_t * 2) + i * 32), b = *reinterpret_cast<const u32x4*>(q + i * 32);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x = fmaf(T::hi(a[z]), T::hi(b[z]), fmaf(T::lo(a[z]), T::lo(b[z]), x));
+        }
+        x = half_sum(x);
+        if (mine && key <= limit) {
+          const float now = fmaxf(m, x), shift = now == -kInf ? 0.f : now;
+          const float shrink = now == m ? 1.f : exp2_fast((m - now) * c), w = exp2_fast((x - shift) * c);
+          m = now;
+          sum = sum * shrink + w;
+          const char* vr = vbase + key * (p.v_t * 2);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const u32x2 v = *reinterpret_cast<const u32x2*>(vr + i * 64 + (r >> 2) * 16);
+              acc[i][r] = fmaf(w, T::lo(v[0]), acc[i][r] * shrink);
+              acc[i][r + 1] = fmaf(w, T::hi(v[0]), acc[i][r + 1] * shrink);
+              acc[i][r + 2] = fmaf(w, T::lo(v[1]), acc[i][r + 2] * shrink);
+              acc[i][r + 3] = fmaf(w, T::hi(v[1]), acc[i][r + 3] * shrink);
+            }
+        }
+      }
+    }
+  }
+  if (valid) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
+}
+
+// Called, it costs a short call nothing (inline: 20 us instead of 18 for 517
+// tokens); with kRest the call's registers are missed in the loop, so there it
+// is inline (440 us and 360 for 8192 tokens).
+template <typename T, int D>
+__device__ __noinline__ void one_by_one_called(const Args* args, Select* sel) {
+  one_by_one<T, D, false>(*args, *sel);
+}
+
 // With kRest the weights of the second product have two terms (16 bits of 24)
 // and the part of out that its own rounding leaves out is stored too: the
 // gradient subtracts dout . out from terms that it nearly cancels.
@@ -236,26 +333,19 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
     }
   }
   sum = half_sum(sum);
-  if (!valid) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t to_at = (tok * p.heads + head) * (2 * D) + half * 8;
-  char* to = static_cast<char*>(p.out) + to_at;
+  // An infinity or NaN that a row does not see can have come in through the
+  // products, as 0 times it
+  bool odd = !(fabsf(sum) < kInf);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      u32x2 w;
-      w[0] = T::pack(acc[i][r] * inv, acc[i][r + 1] * inv);
-      w[1] = T::pack(acc[i][r + 2] * inv, acc[i][r + 3] * inv);
-      *reinterpret_cast<u32x2*>(to + i * 64 + (r >> 2) * 16) = w;
-      if constexpr (kRest) {
-        u32x2 z;
-        z[0] = T::pack(acc[i][r] * inv - T::lo(w[0]), acc[i][r + 1] * inv - T::hi(w[0]));
-        z[1] = T::pack(acc[i][r + 2] * inv - T::lo(w[1]), acc[i][r + 3] * inv - T::hi(w[1]));
-        *reinterpret_cast<u32x2*>(static_cast<char*>(p.rest) + to_at + i * 64 + (r >> 2) * 16) = z;
-      }
-    }
-  if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : m * p.scale + __logf(sum);
+    for (int r = 0; r < 16; ++r) odd |= !(fabsf(acc[i][r]) < kInf);
+  if (__syncthreads_or(valid && odd)) {
+    if constexpr (kRest) one_by_one<T, D, kRest>(p, sh.sel);
+    else one_by_one_called<T, D>((const Args*)__builtin_amdgcn_kernarg_segment_ptr(), &sh.sel);
+    return;
+  }
+  if (valid) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
 }
 
 template <typename T, int D>

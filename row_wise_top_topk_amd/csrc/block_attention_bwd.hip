@@ -234,6 +234,58 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
       if (tile + 1 < tiles) step(Int<1>{}, tile + 1);
     }
   }
+  // as in the forward: what a row does not see must not reach it as 0 times an
+  // infinity or NaN
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) odd |= !(fabsf(acc[i][r]) < kInf);
+  if (__syncthreads_or(valid && odd)) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    for (int w0 = 0; w0 < g.blocks; w0 += width) {
+      const int active = list_window(p, g, hk, w0, width, nw, sh.sel);
+      const int word = tl >> 5 < nw ? tl >> 5 : 0;
+      for (int e = 0; e < active; ++e) {
+        const int id = __builtin_amdgcn_readfirstlane(sh.sel.list[e]);
+        const bool mine = valid && ((sh.sel.mask[id * nw + word] >> (tl & 31)) & 1u);
+        if (!__any(mine)) continue;
+        const int from = (w0 + id) << p.lb, to = min(from + p.bs, g.len_k);
+        for (int key = from; key < to; ++key) {
+          const char* kr = kbase + key * (p.k_t * 2);
+          const char* vr = vbase + key * (p.v_t * 2);
+          float x = 0.f, y = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const u32x4 kv = *reinterpret_cast<const u32x4*>(kr + half * 16 + i * 32), vv = *reinterpret_cast<const u32x4*>(vr + half * 16 + i * 32);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              x = fmaf(T::hi(kv[z]), T::hi(q[i][z]), fmaf(T::lo(kv[z]), T::lo(q[i][z]), x));
+              y = fmaf(T::hi(vv[z]), T::hi(go[i][z]), fmaf(T::lo(vv[z]), T::lo(go[i][z]), y));
+            }
+          }
+          x = half_sum(x);
+          y = half_sum(y);
+          if (mine && key <= limit) {
+            const float w = exp2_fast(fmaf(x, c, -lse2)) * (y - delta);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+              for (int r = 0; r < 16; r += 4) {
+                const u32x2 kv = *reinterpret_cast<const u32x2*>(kr + half * 8 + i * 64 + (r >> 2) * 16);
+                acc[i][r] = fmaf(w, T::lo(kv[0]), acc[i][r]);
+                acc[i][r + 1] = fmaf(w, T::hi(kv[0]), acc[i][r + 1]);
+                acc[i][r + 2] = fmaf(w, T::lo(kv[1]), acc[i][r + 2]);
+                acc[i][r + 3] = fmaf(w, T::hi(kv[1]), acc[i][r + 3]);
+              }
+          }
+        }
+      }
+    }
+  }
   if (!valid) return;
   char* to = static_cast<char*>(p.dq) + (tok * p.heads + head) * (2 * D) + half * 8;
 #pragma unroll
@@ -503,6 +555,55 @@ __global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b)
         dk[i] = T::mfma16(sw, rd.column(qs, first, i), dk[i]);
       }
       read_ahead<D / 8, 4, 2>();
+    }
+  }
+
+  // as in the forward: a row that does not see a key must not reach it as 0 times
+  // an infinity or NaN
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) odd |= !(fabsf(dk[i][r]) < kInf) || !(fabsf(dv[i][r]) < kInf);
+  if (__syncthreads_or(odd)) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) dk[i] = dv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = rwv; r < total; r += RW) {
+      int head;
+      const int64_t tok = token_of(r, head);
+      const char* qr = static_cast<const char*>(p.q) + (tok * p.q_t + head * p.q_h) * 2;
+      const char* gr = static_cast<const char*>(p.dout) + (tok * p.do_t + head * p.do_h) * 2;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const u32x4 qv = *reinterpret_cast<const u32x4*>(qr + quad * 16 + i * 64), gv = *reinterpret_cast<const u32x4*>(gr + quad * 16 + i * 64);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          x = fmaf(T::hi(kf[i][z]), T::hi(qv[z]), fmaf(T::lo(kf[i][z]), T::lo(qv[z]), x));
+          y = fmaf(T::hi(vf[i][z]), T::hi(gv[z]), fmaf(T::lo(vf[i][z]), T::lo(gv[z]), y));
+        }
+      }
+      x = quad_sum(x);
+      y = quad_sum(y);
+      const int64_t at_row = tok * p.heads + head;
+      const float l = p.lse[at_row];
+      const int64_t pos = p.causal ? tok + shift : INT32_MAX;
+      const bool sees = haskey && keypos <= pos && l != -kInf;
+      const float pr = sees ? exp2_fast(fmaf(x, c, -l * kLog2e)) : 0.f;
+      const float ds = sees ? pr * (y - b.delta[at_row]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int from = 4 * quad + j;  // the lane that has key 4 quad + j
+        const bool seen = __shfl(static_cast<int>(sees), from) != 0;
+        const float pj = __shfl(pr, from), dj = __shfl(ds, from);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const float gx = T::lo(reinterpret_cast<const uint16_t*>(gr)[i * 16 + (lane & 15)]);
+          const float qx = T::lo(reinterpret_cast<const uint16_t*>(qr)[i * 16 + (lane & 15)]);
+          dv[i][j] = seen ? fmaf(pj, gx, dv[i][j]) : dv[i][j];
+          dk[i][j] = seen ? fmaf(dj, qx, dk[i][j]) : dk[i][j];
+        }
+      }
     }
   }
 

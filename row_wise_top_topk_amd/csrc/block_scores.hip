@@ -106,13 +106,28 @@ __device__ __forceinline__ void split2(const float* x, u32x4* t) {
   }
 }
 
+// The best score of a group's heads, product by product: the terms of an
+// infinity have a NaN among them, so where the sum of them is one it is none of
+// theirs yet.
+template <typename T, int D>
+__device__ __noinline__ float best_again(const ScoreArgs& p, const float* mean, const char* q) {
+  float s = -kInf;
+  for (int g = 0; g < p.group && s == s; ++g) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(q + g * p.q_h * 2);
+    float x = 0.f;
+    for (int d = 0; d < D / 2; ++d) x = fmaf(T::hi(w[d]), mean[2 * d + 1], fmaf(T::lo(w[d]), mean[2 * d], x));
+    s = x > s || x != x ? x : s;
+  }
+  return s;
+}
+
 // A workgroup takes RT * 16 rows (the group's heads of consecutive tokens) of
 // one key head and `chunk` blocks, a wavefront 16 blocks at a time: the queries
 // stay in registers, the means go from memory to registers and are split
 // there, once for all RT row tiles.  The maximum over the heads crosses lanes
 // through LDS, since a group need not divide a tile.
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
+__global__ void __launch_bounds__(256, RT == 8 ? 2 : 4) block_scores_kernel(ScoreArgs p) {
   constexpr bool kHalf = __is_same(T, Fp16);
   constexpr int kPad = 20;
   __shared__ __attribute__((aligned(16))) float s_best[4][RT * 16 * kPad];
@@ -252,6 +267,11 @@ __global__ void __launch_bounds__(256) block_scores_kernel(ScoreArgs p) {
           for (int g = 1; g < p.group; ++g) {
             const float x = from[g * kPad];
             s = x > s || x != x ? x : s;
+          }
+          if (__any(s != s) && s != s) {
+            const int64_t row = p.table == nullptr ? base + b : p.table[at.seq * p.table_stride + b];
+            s = best_again<T, D>(p, p.means + (row * p.kv_heads + hk) * D,
+                                 static_cast<const char*>(p.q) + ((at.first + tl) * p.q_t + hk * p.group * p.q_h) * 2);
           }
           s *= p.scale;
         }

@@ -217,6 +217,9 @@ __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attentio
   }
 #pragma unroll
   for (int d = 1; d < 16; d <<= 1) least = min(least, __shfl_xor(least, d));
+  bool odd = false;  // NaNs of V were left out
+  // the last key that any row sees
+  const int most = static_cast<int>(rw.pos + rw.tokens - 1 < rw.len ? rw.pos + rw.tokens - 1 : rw.len - 1);
 
   f32x4 acc[MT][D / 16];
   float m[MT], sum[MT];
@@ -291,13 +294,24 @@ __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attentio
         iv[h] = 1.f / vs;
       }
       const bool whole = max(key[0], key[1]) + 15 <= least;
-      // V to LDS; codes behind the sequence's end (never written, or of a page
-      // that is not there) are set to 0
+      // V to LDS; codes that no row sees (behind the last token, never written,
+      // or of a page that is not there) are set to 0, and so are NaNs that only
+      // some rows see: 0 times them would reach the others
 #pragma unroll
       for (int i = 0; i < kLoadsV; ++i) {
         const int row = i * (64 / kLanesV) + lane / kLanesV;
         u32x4 w = x.v[i];
-        if (!whole && (row < 16 ? key[0] : key[1]) + (row & 15) >= rw.len) w = u32x4{0, 0, 0, 0};
+        if (!whole) {
+          const int at = (row < 16 ? key[0] : key[1]) + (row & 15);
+          if (at > most) w = u32x4{0, 0, 0, 0};
+          if (rw.tokens > 1 && at > rw.pos)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t nan = ((w[z] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              w[z] &= ~((nan >> 7) * 0xffu);
+              odd |= nan != 0;
+            }
+        }
         *reinterpret_cast<u32x4*>(vt + v_at<D>(row, lane % kLanesV)) = w;
       }
       f32x4 s[MT][2];
@@ -372,6 +386,24 @@ __global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attentio
     }
   }
 
+  // NaNs of V among the new tokens' keys that were left out: to the rows that see them
+  if (rw.tokens > 1 && __syncthreads_or(odd) && wave == 0) {
+    const int64_t to = min(static_cast<int64_t>(most), (static_cast<int64_t>(e1) << p.lb) - 1);
+    for (int64_t key = max(max(rw.pos + 1, int64_t{0}), static_cast<int64_t>(e0) << p.lb); key <= to; ++key) {
+      const int64_t pg = p.table[rw.seq * p.table_stride + (key >> p.lb)];
+      if (pg < 0 || pg >= p.num_pages) continue;
+      const uint8_t* from = p.v + (((pg * p.kv_heads + rw.hk) << p.lb) + (key & (p.bs - 1))) * D + 4 * g;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(from + i * 16);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (key <= limit[t] && ((w >> (8 * r)) & 0x7fu) == 0x7fu) acc[t][i][r] = __builtin_nanf("");
+      }
+    }
+  }
   // Join the wavefronts: rows' maxima and sums, then 16 rows at a time.
   __syncthreads();
 #pragma unroll
