@@ -44,8 +44,8 @@ extern "C" {
  * tokens the scale can only grow: if the new tokens need a larger one, the
  * codes that are there are rounded again under it; a scale that is no power of
  * two grows to the next one.  Infinite values become
- * +-448 * scale, NaN stays NaN.  No two sequences of a call may store into one
- * page.
+ * +-448 * scale, NaN stays NaN.  A call may store into a page
+ * through one entry of one sequence's row only.
  *
  * k_mean (NULL, or fp32 [num_pages, HK, D]) receives, for each page that got
  * new tokens, the mean of the keys that the page holds then, as their codes

@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import weakref
 
 import torch
 
@@ -331,7 +332,9 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     query that sees no key, and a row behind the last sequence, has 0 and -inf.
 
     Differentiable in q, k and v through autograd (``lse`` is not; ``out=`` and
-    ``rest=`` are refused then).  A caller of ``block_attention_backward`` gives
+    ``rest=`` are refused then).  A graph can capture the call with its backward;
+    an eager gradient graph of the same leaves that is still alive is refused
+    then (any operation's such graph ends a capture; this one sees its own).  A caller of ``block_attention_backward`` gives
     ``rest`` (like ``out``), which receives what the rounding of ``out`` leaves
     out."""
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
@@ -377,9 +380,29 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     return dq, dk, dv
 
 
+_graphs = weakref.WeakSet()  # the calls whose gradient graphs are alive
+
+
+def _check_capture(leaves, stream: int) -> None:
+    """Refuses a call under capture whose leaves have a gradient graph of another
+    stream.  A leaf's gradients are summed on the stream of its first living
+    graph: the backward would pull that stream into the capture, which ends the
+    process."""
+    for ctx in list(_graphs):
+        if ctx.stream != stream and any(x() is y() for x in ctx.leaves for y in leaves):
+            raise RuntimeError("block_attention cannot be captured while a gradient graph of the same leaves, made on another "
+                               "stream, is alive: drop that graph's results first")
+
+
 class _BlockAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
+        ctx.leaves = [weakref.ref(t) for t in (q, k, v) if t.requires_grad and t.is_leaf]
+        if ctx.leaves and q.is_cuda:
+            ctx.stream = _raw_stream(q.device.index)
+            if torch.cuda.is_current_stream_capturing():
+                _check_capture(ctx.leaves, ctx.stream)
+            _graphs.add(ctx)
         rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal, rest=rest)
         ctx.save_for_backward(q, k, v, out, rest, lse, blocks, cu_seqlens, cu_seqlens_k)
@@ -443,8 +466,8 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache:
     A page's scale is the smallest power of two that brings what it holds to
     448 or less; it grows when a token needs it (the codes that are there are
     rounded again) and starts anew in a page whose first token is stored.
-    Pages outside the cache store nothing; no two sequences may store into one
-    page.  ``k_mean`` (float32 ``[pages, kv_heads, dim]``) receives the mean of
+    Pages outside the cache store nothing; a call may store into a page through
+    one entry of one sequence's row only.  ``k_mean`` (float32 ``[pages, kv_heads, dim]``) receives the mean of
     the keys of each page that got tokens: the ``means`` of ``block_scores``."""
     a = _AppendArgs()
     total, hk, dim, a.k_stride_t, a.k_stride_h = _heads(k, "k")

@@ -208,7 +208,7 @@ MI_ATTN_EXPORT int kv8_append(const mi_kv8_append_args* a, hipStream_t stream) {
   if (a == nullptr) return MI_ATTN_EINVAL;
   if ((a->dtype != MI_ATTN_BF16 && a->dtype != MI_ATTN_FP16) || (a->dim != 64 && a->dim != 128) ||
       (a->block_size != 16 && a->block_size != 32 && a->block_size != 64 && a->block_size != 128) || a->kv_heads < 1 ||
-      a->total < 0 || a->total > INT32_MAX || a->num_pages < 0 || a->num_seqs < 0 || a->block_table_cols < 0 ||
+      a->total < 0 || a->total > INT32_MAX || a->num_pages < 0 || a->num_pages > INT32_MAX || a->num_seqs < 0 || a->block_table_cols < 0 ||
       a->block_table_stride < a->block_table_cols || (a->cu == nullptr && a->total != a->num_seqs))
     return MI_ATTN_EINVAL;
   const int64_t strides[] = {a->k_stride_t, a->k_stride_h, a->v_stride_t, a->v_stride_h};
