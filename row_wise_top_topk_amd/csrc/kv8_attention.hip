@@ -173,8 +173,11 @@ __device__ __forceinline__ int list_selected(const DecodeArgs& p, const Rows& r,
   return base;
 }
 
+// Four tiles of rows with 128 columns need more than 256 registers: one
+// wavefront a SIMD there (16 sequences of 16000 keys, 64/4 heads, 4 tokens: 150
+// us, with two 346; with 64 columns two are better, 62 and 91).
 template <typename T, int D, int MT>
-__global__ void __launch_bounds__(256, MT == 4 || D == 128 ? 2 : 3) kv8_attention_kernel(DecodeArgs p) {
+__global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ? 2 : 3)) kv8_attention_kernel(DecodeArgs p) {
   constexpr int R = MT * 16;
   __shared__ __attribute__((aligned(16))) DecodeShared<D> sh;
   const int64_t item = static_cast<int>(blockIdx.x / p.splits);
