@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs p) {
   const char* x = static_cast<const char*>(p.x[side]) + ((from + first - start) * p.x_t[side] + hk * p.x_h[side] + chunk * 8) * 2;
   float* scale_at = p.scale[side] + page * p.kv_heads + hk;
   float old = *scale_at;  // read by all before the barrier, written by one behind it
+  const bool wants_mean = side == 0 && p.mean != nullptr;
+  uint8_t* cache = p.cache[side] + ((page * p.kv_heads + hk) * p.bs) * D + chunk * 8;
   u32x4 in[kSteps];
   float most = 0.f;
 #pragma unroll
@@ -125,15 +127,23 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs p) {
     const int row = row0 + s * kRowsPer;
     in[s] = u32x4{0, 0, 0, 0};
     if (row >= held && row < there) in[s] = *reinterpret_cast<const u32x4*>(x + row * p.x_t[side] * 2);
+    // the mean needs the codes that are there: on their way with the new rows
+    // rather than behind the barrier (11.1 us instead of 11.5 for 64 tokens)
+    if (row < held && wants_mean) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(cache + row * D);
+      in[s] = u32x4{w[0], w[1], 0, 0};
+    }
   }
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
+  for (int s = 0; s < kSteps; ++s) {
+    if (row0 + s * kRowsPer < held) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float a = fabsf(T::lo(in[s][e])), b = fabsf(T::hi(in[s][e]));
       most = fmaxf(most, a < kInf ? a : 0.f);
       most = fmaxf(most, b < kInf ? b : 0.f);
     }
+  }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
   if (lane == 0) s_most[wave] = most;
@@ -146,8 +156,6 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs p) {
   const uint32_t bits = __float_as_uint(old);
   scale = fmaxf(scale, __uint_as_float((bits + 0x7fffffu) & 0x7f800000u));
   const bool grows = scale > old;
-  const bool wants_mean = side == 0 && p.mean != nullptr;
-  uint8_t* cache = p.cache[side] + ((page * p.kv_heads + hk) * p.bs) * D + chunk * 8;
   const float inv = 1.f / scale, shrink = old / scale;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -165,7 +173,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append_kernel(AppendArgs p) {
       *at = w;
     } else {
       if (!grows && !wants_mean) continue;
-      w = *at;
+      w = wants_mean ? u32x2{in[s][0], in[s][1]} : *at;
       if (grows) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
