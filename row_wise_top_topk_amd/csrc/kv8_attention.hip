@@ -180,8 +180,12 @@ template <typename T, int D, int MT>
 __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ? 2 : 3)) kv8_attention_kernel(DecodeArgs p) {
   constexpr int R = MT * 16;
   __shared__ __attribute__((aligned(16))) DecodeShared<D> sh;
-  const int64_t item = static_cast<int>(blockIdx.x / p.splits);
-  const int split = blockIdx.x % p.splits;
+  // Consecutive workgroups go to the eight dies in turn.  The later chunks of a
+  // short sequence are empty: without the shift an even number of chunks would
+  // give a die the same ones of every sequence (64 sequences of 500 to 32000
+  // keys, 8 chunks: 413 us instead of 546, with the join).
+  const uint32_t item = blockIdx.x / p.splits;
+  const int split = static_cast<int>((blockIdx.x + item + (item >> 1) + (item >> 2)) % p.splits);
   const Rows rw = rows_of(p, item, R);
   if (rw.tokens == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ?
     // nothing to add; a selection's chunks are all looked at by the join
     if (p.blocks != nullptr)
       for (int row = tid; row < rw.tokens * rw.heads; row += 256) {
-        const int64_t at = (item * p.splits + split) * R + row;
+        const int64_t at = (static_cast<int64_t>(item) * p.splits + split) * R + row;
         p.part_ml[at * 2] = -kInf;
         p.part_ml[at * 2 + 1] = 0.f;
       }
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ?
         l += sh.ml[w][row][1] * (mm == -kInf ? 0.f : exp2_fast(sh.ml[w][row][0] - mm));
       }
       if (p.splits > 1) {
-        const int64_t at = (item * p.splits + split) * R + row;
+        const int64_t at = (static_cast<int64_t>(item) * p.splits + split) * R + row;
         *reinterpret_cast<f32x4*>(p.part + at * D + d) = o;
         if (d == 0) {
           p.part_ml[at * 2] = mm;
