@@ -142,7 +142,9 @@ __device__ __noinline__ void one_by_one_called(const Args* args, Select* sel) {
 // With kRest the weights of the second product have two terms (16 bits of 24)
 // and the part of out that its own rounding leaves out is stored too: the
 // gradient subtracts dout . out from terms that it nearly cancels.
-template <typename T, int D, bool kWide, bool kRest>
+// With kSplit, for few rows, a workgroup takes 64 rows and two wavefronts share
+// 32 of them: each works on 32 keys of every tile, and they are joined at the end.
+template <typename T, int D, bool kWide, bool kRest, bool kSplit>
 __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(Args p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Shared<T, D>& sh = *reinterpret_cast<Shared<T, D>*>(smem);
@@ -154,7 +156,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
   if (g.tokens == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5;
-  const int row = wave * 32 + (lane & 31);
+  const int rows32 = kSplit ? wave & 1 : wave, keys32 = kSplit ? wave >> 1 : 0;
+  constexpr int kParts = kSplit ? 1 : 2;  // 32-key parts of a tile that a wavefront takes
+  const int row = rows32 * 32 + (lane & 31);
   const int tl = row / p.group, head = hk * p.group + row % p.group;
   const bool valid = tl < g.tokens;
   const int64_t tok = g.t0 + (valid ? tl : 0);
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
 
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const Reads<D> rd(lds_offset(sh.k[0]));
+  const Reads<D> rd(lds_offset(sh.k[0]) + keys32 * (64 * D));
   constexpr int kBuf = kTile * 2 * D;  // from one buffer to the other; the values lie two behind the keys
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
@@ -202,7 +206,12 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
     Half<D> kin, vin;
     kin.load(kbase, p.k_t * 2, next, g.len_k);
     vin.load(vbase, p.v_t * 2, next, g.len_k);
-    Sight ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+    auto sight = [&](const Keys<kWide>& k) {
+      Sight v = sight_of(sh.sel, k, nw, word, tl & 31, limit, valid);
+      if constexpr (kSplit) v.from(keys32);
+      return v;
+    };
+    Sight ahead = sight(next);
     kin.store(sh.k[0]);
     vin.store(sh.v[0]);
     next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 1);
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       constexpr int buf = decltype(which)::value;
       const Sight see = ahead;
       auto look_ahead = [&] {
-        ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+        ahead = sight(next);
         next = after;
         after = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 3);
       };
@@ -226,15 +235,15 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
         look_ahead();
         return;
       }
-      f32x16 s[2];
+      f32x16 s[kParts];
       {
-        u32x4 ka[2][D / 16];
+        u32x4 ka[kParts][D / 16];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kParts; ++mt)
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) ka[mt][i] = rd.row(buf * kBuf, mt * 32, i);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < kParts; ++mt) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
 #pragma unroll
@@ -245,10 +254,12 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
         // reads of the first 32 keys, then a product and a read of the others in
         // turn, then a product and a write
         __builtin_amdgcn_sched_group_barrier(0x100, D / 16, 0);
+        if constexpr (!kSplit) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          for (int i = 0; i < D / 16; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       }
       if (see.partial) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kParts; ++mt)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int off = 8 * ((r >> 2) & 1) + (r & 3);
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       // a row sees all of a 16-key group, nothing of it, or what was just masked
       float top = -kInf;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2 * kParts; ++i) {
         float t = s[i >> 1][8 * (i & 1)];
 #pragma unroll
         for (int r = 1; r < 8; ++r) t = fmaxf(t, s[i >> 1][8 * (i & 1) + r]);
@@ -290,37 +301,35 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       kin.load(kbase, p.k_t * 2, after, g.len_k);
       vin.load(vbase, p.v_t * 2, after, g.len_k);
       const float base = m == -kInf ? 0.f : m * c;
-      u32x4 pr[4];
-      float sums[4];
+      u32x4 pr[2 * kParts];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2 * kParts; ++i) {
         const float from = sees<kWide>(see, i) ? base : kInf;
         float w[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) w[r] = exp2_fast(fmaf(s[i >> 1][8 * (i & 1) + r], c, -from));
 #pragma unroll
         for (int r = 0; r < 4; ++r) pr[i][r] = T::pack(w[2 * r], w[2 * r + 1]);
-        sums[i] = ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
         if constexpr (kRest) {
 #pragma unroll
           for (int r = 0; r < 8; ++r) s[i >> 1][8 * (i & 1) + r] = w[r];
         }
       }
-      sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
       {
-        u32x4 va[D / 32][4];
+        u32x4 va[D / 32][2 * kParts];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int st = 0; st < 4; ++st) va[i][st] = rd.column((2 + buf) * kBuf, 16 * st, i);
+          for (int st = 0; st < 2 * kParts; ++st) va[i][st] = rd.column((2 + buf) * kBuf, 16 * st, i);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
+          for (int st = 0; st < 2 * kParts; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
         if constexpr (kRest) {
           // the second terms read V again: its operands do not fit beside them
 #pragma unroll
-          for (int st = 0; st < 4; ++st) {
+          for (int st = 0; st < 2 * kParts; ++st) {
             u32x4 low;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -332,9 +341,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {  // the loads between the exponentials
             __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 128 / (D / 16), 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 64 * kParts / (D / 16), 0);
           }
-          read_ahead<D / 8, 4, 2>();
+          read_ahead<D / 16 * kParts, 4, 2>();
         }
       }
       look_ahead();
@@ -349,6 +358,30 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
     }
   }
   sum = half_sum(sum);
+  bool last = true;  // this wavefront has its rows' results
+  if constexpr (kSplit) {
+    last = keys32 == 0;
+    float* box = reinterpret_cast<float*>(smem) + rows32 * 64 + lane;
+    if (!last) {
+      box[0] = m;
+      box[128] = sum;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) box[(2 + i * 16 + r) * 128] = acc[i][r];
+    }
+    __syncthreads();
+    if (last) {
+      const float other = box[0], top = fmaxf(m, other);
+      const float f = m == -kInf ? 0.f : exp2_fast((m - top) * c), fo = other == -kInf ? 0.f : exp2_fast((other - top) * c);
+      m = top;
+      sum = sum * f + box[128] * fo;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] = acc[i][r] * f + box[(2 + i * 16 + r) * 128] * fo;
+    }
+  }
   // An infinity or NaN that a row does not see can have come in through the
   // products, as 0 times it
   bool odd = !(fabsf(sum) < kInf);
@@ -356,28 +389,34 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) odd |= !(fabsf(acc[i][r]) < kInf);
-  if (__syncthreads_or(valid && odd)) {
+  if (__syncthreads_or(valid && last && odd)) {
     if constexpr (kRest) one_by_one<T, D, kRest>(p, sh.sel);
     else one_by_one_called<T, D>((const Args*)__builtin_amdgcn_kernarg_segment_ptr(), &sh.sel);
     return;
   }
-  if (valid) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
+  if (valid && last) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
 }
 
-template <typename T, int D>
-int launch(const Args& p, hipStream_t stream) {
+template <typename T, int D, bool kSplit>
+int launch_as(const Args& p, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads;
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
   const dim3 g(static_cast<unsigned>(grid)), b(256);
   const size_t lds = sizeof(Shared<T, D>);
   if (p.lb >= 6) {
-    if (p.rest != nullptr) block_attention_kernel<T, D, true, true><<<g, b, lds, stream>>>(p);
-    else block_attention_kernel<T, D, true, false><<<g, b, lds, stream>>>(p);
+    if (p.rest != nullptr) block_attention_kernel<T, D, true, true, kSplit><<<g, b, lds, stream>>>(p);
+    else block_attention_kernel<T, D, true, false, kSplit><<<g, b, lds, stream>>>(p);
   } else {
-    if (p.rest != nullptr) block_attention_kernel<T, D, false, true><<<g, b, lds, stream>>>(p);
-    else block_attention_kernel<T, D, false, false><<<g, b, lds, stream>>>(p);
+    if (p.rest != nullptr) block_attention_kernel<T, D, false, true, kSplit><<<g, b, lds, stream>>>(p);
+    else block_attention_kernel<T, D, false, false, kSplit><<<g, b, lds, stream>>>(p);
   }
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
+}
+
+template <typename T, int D>
+int launch(const Args& p, hipStream_t stream) {
+  Args few = p;
+  return split_rows(few, D) ? launch_as<T, D, true>(few, stream) : launch_as<T, D, false>(p, stream);
 }
 
 }  // namespace

@@ -35,6 +35,23 @@ struct Args {
 
 int make_args(const mi_block_attention_args* a, Args& p);
 
+// Few rows: 64 of them a workgroup instead of 128 are better where the card's 256
+// compute units would get one workgroup each, or a little more.  There are twice
+// as many, the union of their blocks is smaller and two wavefronts share a tile's
+// keys; but each key is copied more often, the less neighbouring tokens differ
+// (many heads a group: few tokens) the more in vain.  Measured, 128 rows against
+// 64, with n workgroups of 128 (us): 8 heads a group, 128 columns: n 128: 29, 26;
+// 256: 52, 47; 376: 75, 69; 4 heads, 752: 189, 231; one head, 376: 141, 122; 512:
+// 200, 221.  64 columns, 4 heads: 256: 75, 53; 540: 70, 62; 750: 154, 151.  16
+// heads: 188: 43, 44; 256: 61, 73.
+inline bool split_rows(Args& p, int dim) {
+  const int64_t most = p.group > 8 ? 192 : (dim == 64 ? 640 : 384);
+  if (p.slots * p.kv_heads > most || p.group > 64) return false;
+  p.tokens_per = 64 / p.group;
+  p.slots = slots_of(p.total_q, p.num_seqs, p.tokens_per);
+  return true;
+}
+
 constexpr int kRows = 128;        // rows of a workgroup: 32 for each of four wavefronts
 constexpr int kThreads = 256;
 constexpr int kTile = 64;         // keys of a tile
@@ -225,6 +242,12 @@ struct Sight {
   int32_t last[4];
   bool any;      // some row of the wavefront sees something
   bool partial;  // some row sees a part of a group only
+
+  // for a wavefront that takes the 32 keys from 32 * part on only
+  __device__ __forceinline__ void from(int part) {
+    last[0] = part != 0 ? last[2] : last[0];
+    last[1] = part != 0 ? last[3] : last[1];
+  }
 };
 
 template <bool kWide>

@@ -73,7 +73,8 @@ struct QShared {
   Select sel;
 };
 
-template <typename T, int D, bool kWide>
+// kSplit as in the forward: two wavefronts share 32 rows and take 32 keys of a tile each
+template <typename T, int D, bool kWide, bool kSplit>
 __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   QShared<T, D>& sh = *reinterpret_cast<QShared<T, D>*>(smem);
@@ -85,7 +86,9 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   if (g.tokens == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5;
-  const int row = wave * 32 + (lane & 31);
+  const int rows32 = kSplit ? wave & 1 : wave, keys32 = kSplit ? wave >> 1 : 0;
+  const bool last = keys32 == 0;  // this wavefront stores its rows' results
+  const int row = rows32 * 32 + (lane & 31);
   const int tl = row / p.group, head = hk * p.group + row % p.group;
   const bool valid = tl < g.tokens;
   const int64_t tok = g.t0 + (valid ? tl : 0);
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
     if (valid) {
       const float l = p.lse[tok * p.heads + head];
       lse2 = l == -kInf ? kInf : l * kLog2e;
-      if (half == 0) b.delta[tok * p.heads + head] = delta;
+      if (half == 0 && last) b.delta[tok * p.heads + head] = delta;
     }
   }
   const char* kbase = static_cast<const char*>(p.k) + (g.tk0 * p.k_t + hk * p.k_h) * 2;
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   const float c = p.scale * kLog2e;
   const int nw = (tq + 31) >> 5;
   const int width = kMaskWords / nw;
-  const Reads<D> rd(lds_offset(sh.k[0]));
+  const Reads<D> rd(lds_offset(sh.k[0]) + keys32 * (64 * D));
   constexpr int kBuf = kTile * 2 * D;  // from one buffer to the other; the values lie two behind the keys
 
   for (int w0 = 0; w0 < g.blocks; w0 += width) {
@@ -156,7 +159,12 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
     kin.load(kbase, p.k_t * 2, next, g.len_k);
     vin.load(vbase, p.v_t * 2, next, g.len_k);
     const int word = tl >> 5 < nw ? tl >> 5 : 0;
-    Sight ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+    auto sight = [&](const Keys<kWide>& k) {
+      Sight v = sight_of(sh.sel, k, nw, word, tl & 31, limit, valid);
+      if constexpr (kSplit) v.from(keys32);
+      return v;
+    };
+    Sight ahead = sight(next);
     next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, 1);
     auto step = [&](auto which, int tile) {
       constexpr int buf = decltype(which)::value;
@@ -167,12 +175,12 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
       if (tile + 1 < tiles) {
         kin.load(kbase, p.k_t * 2, next, g.len_k);
         vin.load(vbase, p.v_t * 2, next, g.len_k);
-        ahead = sight_of(sh.sel, next, nw, word, tl & 31, limit, valid);
+        ahead = sight(next);
         next = keys_of<kWide>(sh.sel, p.lb, p.bs, w0, active, tile + 2);
       }
       if (!see.any) return;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < (kSplit ? 1 : 2); ++mt) {
         f32x16 s, dp;
         {
           u32x4 ka[D / 16], va[D / 16];
@@ -241,6 +249,21 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
       if (tile + 1 < tiles) step(Int<1>{}, tile + 1);
     }
   }
+  if constexpr (kSplit) {
+    __syncthreads();
+    float* box = reinterpret_cast<float*>(smem) + rows32 * 64 + lane;
+    if (!last)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) box[(i * 16 + r) * 128] = acc[i][r];
+    __syncthreads();
+    if (last)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][r] += box[(i * 16 + r) * 128];
+  }
   // as in the forward: what a row does not see must not reach it as 0 times an
   // infinity or NaN
   bool odd = false;
@@ -248,7 +271,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) odd |= !(fabsf(acc[i][r]) < kInf);
-  if (__syncthreads_or(valid && odd)) {
+  if (__syncthreads_or(valid && last && odd)) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -293,7 +316,7 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
       }
     }
   }
-  if (!valid) return;
+  if (!valid || !last) return;
   char* to = static_cast<char*>(p.dq) + (tok * p.heads + head) * (2 * D) + half * 8;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -698,6 +721,13 @@ int launch_dkv(const BackArgs& b, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
+template <typename T, int D, bool kSplit>
+void launch_dq(const BackArgs& b, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(b.a.slots * b.a.kv_heads));
+  if (b.a.lb >= 6) block_attention_dq_kernel<T, D, true, kSplit><<<grid, dim3(256), sizeof(QShared<T, D>), stream>>>(b);
+  else block_attention_dq_kernel<T, D, false, kSplit><<<grid, dim3(256), sizeof(QShared<T, D>), stream>>>(b);
+}
+
 template <typename T, int D>
 int launch_backward(const BackArgs& b, hipStream_t stream) {
   const Args& p = b.a;
@@ -709,8 +739,9 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   if (words > 0)
     clear_bits_kernel<<<dim3(static_cast<unsigned>(words / 1024 + 1 < 4096 ? words / 1024 + 1 : 4096)), dim3(256), 0, stream>>>(b);
   if (pairs > 0) {
-    if (p.lb >= 6) block_attention_dq_kernel<T, D, true><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
-    else block_attention_dq_kernel<T, D, false><<<dim3(static_cast<unsigned>(grid)), dim3(256), sizeof(QShared<T, D>), stream>>>(b);
+    BackArgs few = b;
+    if (split_rows(few.a, D)) launch_dq<T, D, true>(few, stream);
+    else launch_dq<T, D, false>(b, stream);
   }
   if (p.total_k == 0) return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
   count_bits_kernel<<<dim3(static_cast<unsigned>((entries + 3) / 4)), dim3(256), 0, stream>>>(b);
