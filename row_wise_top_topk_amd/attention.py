@@ -203,6 +203,11 @@ def _output(out, shape, dtype, device, what: str):
     return out
 
 
+def _like(t):
+    """A contiguous tensor of t's shape and type (the quickest way to one)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -280,8 +285,8 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
         cu_q, cu_k, n = _sequences(cu_seqlens, cu_seqlens if cu_seqlens_k is None else cu_seqlens_k, device, total, total)
         if cu_q is None and means.shape[0] < total // bs + 1:
             raise ValueError("means must have a row for every block, as block_means gives them")
-    scores = torch.empty((total, hk, max_blocks), dtype=torch.float32, device=device)
-    counts = torch.empty((total, hk), dtype=torch.int32, device=device)
+    scores = means.new_empty((total, hk, max_blocks))
+    counts = means.new_empty((total, hk), dtype=torch.int32)
     a.q, a.means, a.cu_q, a.cu_k = q.data_ptr(), means.data_ptr(), _ptr(cu_q), _ptr(cu_k)
     a.lengths, a.block_table, a.scores, a.counts = _ptr(lengths), _ptr(block_table), scores.data_ptr(), counts.data_ptr()
     a.total_q, a.total_k, a.mean_rows = total, total, int(means.shape[0])
@@ -342,8 +347,8 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
             raise ValueError("out and rest cannot be given where a gradient is asked for")
         return _BlockAttention.apply(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
-    out = _output(out, q.shape, q.dtype, q.device, "out")
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    out = _like(q) if out is None else _output(out, q.shape, q.dtype, q.device, "out")
+    lse = q.new_empty((a.total_q, a.heads), dtype=torch.float32)
     if rest is not None:
         _output(rest, q.shape, q.dtype, q.device, "rest")
     a.out, a.rest, a.lse = out.data_ptr(), _ptr(rest), lse.data_ptr()
@@ -369,8 +374,7 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     _output(lse, q.shape[:2], torch.float32, q.device, "lse")
     if rest is not None:
         _output(rest, q.shape, q.dtype, q.device, "rest")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk, dv = (torch.empty(k.shape, dtype=q.dtype, device=q.device) for _ in range(2))
+    dq, dk, dv = _like(q), _like(k), _like(v)
     a.out, a.rest, a.lse, a.dout, a.dq, a.dk, a.dv = (_ptr(t) for t in (out, rest, lse, dout, dq, dk, dv))
     lib = _lib()
     a.workspace_bytes = lib.block_attention_workspace(ctypes.byref(a))
@@ -403,7 +407,7 @@ class _BlockAttention(torch.autograd.Function):
             if torch.cuda.is_current_stream_capturing():
                 _check_capture(ctx.leaves, ctx.stream)
             _graphs.add(ctx)
-        rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        rest = _like(q)
         out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal, rest=rest)
         ctx.save_for_backward(q, k, v, out, rest, lse, blocks, cu_seqlens, cu_seqlens_k)
         ctx.rest = (block_size, scale, causal)
@@ -519,8 +523,8 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     max_length = a.block_table_cols * bs if max_length is None else int(max_length)
     if max_length < 0:
         raise ValueError("max_length must not be negative")
-    out = _output(out, q.shape, q.dtype, device, "out")
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=device)
+    out = _like(q) if out is None else _output(out, q.shape, q.dtype, device, "out")
+    lse = q.new_empty((total, heads), dtype=torch.float32)
     a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     a.k_scale, a.v_scale, a.block_table = k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr()
     a.lengths, a.cu, a.blocks, a.out, a.lse = lengths.data_ptr(), _ptr(cu_seqlens), _ptr(blocks), out.data_ptr(), lse.data_ptr()
