@@ -96,3 +96,38 @@ def test_without_the_rest_of_the_rounding():
     got, lse = mt.block_attention(q, k, v, blocks, 32, out=out)
     assert got is out
     check(mt.block_attention_backward(dout, q, k, v, out, lse, blocks, 32), grads, sizes, torch.bfloat16, 0, 0)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 7, 8, 9, 16, 17, 31, 33, 40, 63, 64, 65, 100, 127, 128])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 64)])
+def test_any_group(group, d, bs):
+    """Heads a key head from 1 to 128: attention, gradient, scores and the cache's step."""
+    from test_gpu_kv8 import build, check as check_cache, put
+    dtype = torch.float16 if group % 2 else torch.bfloat16
+    q, k, v, blocks, cu, _ = make(group, [23, 9], [23, 9], group, 1, d, bs, 2, dtype)
+    dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(4)).to(dtype)
+    want, want_lse, *grads, sizes = oracle.attention(q, k, v, blocks, bs, cu, cu, dout=dout)
+    leaves = [x.to(DEV).requires_grad_() for x in (q, k, v)]
+    out, lse = mt.block_attention(*leaves, blocks.to(DEV), bs, cu_seqlens=cu.to(DEV))
+    smax = (q.double().norm(dim=2).max() * k.double().norm(dim=2).max() / math.sqrt(d)).item()
+    check_out(out.detach(), want, lse, want_lse, v, smax, d, dtype)
+    got = torch.autograd.grad(out, leaves, dout.to(DEV))
+    check(got, grads, sizes, dtype, group * 23, max(x.abs().max().item() for x in (q, k, dout)))
+    means = mt.block_means(k.to(DEV), bs, cu_seqlens=cu.to(DEV))
+    scores, counts = mt.block_scores(q.to(DEV), means, bs, 2, cu_seqlens=cu.to(DEV), first=0, last=0)
+    m = means.cpu().double()
+    placed = [(a + r, i, r) for i, (a, n) in enumerate(((0, 23), (23, 9))) for r in range(n)]
+    ws, wc = oracle.scores(q, lambda i, b: m[int(cu[i]) // bs + i + b], bs, 2, placed, 1, 0, 0)
+    assert torch.equal(counts.cpu(), wc)
+    fin = torch.isfinite(ws)
+    size = (q.double().norm(dim=2).max() * m.norm(dim=2).max() / math.sqrt(d)).item()
+    assert torch.equal(scores.cpu()[~fin].double(), ws[~fin])
+    assert (scores.cpu().double() - ws)[fin].abs().max().item() <= (3 * d + 8) * 2.0 ** -23 * size
+    lens = [130, 31]
+    kc, vc, ks, vs, table = build(3, lens, 1, d, bs)
+    for new in (1, 3):
+        cu = torch.tensor([0, new, 2 * new], dtype=torch.int32)
+        one = q[:2 * new].contiguous()
+        want, want_lse = oracle.cache_attention(one, kc, vc, ks, vs, table, lens, bs, cu)
+        out, lse = mt.kv8_attention(one.to(DEV), *put(kc, vc, ks, vs, table), torch.tensor(lens, dtype=torch.int32, device=DEV), cu_seqlens=cu.to(DEV))
+        check_cache(out, lse, want, want_lse, one, kc, vc, ks, vs, d, dtype)
