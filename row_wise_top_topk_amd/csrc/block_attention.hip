@@ -20,10 +20,11 @@
 // matrix units are busy for 30 % of that; what bounds it is a tile's chain of
 // product, maximum, exponentials and product, with two wavefronts a SIMD to fill
 // each other's gaps (192 registers of operands and sums leave no room for a
-// third), and below 1000 tokens the start: 6 us to the list of blocks, 1 us a
-// tile.  Tried and slower: 16 rows a wavefront (350 us where 32 took 311), 256
-// rows a workgroup (332 and 314; the chunk 639 and 546), the wavefronts sharing
-// the keys of 32 rows for few tokens (517 tokens: 21 us and 18).
+// third), and below 1000 tokens (517, 16/2 heads: 17 us) the start: 6 us to the
+// list of blocks, then a tile's chain of about 1 us.  Tried and slower: 16 rows a
+// wavefront (350 us where 32 took 311), 256 rows a workgroup (332 and 314; the
+// chunk 639 and 546), four wavefronts sharing the keys of 32 rows for few tokens
+// (517 tokens: 21 us and 18).
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
