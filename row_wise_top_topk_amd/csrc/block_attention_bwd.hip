@@ -9,14 +9,14 @@
 //
 // dq goes over the rows as the forward does.  dk and dv go over the key blocks:
 // a bit matrix [key head][block][token] says which tokens selected a block
-// (atomic OR, so its content does not depend on their order), a block's tokens
+// (atomic OR and integer counts: nothing depends on their order), a block's tokens
 // are cut into pieces of equal length, and a workgroup takes one piece: the
 // sink and the own blocks, which every token selects, become many pieces.  A
 // block of one piece is written at once; the others' pieces are summed in order
 // by a last kernel, so the result is the same from run to run.
 //
 // Measured on 8192 tokens, 32/2 heads of 128, 16 blocks of 64: dq 510 to 540 us,
-// dk and dv 400 to 425 us, the sums of pieces 27 us, the bits and pieces 14 us.
+// dk and dv 400 to 425 us, the sums of pieces 27 us, the bits and pieces 10 us.
 // The matrix units are busy for 27 % (dq) and 24 % (dk, dv): dq is bound as the
 // forward is, by a tile's chain with two wavefronts a SIMD; dk and dv by LDS,
 // whose reads (each row twice, by rows and transposed, for every 16 keys) take
@@ -49,18 +49,21 @@ struct BackArgs {
   uint32_t group_magic;  // n / group = n * group_magic >> 32 for n below 2^24, group above 1
 };
 
-// Which tokens of the workgroup selected each listed block, into the bit matrix:
-// tokens t0 .. t0 + 31 of mask word w lie in two words of a block's row.
+// Which tokens of the workgroup selected each listed block, into the bit matrix
+// and the blocks' counts: tokens t0 .. t0 + 31 of mask word w lie in two words of a
+// block's row.
 __device__ __forceinline__ void mark_tokens(const BackArgs& b, const Group& g, int hk, int w0, int active, int nw, const Select& s) {
   for (int i = threadIdx.x; i < active * nw; i += 256) {
     const int id = s.list[i / nw], w = i % nw;
     const uint32_t x = s.mask[id * nw + w];
     if (x == 0) continue;
     const int64_t t = g.t0 + 32 * w;
-    uint32_t* to = b.bits + (hk * b.rows + g.row0 + w0 + id) * b.words + (t >> 5);
+    const int64_t entry = hk * b.rows + g.row0 + w0 + id;
+    uint32_t* to = b.bits + entry * b.words + (t >> 5);
     const int up = static_cast<int>(t & 31);
     if (x << up) atomicOr(to, x << up);
     if (up > 0 && (x >> (32 - up))) atomicOr(to + 1, x >> (32 - up));
+    atomicAdd(b.counts + entry, __popc(x));
   }
 }
 
@@ -332,20 +335,10 @@ __global__ void __launch_bounds__(256, 2) block_attention_dq_kernel(BackArgs b) 
 // ---- the pieces of each block's tokens ----
 
 __global__ void __launch_bounds__(256) clear_bits_kernel(BackArgs b) {
-  const int64_t total = b.a.kv_heads * b.rows * b.words;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) b.bits[i] = 0;
-}
-
-// Tokens of each block; one wavefront a block.
-__global__ void __launch_bounds__(256) count_bits_kernel(BackArgs b) {
-  const int lane = threadIdx.x & 63;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (e >= b.a.kv_heads * b.rows) return;
-  const uint32_t* bits = b.bits + e * b.words;
-  int n = 0;
-  for (int64_t w = lane; w < b.words; w += 64) n += __popc(bits[w]);
-  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-  if (lane == 0) b.counts[e] = n;
+  const int64_t entries = b.a.kv_heads * b.rows, total = entries * b.words, step = static_cast<int64_t>(gridDim.x) * 256;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t i = first; i < total; i += step) b.bits[i] = 0;
+  for (int64_t i = first; i < entries; i += step) b.counts[i] = 0;
 }
 
 // Pieces of each block (one at least, for the zeros of a block that nobody
@@ -736,7 +729,7 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   const int64_t pairs = p.total_q * p.kv_heads * p.select;
   if (grid > INT32_MAX || entries > INT32_MAX || (pairs + 255) / 256 > INT32_MAX || b.max_pieces < 0) return MI_ATTN_EINVAL;
   const int64_t words = entries * b.words;
-  if (words > 0)
+  if (entries > 0)
     clear_bits_kernel<<<dim3(static_cast<unsigned>(words / 1024 + 1 < 4096 ? words / 1024 + 1 : 4096)), dim3(256), 0, stream>>>(b);
   if (pairs > 0) {
     BackArgs few = b;
@@ -744,7 +737,6 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
     else launch_dq<T, D, false>(b, stream);
   }
   if (p.total_k == 0) return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
-  count_bits_kernel<<<dim3(static_cast<unsigned>((entries + 3) / 4)), dim3(256), 0, stream>>>(b);
   number_pieces_kernel<<<dim3(1), dim3(1024), 0, stream>>>(b);
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   const int st = p.bs >= 64 ? launch_dkv<T, D, 4>(b, stream) : (p.bs == 32 ? launch_dkv<T, D, 2>(b, stream) : launch_dkv<T, D, 1>(b, stream));
