@@ -13,7 +13,7 @@
 //
 // Measured: 64 sequences of 500 to 32000 keys, 64/8 heads of 128, pages of 64:
 // 400 us and 13 for the join, 2.13 GB at 5.2 TB/s, more than a large copy reaches;
-// 3 x 3 tokens over 20011 keys: 10 + 9 us, 8 single tokens at 32 of 14000 blocks:
+// 3 x 3 tokens over 20011 keys: 10 + 6 us, 8 single tokens at 32 of 14000 blocks:
 // 8 + 5 us: there the chain from the lengths over the table and the scales to the
 // codes bounds it.
 #include <hip/hip_runtime.h>
@@ -471,11 +471,13 @@ __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ?
 }
 
 // Joins the chunks of a workgroup's rows: one wavefront a row (12300 rows of up
-// to 8 chunks: 13 us).
-template <typename T, int D>
+// to 8 chunks: 13 us), or four that share the chunks of a row and are added up in
+// order (kFour; 90 rows of up to 157: 5.5 us, by one wavefront 9).
+template <typename T, int D, bool kFour>
 __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_per) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t index = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ float s_o[4][D], s_l[4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t index = kFour ? blockIdx.x : blockIdx.x * 4 + wave;
   const int64_t item = index / rows_per;
   const int row = static_cast<int>(index % rows_per);
   if (item >= p.slots * p.kv_heads * p.head_chunks) return;
@@ -495,8 +497,9 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_pe
   // 64 chunks at a time: a lane works out the weight of one, then all add the
   // chunks' values, eight loads in flight.  A chunk that added nothing may not
   // have written any.
-  for (int s0 = 0; s0 < used; s0 += 64) {
-    const int n = min(64, used - s0);
+  const int share = kFour ? (used + 3) / 4 : used, end = min(used, (kFour ? wave + 1 : 1) * share);
+  for (int s0 = kFour ? wave * share : 0; s0 < end; s0 += 64) {
+    const int n = min(64, end - s0);
     float f = 0.f;
     if (lane < n) {
       const int64_t a = at + static_cast<int64_t>(s0 + lane) * rows_per;
@@ -520,6 +523,19 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_pe
     }
   }
   for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  if constexpr (kFour) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) s_o[wave][lane * (D / 64) + i] = o[i];
+    if (lane == 0) s_l[wave] = l;
+    __syncthreads();
+    if (wave > 0) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const int d = lane * (D / 64) + i;
+      o[i] = (s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]);
+    }
+  }
   const int64_t tok = rw.first + row / rw.heads, h = rw.head0 + row % rw.heads;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   char* to = static_cast<char*>(p.out) + ((tok * p.heads + h) * D + lane * (D / 64)) * 2;
@@ -539,9 +555,13 @@ int launch_decode(const DecodeArgs& p, int mt, hipStream_t stream) {
   else kv8_attention_kernel<T, D, 4><<<g, dim3(256), 0, stream>>>(p);
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   if (p.splits > 1) {
-    const int64_t joins = (items * mt * 16 + 3) / 4;
+    const int64_t rows = items * mt * 16;
+    const bool four = p.splits > 16;
+    const int64_t joins = four ? rows : (rows + 3) / 4;
     if (joins > INT32_MAX / 4) return MI_ATTN_EINVAL;
-    kv8_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, mt * 16);
+    const dim3 jg(static_cast<unsigned>(joins));
+    if (four) kv8_join_kernel<T, D, true><<<jg, dim3(256), 0, stream>>>(p, mt * 16);
+    else kv8_join_kernel<T, D, false><<<jg, dim3(256), 0, stream>>>(p, mt * 16);
     if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   }
   return MI_ATTN_OK;
