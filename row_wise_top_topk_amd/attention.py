@@ -142,9 +142,9 @@ def _heads(t, what: str, device=None, dtype=None, dim=None):
 
 
 def _ints(t, what: str, device, dims: int, shape=None) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != dims or t.device != device:
         raise ValueError(f"{what} must be a {dims}-D int32 tensor on the others' device")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have the shape {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
@@ -169,11 +169,11 @@ def _sequences(cu_q, cu_k, device, total_q: int, total_k: int):
 
 def _table(t, device):
     """(sequences, columns, stride) of a block table."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 2 or t.device != device
-            or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
-        raise ValueError("block_table must be a 2-D int32 tensor on the others' device with unit stride along its last axis")
-    n, cols = t.shape
-    return n, cols, t.stride(0) if n > 1 else cols
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == 2 and t.device == device:
+        (n, cols), (rows_at, cols_at) = t.shape, t.stride()
+        if (cols <= 1 or cols_at == 1) and (n <= 1 or rows_at >= cols):
+            return n, cols, rows_at if n > 1 else cols
+    raise ValueError("block_table must be a 2-D int32 tensor on the others' device with unit stride along its last axis")
 
 
 def _block_size(block_size) -> int:
@@ -429,20 +429,26 @@ class _BlockAttention(torch.autograd.Function):
         return dq if need[0] else None, dk if need[1] else None, dv if need[2] else None, *(None,) * 6
 
 
+_F8 = torch.float8_e4m3fn
+
+
 def _cache(k_cache, v_cache, k_scale, v_scale, device, hk=None, dim=None):
     """Pages of the 8-bit cache; returns (pages, kv_heads, block_size, dim)."""
     for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float8_e4m3fn or t.dim() != 4 or t.device != device
-                or not t.is_contiguous() or t.shape != k_cache.shape or (t.numel() and t.data_ptr() % 16)):
+        if (not isinstance(t, torch.Tensor) or t.dtype is not _F8 or t.dim() != 4 or t.device != device
+                or not t.is_contiguous() or t.data_ptr() % 16):
             raise ValueError(f"{what} must be a contiguous float8_e4m3fn tensor [pages, kv_heads, block_size, dim] on the "
                              "others' device, 16-byte aligned, k_cache and v_cache of one shape")
-    pages, heads, bs, d = k_cache.shape
+    pages, heads, bs, d = shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape")
     _block_size(bs)
     if d not in HEAD_DIMS or heads < 1 or (hk is not None and heads != hk) or (dim is not None and d != dim):
         raise ValueError(f"the cache must have the others' heads and head dimension, one of {HEAD_DIMS}")
+    shape = shape[:2]
     for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (pages, heads)
-                or not t.is_contiguous() or t.device != device):
+        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous()
+                or t.device != device):
             raise ValueError(f"{what} must be a contiguous float32 tensor [pages, kv_heads] on the others' device")
     return pages, heads, bs, d
 
