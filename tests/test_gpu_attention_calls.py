@@ -441,3 +441,51 @@ def test_scores_past_4_gib():
     assert big.numel() * 4 > 1 << 32 and torch.equal(counts, counts2)
     assert torch.equal(big[:, :, :1063], small)
     assert (big[::97, :, 1063:] == -math.inf).all() and (big[-50:, :, 1063:] == -math.inf).all()
+
+
+def test_padded_batch():
+    """A decode batch filled up with requests of length 0, whose table rows hold anything."""
+    g = torch.Generator().manual_seed(6)
+    lens = [40, 0, 7, 0]
+    kc, vc, ks, vs, table = build(2, [40, 1, 7, 1], 2, 64, 16)
+    table[1], table[3] = torch.tensor([5, 1 << 30, -9]), torch.tensor([0, 1, 2])
+    dev = put(kc, vc, ks, vs, table)
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    mean = torch.zeros(kc.shape[0], 2, 64, device=DEV)
+    q = torch.randn(4, 8, 64, generator=g).to(BF)
+    k, v = (torch.randn(4, 2, 64, generator=g).to(BF) for _ in range(2))
+    q[1], k[3], v[1] = math.nan, math.inf, math.nan
+    mt.kv8_append(k.to(DEV), v.to(DEV), *dev, lengths, k_mean=mean)
+    oracle.append(k, v, kc, vc, ks, vs, table, lens, 16)
+    assert same(dev[0], kc) and same(dev[1], vc) and torch.equal(dev[2].cpu(), ks)
+    mean[:] = torch.randn(mean.shape, generator=g).to(DEV)
+    scores, counts = mt.block_scores(q.to(DEV), mean, 16, 3, lengths=lengths, block_table=dev[4])
+    assert counts[:, 0].tolist() == [3, 0, 1, 0] and (scores[[1, 3]] == -math.inf).all()
+    blocks = mt.topk_indices(scores.flatten(0, 1), counts.flatten(), 2).view(4, 2, 2)
+    assert (blocks[[1, 3]] == -1).all()
+    for b in (None, blocks):
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, lengths, blocks=b)
+        want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, 16, None, None if b is None else b.cpu())
+        assert (out[[1, 3]] == 0).all() and (lse[[1, 3]] == -math.inf).all()
+        top = (vc.nan_to_num() * vs[:, :, None, None]).abs().max().item()
+        assert (out.cpu().double() - want).abs().max().item() <= 2.25 * 2.0 ** -8 * top
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, do not disturb each other."""
+    lens = [3000, 2000]
+    kc, vc, ks, vs, table = build(7, lens, 2, 128, 16)
+    dev = put(kc, vc, ks, vs, table)
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(9)
+    qs = [torch.randn(2, 8, 128, generator=g).to(BF).to(DEV) for _ in range(8)]
+    want = [mt.kv8_attention(q, *dev, lengths)[0] for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [None] * 8
+    for i, q in enumerate(qs):
+        with torch.cuda.stream(streams[i % 2]):
+            got[i] = mt.kv8_attention(q, *dev, lengths)[0]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
