@@ -500,15 +500,14 @@ __global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b)
   };
   const char* qbase = static_cast<const char*>(p.q) + (tid % kLanes) * 16;
   const char* gbase = static_cast<const char*>(p.dout) + (tid % kLanes) * 16;
-  const uint64_t qt = p.q_t * 2, gt = p.do_t * 2;
-  const uint32_t qh = static_cast<uint32_t>(p.q_h * 2), gh = static_cast<uint32_t>(p.do_h * 2);
+  const uint64_t qt = p.q_t * 2, gt = p.do_t * 2, qh = p.q_h * 2, gh = p.do_h * 2;
   auto load_rows = [&](int r0) {
 #pragma unroll
     for (int j = 0; j < kIn; ++j) {
       int head;
       const uint32_t tok = token_of(min(r0 + j * kStep + tid / kLanes, total - 1), head);
-      qin[j] = *reinterpret_cast<const u32x4*>(qbase + (tok * qt + static_cast<uint64_t>(static_cast<uint32_t>(head)) * qh));
-      gin[j] = *reinterpret_cast<const u32x4*>(gbase + (tok * gt + static_cast<uint64_t>(static_cast<uint32_t>(head)) * gh));
+      qin[j] = *reinterpret_cast<const u32x4*>(qbase + (tok * qt + static_cast<uint32_t>(head) * qh));
+      gin[j] = *reinterpret_cast<const u32x4*>(gbase + (tok * gt + static_cast<uint32_t>(head) * gh));
     }
     if (tid < kRowsAt) {
       int head;

@@ -1,0 +1,43 @@
+"""GPU: calls at the corners of the attention operators: head strides past 4 GiB,
+caches and means of no rows, loops that only long inputs enter.
+
+Where two calls have to agree they do the same arithmetic and their results are
+equal; against the 64-bit forms the tolerances are those of the other tests."""
+
+import math
+
+import pytest
+import torch
+
+import attention_oracle as oracle
+import row_wise_top_topk_amd as mt
+from test_gpu_attention_hidden import agree
+from test_gpu_block_attention import check_out, gpu, make
+from test_gpu_kv8 import build, check, put
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF, F16 = torch.bfloat16, torch.float16
+
+
+def test_head_strides_past_4_gib():
+    """Heads of q and dout that lie 4 GiB and more apart."""
+    t, step = 70, (1 << 31) + (1 << 13)
+    q, k, v, blocks, _, _ = make(9, [t], [t], 2, 1, 64, 16, 3, BF)
+    dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(0)).to(BF)
+    store = torch.zeros(step + 2 * t * 64, dtype=BF, device=DEV)
+    far = [store[i * t * 64:].as_strided((t, 2, 64), (64, step, 1)) for i in range(2)]
+    for view, x in zip(far, (q, dout)):
+        view.copy_(x)
+    near = gpu(q, dout)
+    k, v, blocks = gpu(k, v, blocks)
+    results = []
+    for x, g in (near, far):
+        rest = torch.empty_like(q, device=DEV)
+        out, lse = mt.block_attention(x, k, v, blocks, 16, rest=rest)
+        results.append((out, lse, rest, *mt.block_attention_backward(g, x, k, v, out, lse, blocks, 16, rest=rest)))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    means = mt.block_means(k, 16)
+    for a, b in zip(*(mt.block_scores(x, means, 16, 5) for x in (near[0], far[0]))):
+        assert torch.equal(a, b)
