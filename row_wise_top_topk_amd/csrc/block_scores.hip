@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(256, RT == 8 ? 2 : 4) block_scores_kernel(Scor
     const int64_t n = (pos >> p.lb) + 1;
     return static_cast<int>(n < p.max_blocks ? n : p.max_blocks);
   };
-  const int seen = count_of(tokens - 1);  // positions ascend
+  // means of no rows hold no block, and nothing is read of them
+  const int seen = p.mean_rows > 0 ? count_of(tokens - 1) : 0;  // positions ascend
   if (blockIdx.y == 0)
     for (int tl = threadIdx.x; tl < tokens; tl += 256) p.counts[(at.first + tl) * p.kv_heads + hk] = count_of(tl);
 
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(256, RT == 8 ? 2 : 4) block_scores_kernel(Scor
   float* best = s_best[wave];
   const int end = min(p.max_blocks, (static_cast<int>(blockIdx.y) + 1) * p.chunk);
   for (int b0 = blockIdx.y * p.chunk + wave * 16; b0 < end; b0 += 64) {
-    bool bad = false;
+    bool bad = p.mean_rows == 0;
     if (b0 < seen) {
       const int b = min(b0 + (lane & 15), seen - 1);
       int64_t row = base + b;

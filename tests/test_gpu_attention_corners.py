@@ -41,3 +41,21 @@ def test_head_strides_past_4_gib():
     means = mt.block_means(k, 16)
     for a, b in zip(*(mt.block_scores(x, means, 16, 5) for x in (near[0], far[0]))):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("h,hk", [(8, 2), (24, 1), (128, 1)])
+def test_scores_of_no_means(dtype, h, hk):
+    """Means of no rows: a block of none of them has -inf, and the counts are the positions'."""
+    means = torch.empty(0, hk, 128, device=DEV)
+    q = torch.randn(5, h, 128, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    lengths = torch.tensor([1, 700, 0, 64, 65], dtype=torch.int32, device=DEV)
+    table = torch.zeros(5, 11, dtype=torch.int32, device=DEV)
+    cu = torch.arange(6, dtype=torch.int32, device=DEV)
+    for c in (None, cu):
+        scores, counts = mt.block_scores(q, means, 64, 11, cu_seqlens=c, lengths=lengths, block_table=table)
+        assert (scores == -math.inf).all() and counts.tolist() == [[n] * hk for n in (1, 11, 0, 1, 2)]
+    two = torch.tensor([0, 2, 5], dtype=torch.int32, device=DEV)
+    keys = torch.tensor([0, 100, 350], dtype=torch.int32, device=DEV)
+    scores, counts = mt.block_scores(q, means, 64, 4, cu_seqlens=two, cu_seqlens_k=keys)
+    assert (scores == -math.inf).all() and counts.tolist() == [[n] * hk for n in (2, 2, 4, 4, 4)]
