@@ -279,6 +279,8 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
         elif total != n:
             raise ValueError("without cu_seqlens there must be one query for each sequence")
         cu_q, cu_k = cu_seqlens, None
+        if n == 0:  # all rows lie behind the last sequence, as in the packed form
+            cu_k, block_table, lengths = cu_seqlens, None, None
     else:
         if lengths is not None:
             raise ValueError("lengths goes with block_table")
@@ -287,11 +289,14 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
             raise ValueError("means must have a row for every block, as block_means gives them")
     scores = means.new_empty((total, hk, max_blocks))
     counts = means.new_empty((total, hk), dtype=torch.int32)
+    scale = _scale(scale, dim)
+    if total == 0:
+        return scores, counts
     a.q, a.means, a.cu_q, a.cu_k = q.data_ptr(), means.data_ptr(), _ptr(cu_q), _ptr(cu_k)
     a.lengths, a.block_table, a.scores, a.counts = _ptr(lengths), _ptr(block_table), scores.data_ptr(), counts.data_ptr()
     a.total_q, a.total_k, a.mean_rows = total, total, int(means.shape[0])
     a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
-    a.max_blocks, a.first, a.last, a.scale = max_blocks, first, last, _scale(scale, dim)
+    a.max_blocks, a.first, a.last, a.scale = max_blocks, first, last, scale
     _run(device, "block_scores", _lib().block_scores, ctypes.byref(a))
     return scores, counts
 

@@ -59,3 +59,16 @@ def test_scores_of_no_means(dtype, h, hk):
     keys = torch.tensor([0, 100, 350], dtype=torch.int32, device=DEV)
     scores, counts = mt.block_scores(q, means, 64, 4, cu_seqlens=two, cu_seqlens_k=keys)
     assert (scores == -math.inf).all() and counts.tolist() == [[n] * hk for n in (2, 2, 4, 4, 4)]
+
+
+@pytest.mark.parametrize("tail", [0, 3])
+def test_scores_of_an_empty_batch(tail):
+    """A paged call without sequences, alone or with rows behind the last one."""
+    means = torch.randn(4, 2, 64, device=DEV)
+    q = torch.randn(tail, 4, 64, device=DEV).to(BF)
+    table, lengths = (torch.zeros(*n, dtype=torch.int32, device=DEV) for n in ((3, 6), (3,)))
+    cu = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for c in (cu,) if tail else (None, cu):
+        for x, n in ((table[:0], lengths[:0]), (table[:0].clone(), lengths[:0].clone()), (table[:0], lengths[:0].clone())):
+            scores, counts = mt.block_scores(q, means, 16, 6, cu_seqlens=c, lengths=n, block_table=x)
+            assert scores.shape == (tail, 2, 6) and (scores == -math.inf).all() and (counts == 0).all() and counts.shape == (tail, 2)
