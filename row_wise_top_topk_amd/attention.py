@@ -296,7 +296,7 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     a.lengths, a.block_table, a.scores, a.counts = _ptr(lengths), _ptr(block_table), scores.data_ptr(), counts.data_ptr()
     a.total_q, a.total_k, a.mean_rows = total, total, int(means.shape[0])
     a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size = _DTYPES[q.dtype], n, heads, hk, dim, bs
-    a.max_blocks, a.first, a.last, a.scale = max_blocks, first, last, scale
+    a.max_blocks, a.first, a.last, a.scale = max_blocks, min(first, max_blocks), min(last, max_blocks), scale
     _run(device, "block_scores", _lib().block_scores, ctypes.byref(a))
     return scores, counts
 

@@ -72,3 +72,12 @@ def test_scores_of_an_empty_batch(tail):
         for x, n in ((table[:0], lengths[:0]), (table[:0].clone(), lengths[:0].clone()), (table[:0], lengths[:0].clone())):
             scores, counts = mt.block_scores(q, means, 16, 6, cu_seqlens=c, lengths=n, block_table=x)
             assert scores.shape == (tail, 2, 6) and (scores == -math.inf).all() and (counts == 0).all() and counts.shape == (tail, 2)
+
+
+def test_more_forced_blocks_than_32_bits_count():
+    k = torch.randn(70, 2, 64, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    means = mt.block_means(k, 16)
+    want, _ = mt.block_scores(k, means, 16, 5, first=5, last=0)
+    for n in (1 << 31, 1 << 32, 1 << 70):
+        for kw in (dict(first=n, last=0), dict(first=0, last=n)):
+            assert torch.equal(mt.block_scores(k, means, 16, 5, **kw)[0], want)
