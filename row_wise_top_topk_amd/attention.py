@@ -25,6 +25,7 @@ import math
 import weakref
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 __all__ = ["block_means", "block_scores", "block_attention", "block_attention_backward", "kv8_append", "kv8_attention"]
 
@@ -117,10 +118,17 @@ def _run(device, what: str, fn, *args) -> None:
         raise RuntimeError(f"{what} failed: {_STATUS.get(status, 'unknown status')} (status {status})")
 
 
+def _no_tangent(t, what: str) -> None:
+    """Refuses an operand with a forward-mode derivative, which the result would not have."""
+    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{what} has a tangent: there is no forward-mode derivative")
+
+
 def _heads(t, what: str, device=None, dtype=None, dim=None):
     """Checks a [tokens, heads, dim] operand; returns its shape and (token, head) strides, 0 for an axis of one entry."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() != 3:
         raise ValueError(f"{what} must be a 3-D bfloat16 or float16 tensor [tokens, heads, dim]")
+    _no_tangent(t, what)
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a GPU")
     if (device is not None and t.device != device) or (dtype is not None and t.dtype != dtype):
@@ -219,7 +227,7 @@ def block_means(k: torch.Tensor, block_size: int, cu_seqlens: torch.Tensor = Non
     ``k``: bfloat16 or float16 ``[tokens, kv_heads, dim]``.  Returns float32
     ``[tokens // block_size + sequences, kv_heads, dim]``: block b of sequence
     i is row ``cu_seqlens[i] // block_size + i + b``; rows that are no block
-    are 0."""
+    are 0.  No gradient goes back through the means."""
     bs = _block_size(block_size)
     total, hk, dim, st, sh = _heads(k, "k")
     device = k.device
@@ -252,7 +260,8 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     queries' own) and ``means`` float32 ``[pages, kv_heads, dim]``; without
     ``cu_seqlens`` each sequence has one query.  An entry of the table outside
     the pages gives its block -inf.  Rows behind the last sequence are -inf
-    with count 0."""
+    with count 0.  No gradient goes back through the scores: what is selected
+    is constant to ``block_attention``."""
     bs = _block_size(block_size)
     a = _ScoreArgs()
     total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
@@ -260,6 +269,7 @@ def block_scores(q: torch.Tensor, means: torch.Tensor, block_size: int, max_bloc
     if (not isinstance(means, torch.Tensor) or means.dtype != torch.float32 or means.dim() != 3 or means.device != device
             or not means.is_contiguous() or means.shape[2] != dim or means.shape[1] < 1):
         raise ValueError("means must be a contiguous float32 tensor [rows, kv_heads, dim] on q's device")
+    _no_tangent(means, "means")
     if means.numel() and means.data_ptr() % 16:
         raise ValueError("means must be 16-byte aligned")
     hk = int(means.shape[1])
@@ -341,8 +351,8 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     log-sum of the scaled scores' exponentials, float32 ``[tokens, heads]``.  A
     query that sees no key, and a row behind the last sequence, has 0 and -inf.
 
-    Differentiable in q, k and v through autograd (``lse`` is not; ``out=`` and
-    ``rest=`` are refused then).  A graph can capture the call with its backward;
+    Differentiable once in q, k and v through autograd (``lse`` is not; ``out=``
+    and ``rest=`` are refused then; forward-mode derivatives are refused always).  A graph can capture the call with its backward;
     an eager gradient graph of the same leaves that is still alive is refused
     then (any operation's such graph ends a capture; this one sees its own).  A caller of ``block_attention_backward`` gives
     ``rest`` (like ``out``), which receives what the rounding of ``out`` leaves
@@ -370,7 +380,7 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     called; ``rest`` as ``block_attention`` filled it in (without it dq loses
     precision).  The result is the same from run to run.  With float16 the scores'
     gradients are held in float16: below about 6e-8 they are lost (scale the
-    loss)."""
+    loss).  The gradients are constants: nothing goes back through them."""
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     _, _, _, a.dout_stride_t, a.dout_stride_h = _heads(dout, "dout", q.device, q.dtype, q.shape[2])
     if dout.shape != q.shape:
@@ -517,7 +527,8 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     the caller knows them (default: what the table can hold); it only decides
     how the work is split.
 
-    Returns ``(out, lse)`` as ``block_attention`` does."""
+    Returns ``(out, lse)`` as ``block_attention`` does, without its gradient:
+    neither is differentiable, whatever ``q`` asks for."""
     a = _DecodeArgs()
     total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
     device = q.device

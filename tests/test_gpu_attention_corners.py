@@ -8,6 +8,7 @@ import math
 
 import pytest
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 import attention_oracle as oracle
 import row_wise_top_topk_amd as mt
@@ -81,3 +82,20 @@ def test_more_forced_blocks_than_32_bits_count():
     for n in (1 << 31, 1 << 32, 1 << 70):
         for kw in (dict(first=n, last=0), dict(first=0, last=n)):
             assert torch.equal(mt.block_scores(k, means, 16, 5, **kw)[0], want)
+
+
+def test_forward_mode_derivatives_are_refused():
+    q, b = torch.zeros(10, 2, 64, dtype=BF, device=DEV), torch.zeros(10, 2, 1, dtype=torch.int32, device=DEV)
+    means, lse = torch.zeros(1, 2, 64, device=DEV), torch.zeros(10, 2, device=DEV)
+    with forward_ad.dual_level():
+        calls = [(mt.block_attention, (q, q, q, b, 16), 3), (mt.block_attention_backward, (q, q, q, q, q, lse, b, 16), 4),
+                 (mt.block_scores, (q, means, 16, 1), 2), (mt.block_means, (q, 16), 1)]
+        for fn, args, operands in calls:
+            fn(*args)
+            for i in range(operands):
+                dual = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+                with pytest.raises(ValueError, match="forward-mode"):
+                    fn(*args[:i], dual, *args[i + 1:])
+                if fn is mt.block_attention and i < 3:
+                    with pytest.raises((ValueError, RuntimeError, NotImplementedError)):
+                        fn(*(t.clone().requires_grad_() if j < 3 and j != i else t for j, t in enumerate((*args[:i], dual, *args[i + 1:]))))
