@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 import weakref
 
 import torch
@@ -352,11 +353,13 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blocks: t
     query that sees no key, and a row behind the last sequence, has 0 and -inf.
 
     Differentiable once in q, k and v through autograd (``lse`` is not; ``out=``
-    and ``rest=`` are refused then; forward-mode derivatives are refused always).  A graph can capture the call with its backward;
-    an eager gradient graph of the same leaves that is still alive is refused
-    then (any operation's such graph ends a capture; this one sees its own).  A caller of ``block_attention_backward`` gives
-    ``rest`` (like ``out``), which receives what the rounding of ``out`` leaves
-    out."""
+    and ``rest=`` are refused then; forward-mode derivatives are refused always).
+    A graph can capture the call with its backward, but not while an eager
+    gradient graph of the same leaves is alive: any operation's such graph would
+    end the capture, this one sees its own and refuses the call, also where only
+    the forward would be captured (capture that under ``torch.no_grad``).  A
+    caller of ``block_attention_backward`` gives ``rest`` (like ``out``), which
+    receives what the rounding of ``out`` leaves out."""
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
         if out is not None or rest is not None:
             raise ValueError("out and rest cannot be given where a gradient is asked for")
@@ -399,29 +402,49 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     return dq, dk, dv
 
 
-_graphs = weakref.WeakSet()  # the calls whose gradient graphs are alive
+class _Summing:
+    """Stands for the node that sums a leaf's gradients: made by the first gradient
+    graph of the leaf and kept by all that follow while any of them lives."""
+
+    def __init__(self, leaf, stream: int):
+        self.leaf, self.stream = weakref.ref(leaf), stream
 
 
-def _check_capture(leaves, stream: int) -> None:
-    """Refuses a call under capture whose leaves have a gradient graph of another
-    stream.  A leaf's gradients are summed on the stream of its first living
-    graph: the backward would pull that stream into the capture, which ends the
-    process."""
-    for ctx in list(_graphs):
-        if ctx.stream != stream and any(x() is y() for x in ctx.leaves for y in leaves):
-            raise RuntimeError("block_attention cannot be captured while a gradient graph of the same leaves, made on another "
-                               "stream, is alive: drop that graph's results first")
+_summing = weakref.WeakValueDictionary()  # by the leaf's id: held by the calls' gradient graphs
+_summing_lock = threading.Lock()
+
+
+def _summed(leaves, stream: int) -> list:
+    """The leaves' nodes, for a call on ``stream``."""
+    nodes = []
+    with _summing_lock:
+        for leaf in leaves:
+            node = _summing.get(id(leaf))
+            if node is None or node.leaf() is not leaf:
+                node = _summing[id(leaf)] = _Summing(leaf, stream)
+            nodes.append(node)
+    return nodes
+
+
+def _check_capture(nodes, stream: int) -> None:
+    """Refuses a call under capture whose leaves' gradients are summed on another
+    stream, that of the first living gradient graph: the backward would pull that
+    stream into the capture, which ends the process."""
+    if any(node.stream != stream for node in nodes):
+        raise RuntimeError("block_attention cannot be captured while a gradient graph of the same leaves, first made on another "
+                           "stream, is alive: drop the results of all such graphs first, or capture without gradients "
+                           "(torch.no_grad)")
 
 
 class _BlockAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal):
-        ctx.leaves = [weakref.ref(t) for t in (q, k, v) if t.requires_grad and t.is_leaf]
-        if ctx.leaves and q.is_cuda:
-            ctx.stream = _raw_stream(q.device.index)
+        leaves = [t for t in (q, k, v) if t.requires_grad and t.is_leaf]
+        if leaves and q.is_cuda:
+            stream = _raw_stream(q.device.index)
+            ctx.nodes = _summed(leaves, stream)
             if torch.cuda.is_current_stream_capturing():
-                _check_capture(ctx.leaves, ctx.stream)
-            _graphs.add(ctx)
+                _check_capture(ctx.nodes, stream)
         rest = _like(q)
         out, lse = block_attention(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal, rest=rest)
         ctx.save_for_backward(q, k, v, out, rest, lse, blocks, cu_seqlens, cu_seqlens_k)

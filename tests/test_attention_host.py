@@ -1,10 +1,14 @@
 """What the attention operators decide on the host: no GPU needed."""
 
+import sys
+import threading
+
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
 
 import row_wise_top_topk_amd as mt
+from row_wise_top_topk_amd import attention as binding
 
 
 def test_forward_mode_derivatives_are_refused():
@@ -23,3 +27,52 @@ def test_forward_mode_derivatives_are_refused():
         # the operands themselves are looked at: a primal of a level has no tangent
         with pytest.raises(ValueError, match="GPU"):
             mt.block_means(forward_ad.unpack_dual(dual).primal, 16)
+
+
+def test_the_node_that_sums_a_leafs_gradients():
+    """It keeps the stream of the first living graph, also when that graph goes before the others."""
+    x, y = torch.zeros(4), torch.zeros(4)
+    first = binding._summed([x], 1)
+    second = binding._summed([y, x], 2)
+    assert second[1] is first[0] and [n.stream for n in second] == [2, 1]
+    del first
+    third = binding._summed([x], 2)
+    assert third[0].stream == 1
+    with pytest.raises(RuntimeError, match="captured"):
+        binding._check_capture(third, 2)
+    binding._check_capture(third, 1)
+    del second, third
+    assert len(binding._summing) == 0
+    assert [n.stream for n in binding._summed([x], 2)] == [2]
+    assert len(binding._summing) == 0
+    other = binding._summed([x], 3)
+    binding._summing[id(y)] = other[0]                    # what a reused id would look like
+    assert [n.stream for n in binding._summed([y], 4)] == [4]
+
+
+def test_threads_of_graphs():
+    """Graphs that come and go in several threads while others look them up."""
+    leaves = [torch.zeros(1) for _ in range(3)]
+    errors, interval = [], sys.getswitchinterval()
+
+    def work(stream):
+        try:
+            kept = []
+            for i in range(4000):
+                kept.append(binding._summed(leaves if stream else leaves[:1], stream))
+                binding._check_capture(kept[-1][:1], kept[-1][0].stream)
+                if i % 50 == stream:
+                    kept.clear()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    sys.setswitchinterval(1e-6)
+    try:
+        threads = [threading.Thread(target=work, args=(s,)) for s in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert not errors and len(binding._summing) == 0

@@ -99,3 +99,36 @@ def test_forward_mode_derivatives_are_refused():
                 if fn is mt.block_attention and i < 3:
                     with pytest.raises((ValueError, RuntimeError, NotImplementedError)):
                         fn(*(t.clone().requires_grad_() if j < 3 and j != i else t for j, t in enumerate((*args[:i], dual, *args[i + 1:]))))
+
+
+def test_capture_on_a_stream_of_later_graphs():
+    """Leaves whose first graph was another stream's: the later graphs' stream does not make them fit for a capture on it."""
+    q, k, v, blocks, _, _ = make(3, [40], [40], 4, 2, 64, 16, 2, BF)
+    blocks = blocks.to(DEV)
+    leaves = [x.to(DEV).requires_grad_() for x in (q, k, v)]
+    stream = torch.cuda.Stream()
+    first = mt.block_attention(*leaves, blocks, 16)[0]
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        second = mt.block_attention(*leaves, blocks, 16)[0]
+    torch.cuda.synchronize()
+    del first                                               # the second keeps the node that the first made
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        with pytest.raises(RuntimeError, match="captured"):
+            mt.block_attention(*leaves, blocks, 16)
+        with torch.no_grad():
+            plain = mt.block_attention(*leaves, blocks, 16)[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.isfinite(plain).all() and plain.abs().max() > 0
+    del second
+    with torch.cuda.stream(stream):
+        want = torch.autograd.grad(mt.block_attention(*leaves, blocks, 16)[0], leaves, torch.ones_like(leaves[0]))
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph := torch.cuda.CUDAGraph(), stream=stream):
+        got = torch.autograd.grad(mt.block_attention(*leaves, blocks, 16)[0], leaves, torch.ones_like(leaves[0]))
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
