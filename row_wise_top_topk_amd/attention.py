@@ -565,9 +565,10 @@ def kv8_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or not 1 <= blocks.shape[2] <= MAX_SELECT:
             raise ValueError(f"blocks must be an int32 tensor [tokens, kv_heads, selected], selected in [1, {MAX_SELECT}]")
         _ints(blocks, "blocks", device, 3, (total, hk, blocks.shape[2]))
-    max_length = a.block_table_cols * bs if max_length is None else int(max_length)
-    if max_length < 0:
+    if max_length is not None and max_length < 0:
         raise ValueError("max_length must not be negative")
+    most = a.block_table_cols * bs
+    max_length = most if max_length is None else min(int(max_length), most)
     out = _like(q) if out is None else _output(out, q.shape, q.dtype, device, "out")
     lse = q.new_empty((total, heads), dtype=torch.float32)
     a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()

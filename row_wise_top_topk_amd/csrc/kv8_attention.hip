@@ -590,7 +590,7 @@ Plan make_plan(const mi_kv8_attention_args* a) {
   p.head_chunks = (group + p.mt * 16 - 1) / (p.mt * 16);
   p.slots = slots_of(a->total_q, a->num_seqs, p.tokens_per);
   p.items = p.slots * a->kv_heads * p.head_chunks;
-  int64_t most = (a->max_length + a->block_size - 1) / a->block_size;
+  int64_t most = a->max_length / a->block_size + (a->max_length % a->block_size != 0);
   if (most > a->block_table_cols) most = a->block_table_cols;
   if (sparse && most > a->select) most = a->select;
   if (most < 1) most = 1;

@@ -1,5 +1,6 @@
 """What the attention operators decide on the host: no GPU needed."""
 
+import ctypes
 import sys
 import threading
 
@@ -76,3 +77,23 @@ def test_threads_of_graphs():
     finally:
         sys.setswitchinterval(interval)
     assert not errors and len(binding._summing) == 0
+
+
+def decode(total_q, columns, max_length=None, heads=64, kv_heads=8, dim=128, block_size=64, num_seqs=1, select=0):
+    a = binding._DecodeArgs()
+    for name in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "lengths", "cu", "out", "lse"):
+        setattr(a, name, 1 << 20)
+    a.blocks, a.select = (1 << 20, select) if select else (0, 0)
+    a.q_stride_t, a.q_stride_h, a.total_q, a.num_pages = heads * dim, dim, total_q, 1 << 20
+    a.block_table_cols = a.block_table_stride = columns
+    a.max_length = columns * block_size if max_length is None else max_length
+    a.dtype, a.num_seqs, a.heads, a.kv_heads, a.dim, a.block_size, a.scale = 0, num_seqs, heads, kv_heads, dim, block_size, 0.1
+    return mt.load_library().kv8_attention_workspace(ctypes.byref(a))
+
+
+def test_the_largest_bound_of_the_lengths():
+    """A bound past what the table can hold is the table's."""
+    want = decode(4, 1000)
+    assert want > 0
+    for n in (64000, 64001, 1 << 32, (1 << 63) - 64, (1 << 63) - 1):
+        assert decode(4, 1000, max_length=n) == want

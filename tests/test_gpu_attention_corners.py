@@ -132,3 +132,13 @@ def test_capture_on_a_stream_of_later_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_bounds_of_the_lengths_past_64_bits():
+    lens = [700]
+    dev = put(*build(1, lens, 1, 64, 16))
+    q = torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    want = mt.kv8_attention(q, *dev, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    for n in ((1 << 63) - 1, 1 << 63, 1 << 70):
+        got = mt.kv8_attention(q, *dev, torch.tensor(lens, dtype=torch.int32, device=DEV), max_length=n)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
