@@ -496,15 +496,16 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_pe
   for (int i = 0; i < D / 64; ++i) o[i] = 0.f;
   // 64 chunks at a time: a lane works out the weight of one, then all add the
   // chunks' values, eight loads in flight.  A chunk that added nothing may not
-  // have written any.
+  // have written any (-1); one whose weight is 0 beside the others' has, and 0
+  // times its NaN counts.
   const int share = kFour ? (used + 3) / 4 : used, end = min(used, (kFour ? wave + 1 : 1) * share);
   for (int s0 = kFour ? wave * share : 0; s0 < end; s0 += 64) {
     const int n = min(64, end - s0);
-    float f = 0.f;
+    float f = -1.f;
     if (lane < n) {
       const int64_t a = at + static_cast<int64_t>(s0 + lane) * rows_per;
       const float ll = p.part_ml[a * 2 + 1];
-      f = ll == 0.f ? 0.f : exp2_fast(p.part_ml[a * 2] - from);
+      f = ll == 0.f ? -1.f : exp2_fast(p.part_ml[a * 2] - from);
       l += ll * (ll == ll ? f : 1.f);
     }
     const float* values = p.part + (at + static_cast<int64_t>(s0) * rows_per) * D + lane * (D / 64);
@@ -516,9 +517,9 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(DecodeArgs p, int rows_pe
         for (int i = 0; i < D / 64; ++i) x[u][i] = values[static_cast<int64_t>(min(s + u, n - 1)) * rows_per * D + i];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s + u));  // 0 from n on
+        const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s + u));  // -1 from n on
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) o[i] += fs == 0.f ? 0.f : x[u][i] * fs;
+        for (int i = 0; i < D / 64; ++i) o[i] += fs < 0.f ? 0.f : x[u][i] * fs;
       }
     }
   }

@@ -142,3 +142,27 @@ def test_bounds_of_the_lengths_past_64_bits():
     for n in ((1 << 63) - 1, 1 << 63, 1 << 70):
         got = mt.kv8_attention(q, *dev, torch.tensor(lens, dtype=torch.int32, device=DEV), max_length=n)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("selected", [False, True])
+def test_nan_of_a_key_that_weighs_nothing(dtype, selected):
+    """A visible NaN counts in whatever chunk it lies: its weight is 0 in 64 bits too, and 0 times it is NaN."""
+    lens = [700]
+    kc, vc, ks, vs, table = build(1, lens, 1, 64, 16, spare=0)
+    kc[:] = 0.0
+    ks[:] = 1.0
+    vc = vc.nan_to_num()
+    kc[table[0, 0], 0, 5] = 30.0
+    vc[table[0, 37], 0, 8, 3] = math.nan                       # key 600
+    q = torch.full((1, 4, 64), 8.0, dtype=dtype)               # the score of key 5 is 1920, all others' 0
+    blocks = torch.arange(44, dtype=torch.int32).expand(1, 1, 44).contiguous() if selected else None
+    want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, 16, blocks=blocks)
+    assert torch.isnan(want[0, :, 3]).all() and torch.isfinite(want).sum() == 4 * 63
+    dev = put(kc, vc, ks, vs, table)
+    top = (vc.nan_to_num() * vs[:, :, None, None]).abs().max().item()
+    for bound in (None, 1):                                    # six chunks, one chunk
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                    blocks=None if blocks is None else blocks.to(DEV), max_length=bound)
+        agree(out, want, 2.25 * torch.finfo(dtype).eps / 2 * top)
+        assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * 128 * 1930
