@@ -80,7 +80,9 @@ int kv8_append(const mi_kv8_append_args* args, hipStream_t stream);
  *
  *   q          [total_q, H, D] of `dtype`, strides as in mi_block_attention.h.
  *   out        [total_q, H, D] of `dtype`, contiguous; lse fp32 [total_q, H].
- *   scales     positive and finite; V scales count as between 2^-100 and 2^100.
+ *   scales     positive and finite; V scales count as between 2^-80 and 2^100.
+ *              Where those that one query sees lie more than 2^100 apart, keys
+ *              under the smaller ones lose their share of the weights' sum.
  *   workspace  kv8_attention_workspace() bytes, 16-byte aligned, need not be
  *              cleared; calls that overlap in time need one each.
  */

@@ -28,7 +28,9 @@ namespace miattn {
 namespace {
 
 constexpr int kSeg = 256;          // blocks whose page numbers and scales are in LDS at a time
-constexpr float kLeast = 0x1p-100f, kMost = 0x1p100f;  // V scales are held between these
+// V scales are held between these: 2^30 weights of up to 2^14, divided by the
+// least, stay within fp32
+constexpr float kLeast = 0x1p-80f, kMost = 0x1p100f;
 
 struct DecodeArgs {
   const void* q;
@@ -234,6 +236,10 @@ __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ?
   // the last key that any row sees
   const int most = static_cast<int>(rw.pos + rw.tokens - 1 < rw.len ? rw.pos + rw.tokens - 1 : rw.len - 1);
 
+  // A weight is rounded once, to the type of q, relative to m: fp16 has no bits
+  // below 2^-24, so there m stays 2^14 under the largest exponent and the weights
+  // go up to 2^14 (bf16 has the exponents of fp32)
+  constexpr float kRoom = __is_same(T, Fp16) ? 14.f : 0.f;
   f32x4 acc[MT][D / 16];
   float m[MT], sum[MT];
 #pragma unroll
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ?
             s[t][h][r] = y;
             top = fmaxf(top, y);
           }
-        top = quad_max(top);
+        top = quad_max(top) - kRoom;
         if (__any(top > m[t])) {
           const float now = fmaxf(m[t], top);
           const float shrink = now == -kInf ? 1.f : exp2_fast(m[t] - now);

@@ -166,3 +166,45 @@ def test_nan_of_a_key_that_weighs_nothing(dtype, selected):
                                     blocks=None if blocks is None else blocks.to(DEV), max_length=bound)
         agree(out, want, 2.25 * torch.finfo(dtype).eps / 2 * top)
         assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * 128 * 1930
+
+
+def test_many_small_weights():
+    """800000 keys that each weigh 2^-26 of the first one, in one chunk: together more than fp16's step.  Weights are
+    held to 2^-39 of a wavefront's largest one, which over 2^20 keys is 2^-19 max|v|, within the quarter.  A wavefront adds
+    up 12500 groups of weights in 32 bits: 12500 * 2^-24, relative, of the sum."""
+    lens = [800_000]
+    pages = lens[0] // 128
+    kc, vc = torch.zeros(pages, 1, 128, 64), torch.ones(pages, 1, 128, 64)
+    kc[0, 0, 0], vc[0, 0, 0] = 2.25, 0.0
+    ks = vs = torch.ones(pages, 1)
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    q = torch.ones(1, 1, 64, dtype=F16)                        # scores 18 and 0: 2^26 to 1
+    want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, 128)
+    dev = put(kc, vc, ks, vs, table)
+    for bound in (1, None):
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV), max_length=bound)
+        allowed = (2.25 * 2.0 ** -11 + 12500 * 2.0 ** -24) * want
+        assert ((out.cpu().double() - want).abs() <= allowed).all(), (out[0, 0, 0].item(), want[0, 0, 0].item())
+        assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * (128 * 28 + 12500)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("scale", [2.0 ** -80, 2.0 ** -60, 2.0 ** 100])
+def test_the_least_and_largest_value_scales(dtype, scale):
+    """Sums of weights that are divided by the scale, over 20000 keys in one chunk: in fp32's range."""
+    lens = [20000]
+    kc, vc, ks, vs, table = build(3, lens, 1, 64, 128)
+    vs[:] = scale
+    q = (2 * torch.randn(1, 4, 64, generator=torch.Generator().manual_seed(5))).to(dtype)
+    want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, 128)
+    dev = put(kc, vc, ks, vs, table)
+    top = (vc.nan_to_num() * vs[:, :, None, None]).abs().max().item()
+    smax = (q.double().norm(dim=2).max() * (kc.nan_to_num() * ks[:, :, None, None]).double().norm(dim=3).max() / 8).item()
+    for bound in (None, 1):
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV), max_length=bound)
+        if dtype == BF:
+            assert (out.cpu().double() - want).abs().max().item() <= 2.25 * 2.0 ** -8 * top
+        else:
+            assert ((out == 0) if scale < 1 else torch.isinf(out)).all()      # fp16 has neither these values nor a step that near 0
+        # the logarithm of the sum and the maximum carry that of the scale: up to 80 ln 2 beside the score
+        assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * 128 * (smax + 10 + 70)
