@@ -381,9 +381,10 @@ def block_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     """Gradients ``(dq, dk, dv)`` of ``block_attention`` for the gradient ``dout``
     of its ``out``; ``out`` and ``lse`` as it returned them, the rest as it was
     called; ``rest`` as ``block_attention`` filled it in (without it dq loses
-    precision).  The result is the same from run to run.  With float16 the scores'
-    gradients are held in float16: below about 6e-8 they are lost (scale the
-    loss).  The gradients are constants: nothing goes back through them."""
+    precision).  The result is the same from run to run.  With float16 the
+    probabilities and the scores' gradients are held in float16: below about 6e-8
+    they are lost (to dv; to dq and dk, unless the loss is scaled).  The gradients
+    are constants: nothing goes back through them."""
     a = _attention_args(q, k, v, blocks, block_size, cu_seqlens, cu_seqlens_k, scale, causal)
     _, _, _, a.dout_stride_t, a.dout_stride_h = _heads(dout, "dout", q.device, q.dtype, q.shape[2])
     if dout.shape != q.shape:

@@ -43,10 +43,17 @@ struct Shared {
   Select sel;
 };
 
+// A weight is rounded once, to the type of q.  fp16 has no bits below 2^-24, so
+// there the weights are relative to a maximum 2^7 below the row's: with the 2^8
+// that the maximum may lag behind they go up to 2^15 (bf16 has fp32's exponents).
+template <typename T>
+constexpr float kRoom = __is_same(T, Fp16) ? 7.f : 0.f;
+
 // A row's output, divided by the sum of its weights: lane half `half` has the
-// columns 32 i + 8 (r / 4) + 4 half + r % 4 in acc[i][r].
+// columns 32 i + 8 (r / 4) + 4 half + r % 4 in acc[i][r].  A weight of 1 counts
+// as `one` in the sum.
 template <typename T, int D, bool kRest>
-__device__ __forceinline__ void store_row(const Args& p, int64_t tok, int head, int half, const f32x16 (&acc)[D / 32], float m, float sum) {
+__device__ __forceinline__ void store_row(const Args& p, int64_t tok, int head, int half, const f32x16 (&acc)[D / 32], float m, float sum, float one) {
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t to_at = (tok * p.heads + head) * (2 * D) + half * 8;
   char* to = static_cast<char*>(p.out) + to_at;
@@ -65,7 +72,7 @@ __device__ __forceinline__ void store_row(const Args& p, int64_t tok, int head, 
         *reinterpret_cast<u32x2*>(static_cast<char*>(p.rest) + to_at + i * 64 + (r >> 2) * 16) = z;
       }
     }
-  if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : (m == kInf ? kInf : m * p.scale + __logf(sum));
+  if (half == 0) p.lse[tok * p.heads + head] = sum == 0.f ? -kInf : (m == kInf ? kInf : m * p.scale + __logf(sum / one));
 }
 
 // The rows of the workgroup once more, key by key, with what a row does not see
@@ -129,7 +136,7 @@ __device__ __forceinline__ void one_by_one(const Args& p, Select& sel) {
       }
     }
   }
-  if (valid) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
+  if (valid) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum, 1.f);
 }
 
 // Called, it costs a short call nothing (inline: 20 us instead of 18 for 517
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
       }
       kin.load(kbase, p.k_t * 2, after, g.len_k);
       vin.load(vbase, p.v_t * 2, after, g.len_k);
-      const float base = m == -kInf ? 0.f : m * c;
+      const float base = m == -kInf ? 0.f : m * c - kRoom<T>;
       u32x4 pr[2 * kParts];
 #pragma unroll
       for (int i = 0; i < 2 * kParts; ++i) {
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) block_attention_kernel(A
     else one_by_one_called<T, D>((const Args*)__builtin_amdgcn_kernarg_segment_ptr(), &sh.sel);
     return;
   }
-  if (valid && last) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum);
+  if (valid && last) store_row<T, D, kRest>(p, tok, head, half, acc, m, sum, kRoom<T> > 0.f ? 128.f : 1.f);
 }
 
 template <typename T, int D, bool kSplit>

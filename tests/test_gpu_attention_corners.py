@@ -208,3 +208,26 @@ def test_the_least_and_largest_value_scales(dtype, scale):
             assert ((out == 0) if scale < 1 else torch.isinf(out)).all()      # fp16 has neither these values nor a step that near 0
         # the logarithm of the sum and the maximum carry that of the scale: up to 80 ln 2 beside the score
         assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * 128 * (smax + 10 + 70)
+
+
+@pytest.mark.parametrize("heads", [1, 128])
+def test_many_small_weights_of_selected_blocks(heads):
+    """131072 keys that each weigh 2^-26 of the first one, the most that a query can select: together more than fp16's
+    step.  Weights are held to 2^-32 of the largest one, which over 2^17 keys is 2^-15 max|v|; a lane adds up 8192
+    groups of weights in 32 bits."""
+    t = 131072
+    q = torch.ones(1, heads, 64, dtype=F16)
+    k, v = torch.zeros(t, 1, 64, dtype=F16), torch.ones(t, 1, 64, dtype=F16)
+    k[0], v[0] = 2.25, 0.0                                     # scores 18 and 0
+    blocks = torch.arange(1024, dtype=torch.int32).expand(1, 1, 1024).contiguous()
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (1, t))
+    want = (t - 1) / (math.exp(18) + t - 1)
+    want_lse = math.log(math.exp(18) + t - 1)
+    leaves = [x.to(DEV).requires_grad_() for x in (q, k, v)]
+    out, lse = mt.block_attention(*leaves, blocks.to(DEV), 128, cu_seqlens=cu_q, cu_seqlens_k=cu_k)
+    with torch.no_grad():
+        plain, plain_lse = mt.block_attention(*leaves, blocks.to(DEV), 128, cu_seqlens=cu_q, cu_seqlens_k=cu_k)
+    allowed = (2.25 * 2.0 ** -11 + 8192 * 2.0 ** -24) * want + 2.0 ** -15
+    for o, l in ((out, lse), (plain, plain_lse)):
+        assert ((o.detach().cpu().double() - want).abs() <= allowed).all(), (o[0, 0, 0].item(), want)
+        assert ((l.cpu().double() - want_lse).abs() <= 2.0 ** -24 * (128 * 28 + 8192)).all()
