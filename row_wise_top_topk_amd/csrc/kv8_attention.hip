@@ -48,6 +48,7 @@ struct DecodeArgs {
   float* part_ml;
   int64_t q_t, q_h, total_q, num_pages, table_stride, slots;
   int32_t table_cols, num_seqs, heads, kv_heads, group, bs, lb, select, tokens_per, head_chunks, splits, chunk;
+  int32_t spread;  // splits is 2^spread, or -1
   float scale;
 };
 
@@ -188,12 +189,19 @@ template <typename T, int D, int MT>
 __global__ void __launch_bounds__(256, D == 128 ? (MT == 4 ? 1 : 2) : (MT == 4 ? 2 : 3)) kv8_attention_kernel(DecodeArgs p) {
   constexpr int R = MT * 16;
   __shared__ __attribute__((aligned(16))) DecodeShared<D> sh;
-  // Consecutive workgroups go to the eight dies in turn.  The later chunks of a
-  // short sequence are empty: without the shift an even number of chunks would
-  // give a die the same ones of every sequence (64 sequences of 500 to 32000
-  // keys, 8 chunks: 413 us instead of 546, with the join).
+  // Consecutive workgroups go to the eight dies in turn, and on each to its four
+  // engines.  The later chunks of a short sequence are empty: without the shift
+  // an even number of chunks would give a die the same ones of every sequence (64
+  // sequences of 500 to 32000 keys, 8 chunks: 413 us instead of 546, with the
+  // join).  Few chunks (2^spread) are shifted by the bits of the item above those
+  // that choose the engine.
   const uint32_t item = blockIdx.x / p.splits;
-  const int split = static_cast<int>((blockIdx.x + item + (item >> 1) + (item >> 2)) % p.splits);
+  uint32_t shift = item + (item >> 1) + (item >> 2);
+  if (p.spread >= 0) {
+    shift = item >> max(0, 5 - p.spread);
+    shift ^= (shift >> p.spread) ^ (shift >> min(31, 2 * p.spread));
+  }
+  const int split = static_cast<int>((blockIdx.x + shift) % p.splits);
   const Rows rw = rows_of(p, item, R);
   if (rw.tokens == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -575,7 +583,7 @@ int launch_decode(const DecodeArgs& p, int mt, hipStream_t stream) {
 }
 
 struct Plan {
-  int mt, tokens_per, head_chunks, splits, chunk;
+  int mt, tokens_per, head_chunks, splits, chunk, spread;
   int64_t slots, items;
   uint64_t bytes;
 };
@@ -584,7 +592,12 @@ struct Plan {
 // tokens of a sequence where it reads its whole cache; one token's heads where
 // each token selects its own blocks), 64 at most.  Chunks: about four
 // workgroups for each of the 256 compute units, chunks of 128 keys at least
-// and 4096 at most, so that long and short sequences of a batch even out.
+// and 4096 at most, so that long and short sequences of a batch even out; longer
+// ones where the chunks' partial results would pass kMostRows rows: there are
+// many workgroups then, and the results would outgrow the output many times
+// (8192 tokens, 64/8 heads, a table for 131072 keys: 8.7 GB).
+constexpr int64_t kMostRows = 1 << 19;
+
 Plan make_plan(const mi_kv8_attention_args* a) {
   Plan p;
   const int group = a->heads / a->kv_heads;
@@ -605,6 +618,17 @@ Plan make_plan(const mi_kv8_attention_args* a) {
   const int64_t want = p.items > 0 ? (1024 + p.items - 1) / p.items : 1;  // chunks of an item
   int64_t chunk = (most + want - 1) / want;
   chunk = chunk < least ? least : (chunk > top ? top : chunk);
+  // sequences of few tokens leave up to half of the slots empty: with a multiple of
+  // 32 workgroups a slot those do not fall on the same engines
+  int64_t splits_most = 1;
+  if (p.tokens_per > 1 && p.slots < 8 * static_cast<int64_t>(a->num_seqs))
+    while (splits_most < 32 && (a->kv_heads * p.head_chunks * splits_most) % 32 != 0) splits_most *= 2;
+  while (p.items > 0 && p.items * p.mt * 16 * splits_most * 2 <= kMostRows) splits_most *= 2;
+  p.spread = -1;
+  if (chunk * splits_most < most) {
+    chunk = (most + splits_most - 1) / splits_most;
+    p.spread = (most + chunk - 1) / chunk == splits_most ? __builtin_ctz(static_cast<unsigned>(splits_most)) : -1;
+  }
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((most + chunk - 1) / chunk);
   p.bytes = p.splits > 1 ? static_cast<uint64_t>(p.items) * p.splits * p.mt * 16 * (a->dim + 2) * 4 : 0;
@@ -662,7 +686,7 @@ MI_ATTN_EXPORT int kv8_attention(const mi_kv8_attention_args* a, hipStream_t str
   p.num_seqs = a->num_seqs; p.heads = a->heads; p.kv_heads = a->kv_heads; p.group = a->heads / a->kv_heads;
   p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
   p.select = a->select; p.tokens_per = plan.tokens_per; p.head_chunks = plan.head_chunks; p.splits = plan.splits;
-  p.chunk = plan.chunk; p.scale = a->scale;
+  p.chunk = plan.chunk; p.spread = plan.spread; p.scale = a->scale;
   if (a->dtype == MI_ATTN_BF16)
     return a->dim == 128 ? launch_decode<Bf16, 128>(p, plan.mt, stream) : launch_decode<Bf16, 64>(p, plan.mt, stream);
   return a->dim == 128 ? launch_decode<Fp16, 128>(p, plan.mt, stream) : launch_decode<Fp16, 64>(p, plan.mt, stream);

@@ -97,3 +97,26 @@ def test_the_largest_bound_of_the_lengths():
     assert want > 0
     for n in (64000, 64001, 1 << 32, (1 << 63) - 64, (1 << 63) - 1):
         assert decode(4, 1000, max_length=n) == want
+
+
+def test_the_workspace_of_many_tokens_is_bounded():
+    """Many new tokens fill the card by themselves: their chunks are longer, so that the partial results stay below a
+    fixed size whatever the table can hold (2^19 rows of dim + 2 floats), and a large call needs none.  Where sequences
+    have few tokens there may be 32 results for each row."""
+    bound = (1 << 19) * (128 + 2) * 4
+    for columns in (1, 100, 2048, 14063, (1 << 24) - 1):        # pages of 64: up to 2^30 tokens
+        for total_q in (1, 7, 64, 500, 2048, 4095, 8192, 32768, 1 << 20):
+            for heads, kv in ((64, 8), (8, 8), (128, 1), (32, 2), (30, 3)):
+                for seqs in (1, 3, 64, 1024):
+                    for select in (0, 32):
+                        if seqs <= total_q:
+                            got = decode(total_q, columns, heads=heads, kv_heads=kv, num_seqs=seqs, select=select)
+                            rows = total_q * heads + 2 * 128 * kv * seqs if total_q < 64 * seqs else 0
+                            assert got <= max(bound, 32 * rows * 130 * 4), (columns, total_q, heads, kv, seqs, select, got)
+    for total_q in (8192, 32768):
+        for columns in (2048, 14063):
+            assert decode(total_q, columns) <= 2 * total_q * 64 * 128
+    for heads, seqs in ((8, 0), (64, 0), (64, 3), (1024, 2)):
+        assert decode(0, 2048, heads=heads, num_seqs=seqs) <= bound
+    # a decode batch keeps its chunks
+    assert decode(64, 500, num_seqs=64) == (64 // 2 + 64 + 1) * 8 * 8 * 16 * 130 * 4
