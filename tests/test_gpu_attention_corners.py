@@ -231,3 +231,144 @@ def test_many_small_weights_of_selected_blocks(heads):
     for o, l in ((out, lse), (plain, plain_lse)):
         assert ((o.detach().cpu().double() - want).abs() <= allowed).all(), (o[0, 0, 0].item(), want)
         assert ((l.cpu().double() - want_lse).abs() <= 2.0 ** -24 * (128 * 28 + 8192)).all()
+
+
+def windows(seed, t, h, hk, d, few, dtype):
+    """t queries at the end of 17600 keys in blocks of 16: 1100 block numbers, more than a workgroup's window of them
+    at any number of tokens (2048 words of token bits, one a block for 32 tokens).  Only the tokens of ``few`` select
+    anything, half of it on each side of the borders at 512 and 1024."""
+    keys = 17600
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(t, h, d, generator=g).to(dtype)
+    k, v = (torch.randn(keys, hk, d, generator=g).to(dtype) for _ in range(2))
+    dout = torch.randn(t, h, d, generator=g).to(dtype)
+    blocks = torch.full((t, hk, 12), -1, dtype=torch.int32)
+    for r in few:
+        for c in range(hk):
+            pick = [511, 512, 1023, 1024, 1055] + torch.randint(0, 1056, (6,), generator=g).tolist()
+            blocks[r, c, :11] = torch.tensor(pick, dtype=torch.int32)[torch.randperm(11, generator=g)]
+            blocks[r, c, 11] = (keys - t + r) // 16
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32) for n in (t, keys))
+    return q, k, v, dout, blocks, cu_q, cu_k
+
+
+WINDOWS = [
+    # tokens, heads, kv_heads, dim, tokens that select, type
+    (40, 2, 2, 64, range(40), BF),                             # 64 rows a workgroup: windows of 1024 block numbers
+    (600, 1, 1, 128, range(0, 600, 37), F16),
+    (70, 16, 2, 128, range(0, 70, 3), BF),                     # several heads a group: one window
+    (3200, 16, 16, 128, range(2005, 3200, 149), BF),              # 416 workgroups of 128 rows: windows of 512
+]
+
+
+@pytest.mark.parametrize("hidden", [False, True])
+@pytest.mark.parametrize("case", WINDOWS, ids=[str(i) for i in range(len(WINDOWS))])
+def test_windows_of_block_numbers(case, hidden):
+    """Blocks in several windows, forward and gradient; with NaN at a key that few see, so that the walk key by key
+    passes the borders too."""
+    t, h, hk, d, few, dtype = case
+    q, k, v, dout, blocks, cu_q, cu_k = windows(3, t, h, hk, d, few, dtype)
+    few = list(few)
+    if hidden:
+        blocks[few[1:]] = torch.where(blocks[few[1:]] == 1024, -1, blocks[few[1:]])
+        blocks[few[0], :, 0] = 1024
+        k[1024 * 16 + 3, 0, 5], v[1024 * 16 + 9, hk - 1, 7] = math.nan, math.nan
+    dout[[r for r in range(t) if r not in set(few)]] = 0.0
+    want, want_lse, *wants, sizes = oracle.attention(q, k, v, blocks, 16, cu_q, cu_k, dout=dout)
+    leaves = [x.to(DEV).requires_grad_() for x in (q, k, v)]
+    args = dict(cu_seqlens=cu_q.to(DEV), cu_seqlens_k=cu_k.to(DEV))
+    out, lse = mt.block_attention(*leaves, blocks.to(DEV), 16, **args)
+    with torch.no_grad():
+        plain, plain_lse = mt.block_attention(*leaves, blocks.to(DEV), 16, **args)
+    u = torch.finfo(dtype).eps / 2
+    if not hidden:
+        for o, l in ((out, lse), (plain, plain_lse)):
+            check_out(o.detach(), want, l, want_lse, v, 80, d, dtype)
+    else:
+        assert torch.isnan(want).any() and torch.isfinite(want[few[1:]]).all()
+        for o in (out, plain):
+            agree(o.detach(), want, 2.25 * u * v.nan_to_num().abs().max().item())
+    step = 2.0 ** -24 * (h // hk) * len(few) * 8 if dtype == F16 else 0.0
+    for got, w, s in zip(torch.autograd.grad(out, leaves, dout.to(DEV)), wants, sizes):
+        agree(got, w, 1.25 * u * (s + w.abs()) + step + 1e-30)
+
+
+def picks(g, select, nb, rows, hk):
+    """Rows of ``select`` entries: block numbers in any order with repeats, and some that name no block."""
+    out = torch.empty(rows, hk, select, dtype=torch.int32)
+    for r in range(rows):
+        for c in range(hk):
+            row = torch.randperm(nb, generator=g)[:select]
+            if r % 2 == 0:
+                row[select // 2:] = row[torch.randint(0, select // 2, (select - select // 2,), generator=g)]
+                row[torch.randperm(select, generator=g)[:7]] = torch.tensor([-1, nb, -(1 << 31), (1 << 31) - 1, -5, nb + 3, 0])
+            elif r % 4 == 1:
+                row = row.sort()[0]
+            out[r, c] = row.to(torch.int32)
+    return out
+
+
+@pytest.mark.parametrize("select", [255, 256, 257, 700, 1024])
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_many_selected_blocks_of_a_cache(select, dtype):
+    """Selections of more entries than a workgroup has threads, up to the limit; many chunks and one."""
+    lens = [20000, 17001]
+    kc, vc, ks, vs, table = build(6, lens, 2, 64, 16)
+    g = torch.Generator().manual_seed(select)
+    q = (2 * torch.randn(5, 4, 64, generator=g)).to(dtype)
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32)
+    blocks = picks(g, select, 1250, 5, 2)
+    want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, 16, cu, blocks)
+    dev = put(kc, vc, ks, vs, table)
+    for bound in (None, 1):
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV), cu_seqlens=cu.to(DEV),
+                                    blocks=blocks.to(DEV), max_length=bound)
+        check(out, lse, want, want_lse, q, kc, vc, ks, vs, 64, dtype)
+
+
+@pytest.mark.parametrize("select", [257, 1024])
+@pytest.mark.parametrize("h,hk,dtype", [(4, 2, BF), (32, 1, F16)])
+def test_many_selected_blocks(select, h, hk, dtype):
+    g = torch.Generator().manual_seed(select)
+    q, k, v, _, cu_q, cu_k = make(2, [5, 3], [20000, 17001], h, hk, 64, 16, 1, dtype)
+    dout = torch.randn(q.shape, generator=g).to(dtype)
+    blocks = picks(g, select, 1250, 8, hk)
+    want, want_lse, *wants, sizes = oracle.attention(q, k, v, blocks, 16, cu_q, cu_k, dout=dout)
+    leaves = [x.to(DEV).requires_grad_() for x in (q, k, v)]
+    out, lse = mt.block_attention(*leaves, blocks.to(DEV), 16, cu_seqlens=cu_q.to(DEV), cu_seqlens_k=cu_k.to(DEV))
+    # fp16: 2^-25 of the largest weight for each of 16384 keys at most: 2^-11 max|v|, one half step beside the 2.25
+    u = torch.finfo(dtype).eps / 2
+    top = v.abs().double().max().item()
+    assert (out.detach().cpu().double() - want).abs().max().item() <= (2.25 if dtype == BF else 3.25) * u * top
+    assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * 128 * 60
+    # and of each term of the gradients: 16384 keys of dq, with the scale; 8 tokens and a group's heads of dk and dv
+    for got, w, s, terms in zip(torch.autograd.grad(out, leaves, dout.to(DEV)), wants, sizes, (16384 / 8, 8 * h // hk, 8 * h // hk)):
+        agree(got, w, 1.25 * u * (s + w.abs()) + (2.0 ** -25 * 6 * terms if dtype == F16 else 0.0) + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("lens,new,h,hk,d,bs", [
+    ([9000, 4097], None, 8, 2, 128, 16),                        # three segments of 256 pages in one chunk; one page over
+    ([9000], [3], 24, 1, 64, 16),
+    ([40000, 300], None, 4, 1, 64, 16),                         # 313 chunks: more than the join's 4 x 64
+    ([70000], [2], 40, 1, 128, 32),
+])
+def test_long_caches(lens, new, h, hk, d, bs, dtype):
+    """Chunks of several segments of pages, joins of several rounds of chunks.  Over more than 4096 keys fp16's smallest
+    weights (2^-25 of the largest one, over n keys) add n * 2^-25 max|v| where one wavefront has them all."""
+    kc, vc, ks, vs, table = build(7, lens, hk, d, bs)
+    g = torch.Generator().manual_seed(4)
+    n = [1] * len(lens) if new is None else new
+    q = (2 * torch.randn(sum(n), h, d, generator=g)).to(dtype)
+    cu = None if new is None else torch.tensor([0] + n).cumsum(0).to(torch.int32)
+    want, want_lse = oracle.cache_attention(q, kc, vc, ks, vs, table, lens, bs, cu)
+    dev = put(kc, vc, ks, vs, table)
+    u = torch.finfo(dtype).eps / 2
+    top = (vc.nan_to_num() * vs[:, :, None, None]).abs().max().item()
+    smax = (q.double().norm(dim=2).max() * (kc.nan_to_num() * ks[:, :, None, None]).double().norm(dim=3).max() / math.sqrt(d)).item()
+    for bound in (None, 1):
+        out, lse = mt.kv8_attention(q.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                    cu_seqlens=None if cu is None else cu.to(DEV), max_length=bound)
+        allowed = 2.25 * u * top + (max(lens) / 4 * 2.0 ** -25 * top if dtype == F16 else 0.0)
+        assert (out.cpu().double() - want).abs().max().item() <= allowed
+        assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * (d + 64) * (smax + 10)
