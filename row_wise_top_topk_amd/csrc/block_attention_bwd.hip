@@ -581,12 +581,17 @@ __global__ void __launch_bounds__(256, 2) block_attention_dkv_kernel(BackArgs b)
   }
 
   // as in the forward: a row that does not see a key must not reach it as 0 times
-  // an infinity or NaN
+  // an infinity or NaN.  Places behind the block's last key do not count: their
+  // scores are 0, and e^(0 - lse) has no bound (where a sequence ends in a part of
+  // a block and lse is below -11 in fp16 or -88 in bf16)
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
+  for (int r = 0; r < 4; ++r) {
+    bool bad = false;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) odd |= !(fabsf(dk[i][r]) < kInf) || !(fabsf(dv[i][r]) < kInf);
+    for (int i = 0; i < D / 16; ++i) bad |= !(fabsf(dk[i][r]) < kInf) || !(fabsf(dv[i][r]) < kInf);
+    odd |= bad && key0 + 4 * quad + r < keys;
+  }
   if (__syncthreads_or(odd)) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) dk[i] = dv[i] = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -372,3 +372,45 @@ def test_long_caches(lens, new, h, hk, d, bs, dtype):
         allowed = 2.25 * u * top + (max(lens) / 4 * 2.0 ** -25 * top if dtype == F16 else 0.0)
         assert (out.cpu().double() - want).abs().max().item() <= allowed
         assert (lse.cpu().double() - want_lse).abs().max().item() <= 2.0 ** -24 * (d + 64) * (smax + 10)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+def test_low_scores_and_a_part_of_a_block(dtype, bs):
+    """Finite inputs whose scores are all far below 0, where the last block has few keys: right, and no slower by it."""
+    t, h, hk, d = 1037, 16, 2, 64
+    times = []
+    for low in (0.0, 120.0):
+        g = torch.Generator().manual_seed(bs)
+        q, k, v, dout = (torch.randn(t, n, d, generator=g) for n in (h, hk, hk, h))
+        q[..., 0], k[..., 0] = 16.0, -low / 2                   # all scores lower by low
+        q, k, v, dout = (x.to(dtype) for x in (q, k, v, dout))
+        blocks = torch.zeros(t, hk, 2, dtype=torch.int32)
+        blocks[..., 1] = (t - 1) // bs
+        want, want_lse, *wants, sizes = oracle.attention(q, k, v, blocks, bs, causal=False, dout=dout)
+        assert low == 0 or want_lse.max() < -100
+        args = gpu(q, k, v, blocks)
+        rest = torch.empty_like(args[0])
+        out, lse = mt.block_attention(*args, bs, causal=False, rest=rest)
+
+        def run():
+            return mt.block_attention_backward(dout.to(DEV), *args[:3], out, lse, args[3], bs, causal=False, rest=rest)
+
+        got = run()
+        u = torch.finfo(dtype).eps / 2
+        # 32-bit scores of up to 130 and their exponentials: 2^-15, relative, of each term, twice, beside the types' roundings;
+        # fp16's smallest step for each of the terms, a probability's times dout and a score's gradient's times q or k
+        step = 2.0 ** -25 * t * (h // hk) * max(16.0, low / 2) if dtype == F16 else 0.0
+        for x, w, s in zip(got, wants, sizes):
+            agree(x, w, (1.25 * u + 2.0 ** -14) * (s + w.abs()) + step + 1e-30)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        best = math.inf
+        for _ in range(5):
+            a.record()
+            for _ in range(5):
+                run()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert times[1] < 4 * times[0], times
