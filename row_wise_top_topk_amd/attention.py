@@ -412,7 +412,7 @@ class _Summing:
 
 
 _summing = weakref.WeakValueDictionary()  # by the leaf's id: held by the calls' gradient graphs
-_summing_lock = threading.Lock()
+_summing_lock = threading.RLock()  # a finalizer may call in between
 
 
 def _summed(leaves, stream: int) -> list:

@@ -14,7 +14,7 @@ import attention_oracle as oracle
 import row_wise_top_topk_amd as mt
 from test_gpu_attention_hidden import agree
 from test_gpu_block_attention import check_out, gpu, make
-from test_gpu_kv8 import build, check, put
+from test_gpu_kv8 import build, check, put, same
 
 pytestmark = pytest.mark.gpu
 
@@ -414,3 +414,31 @@ def test_low_scores_and_a_part_of_a_block(dtype, bs):
             best = min(best, a.elapsed_time(b))
         times.append(best)
     assert times[1] < 4 * times[0], times
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("bs,d", [(16, 64), (128, 128)])
+def test_append_of_more_tokens_than_lengths_or_table(dtype, bs, d):
+    """More new tokens than a sequence's length (the first ones have no place), more than its table holds (the last ones
+    have none), keys with strides of other tensors, one tensor for keys and values."""
+    lens, new = [20, 2, 40 * bs, 5], [30, 5, 2 * bs + 3, 5]
+    kc, vc, ks, vs, table = build(3, [20, 2, 3 * bs, 5], 2, d, bs)
+    lens[2] = table.shape[1] * bs + 7                           # seven past the table
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(sum(new) + 1, 5, d, generator=g).to(dtype)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32)
+    k = x[:, 1:4:2]
+    for one in (False, True):
+        v = k if one else x[:, 3:].contiguous()
+        dev = put(kc, vc, ks, vs, table)
+        mean = torch.full((kc.shape[0], 2, d), 7.0)
+        mean_dev = mean.to(DEV)
+        far = x.to(DEV)
+        mt.kv8_append(far[:, 1:4:2], far[:, 1:4:2] if one else v.to(DEV), *dev, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                      cu_seqlens=cu.to(DEV), k_mean=mean_dev)
+        want = [t.clone() for t in (kc, vc, ks, vs)]
+        oracle.append(k, v, *want, table, lens, bs, cu, mean)
+        assert all(same(a, b) for a, b in zip(dev[:2], want[:2])) and all(torch.equal(a.cpu(), b) for a, b in zip(dev[2:4], want[2:]))
+        fin = torch.isfinite(mean)
+        assert torch.equal(torch.isfinite(mean_dev.cpu()), fin)
+        assert (mean_dev.cpu() - mean)[fin].abs().max().item() <= 140 * 2.0 ** -24 * (448 * want[2]).max().item()
