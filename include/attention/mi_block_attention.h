@@ -133,7 +133,10 @@ int block_scores(const mi_block_scores_args* args, hipStream_t stream);
  *                  one).
  *   scale          positive and finite.
  * block_attention_backward() takes out, rest and lse as block_attention()
- * gave them and a workspace of block_attention_workspace() bytes (16-byte aligned).
+ * gave them and a workspace of block_attention_workspace() bytes (16-byte aligned):
+ * a bit for each token, key head and block, of one sequence or another, so it
+ * grows with the square of the tokens, and fp32 sums of block_size x D keys and
+ * values for every block and every 2048 rows (tokens x H / HK) that select.
  */
 typedef struct mi_block_attention_args {
   const void* q;

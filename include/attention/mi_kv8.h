@@ -84,7 +84,9 @@ int kv8_append(const mi_kv8_append_args* args, hipStream_t stream);
  *              Where those that one query sees lie more than 2^100 apart, keys
  *              under the smaller ones lose their share of the weights' sum.
  *   workspace  kv8_attention_workspace() bytes, 16-byte aligned, need not be
- *              cleared; calls that overlap in time need one each.
+ *              cleared; calls that overlap in time need one each.  At most 2^19
+ *              rows of D + 2 floats, or about 32 rows for each token and head where
+ *              sequences have few tokens.
  */
 typedef struct mi_kv8_attention_args {
   const void* q;

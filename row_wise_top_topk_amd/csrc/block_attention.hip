@@ -14,16 +14,20 @@
 // product's operand as they stand, with V read transposed from LDS in the order
 // in which the scores lie.
 //
-// Measured: 2048 tokens over 65536 keys, 64/4 heads of 128, 32 blocks of 64: 510
-// us, 263 TFLOP/s of the selected keys' products, 2.2 TB/s from memory; 8192
-// tokens, 32/2 heads, 16 blocks, with the gradient's second terms: 350 us.  The
-// matrix units are busy for 30 % of that; what bounds it is a tile's chain of
-// product, maximum, exponentials and product, with two wavefronts a SIMD to fill
-// each other's gaps (192 registers of operands and sums leave no room for a
-// third), and below 1000 tokens (517, 16/2 heads: 17 us) the start: 6 us to the
-// list of blocks, then a tile's chain of about 1 us.  Tried and slower: 16 rows a
+// Measured (kernel, on a card that has run for 50 ms; 13 % longer before): 2048
+// tokens over 65536 keys, 64/4 heads of 128, 32 blocks of 64: 467 us, 290 TFLOP/s
+// of the selected keys' products, 2.6 TB/s from memory; 8192 tokens, 32/2 heads,
+// 16 blocks, with the gradient's second terms: 347 us.  The matrix units are busy
+// for 19 % and 30 % of that.  Two things bound it.  A workgroup walks the union of
+// what its tokens select, 3.9 times (the second case 2.1 times) one token's blocks
+// with 8 tokens, while a wavefront's two tokens need 1.6 (1.3) times one token's:
+// in the other tiles it copies and waits.  And a tile's chain of product, maximum,
+// exponentials and product has two wavefronts a SIMD to fill each other's gaps
+// (192 registers of operands and sums leave no room for a third).  Below 1000
+// tokens (517, 16/2 heads: 17 us) it is the start: 6 us to the list of blocks,
+// then a tile's chain of about 1 us.  Tried and slower: 16 rows a
 // wavefront (350 us where 32 took 311), 256 rows a workgroup (332 and 314; the
-// chunk 639 and 546), four wavefronts sharing the keys of 32 rows for few tokens
+// first case 639 and 546), four wavefronts sharing the keys of 32 rows for few tokens
 // (517 tokens: 21 us and 18).
 #include <hip/hip_runtime.h>
 #include <math.h>

@@ -43,7 +43,9 @@ int make_args(const mi_block_attention_args* a, Args& p);
 // 64, with n workgroups of 128 (us): 8 heads a group, 128 columns: n 128: 29, 26;
 // 256: 52, 47; 376: 75, 69; 4 heads, 752: 189, 231; one head, 376: 141, 122; 512:
 // 200, 221.  64 columns, 4 heads: 256: 75, 53; 540: 70, 62; 750: 154, 151.  16
-// heads: 188: 43, 44; 256: 61, 73.
+// heads: 188: 43, 44; 256: 61, 73.  The cuts lie where the two come within 3 % of
+// each other, so next to them (64 columns at 750, 16 heads at 188) the other side
+// can be ahead by that.
 inline bool split_rows(Args& p, int dim) {
   const int64_t most = p.group > 8 ? 192 : (dim == 64 ? 640 : 384);
   if (p.slots * p.kv_heads > most || p.group > 64) return false;

@@ -17,8 +17,9 @@
 //
 // Measured on 8192 tokens, 32/2 heads of 128, 16 blocks of 64: dq 510 to 540 us,
 // dk and dv 400 to 425 us, the sums of pieces 27 us, the bits and pieces 10 us.
-// The matrix units are busy for 27 % (dq) and 24 % (dk, dv): dq is bound as the
-// forward is, by a tile's chain with two wavefronts a SIMD; dk and dv by LDS,
+// The matrix units are busy for 27 % (dq) and 25 % (dk, dv): dq is bound as the
+// forward is, by the union of its tokens' blocks and a tile's chain with two
+// wavefronts a SIMD; dk and dv by LDS,
 // whose reads (each row twice, by rows and transposed, for every 16 keys) take
 // nine tenths of the time.
 #include <hip/hip_runtime.h>
@@ -375,7 +376,8 @@ __global__ void __launch_bounds__(1024) number_pieces_kernel(BackArgs b) {
 // ---- dk, dv ----
 
 // Rows of a stage for each group of wavefronts that shares them: the more, the
-// more of the loads' time is covered (64: 410 us, 32: 600, on the case below).
+// more of the loads' time is covered (8192 tokens, 32/2 heads of 128, 16 blocks of
+// 64: 64 rows 410 us, 32 rows 600).
 template <int KW>
 constexpr int kStage = KW == 4 ? 64 : 32;
 
@@ -731,7 +733,7 @@ int launch_backward(const BackArgs& b, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads;
   const int64_t entries = p.kv_heads * b.rows;
   const int64_t pairs = p.total_q * p.kv_heads * p.select;
-  if (grid > INT32_MAX || entries > INT32_MAX || (pairs + 255) / 256 > INT32_MAX || b.max_pieces < 0) return MI_ATTN_EINVAL;
+  if (grid > INT32_MAX || entries > INT32_MAX || b.max_pieces < 0) return MI_ATTN_EINVAL;
   const int64_t words = entries * b.words;
   if (entries > 0)
     clear_bits_kernel<<<dim3(static_cast<unsigned>(words / 1024 + 1 < 4096 ? words / 1024 + 1 : 4096)), dim3(256), 0, stream>>>(b);
