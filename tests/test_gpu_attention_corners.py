@@ -442,3 +442,46 @@ def test_append_of_more_tokens_than_lengths_or_table(dtype, bs, d):
         fin = torch.isfinite(mean)
         assert torch.equal(torch.isfinite(mean_dev.cpu()), fin)
         assert (mean_dev.cpu() - mean)[fin].abs().max().item() <= 140 * 2.0 ** -24 * (448 * want[2]).max().item()
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("lens,new,h,hk,d,bs,cols", [
+    ([4300], 4200, 64, 1, 64, 128, 600),                        # a prompt: one chunk
+    ([17500], 1100, 64, 1, 64, 128, 140),                       # four chunks, the last one short
+    ([8000, 300], 1000, 32, 2, 128, 64, 2048),                  # the table holds far more than the sequences: later chunks empty
+    ([40 + 7 * (i % 40) for i in range(300)], 4, 64, 4, 64, 64, 1000),   # few tokens a sequence: eight chunks, most of them empty
+    ([9000 + i for i in range(5)] + [64] * 600, 2, 40, 1, 64, 128, 1000),
+])
+def test_calls_whose_chunks_are_limited(lens, new, h, hk, d, bs, cols, dtype):
+    """So many rows that the partial results' limit decides the chunks: some rows against 64 bits, all against the same
+    call with a bound of the lengths that gives other chunks (the same sums in another order: twice the tolerance)."""
+    seqs = len(lens)
+    g = torch.Generator().manual_seed(seqs + new)
+    lens = [max(n, new) for n in lens] if seqs > 1 and new < 10 else lens
+    kc, vc, ks, vs, table = build(7, lens, hk, d, bs)
+    wide = torch.full((seqs, cols), -7, dtype=torch.int32)
+    wide[:, :min(cols, table.shape[1])] = table[:, :cols]
+    q = (2 * torch.randn(new * seqs, h, d, generator=g)).to(dtype)
+    cu = (torch.arange(seqs + 1) * new).to(torch.int32).to(DEV)
+    dev = put(kc, vc, ks, vs, wide)
+    lengths = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out, lse = mt.kv8_attention(q.to(DEV), *dev, lengths, cu_seqlens=cu)
+    other, lse2 = mt.kv8_attention(q.to(DEV), *dev, lengths, cu_seqlens=cu, max_length=1)
+    u = torch.finfo(dtype).eps / 2
+    top = (vc.nan_to_num() * vs[:, :, None, None]).abs().max().item()
+    smax = (q.double().norm(dim=2).max() * (kc.nan_to_num() * ks[:, :, None, None]).double().norm(dim=3).max() / math.sqrt(d)).item()
+    assert torch.isfinite(out[lengths.repeat_interleave(new) >= new]).all()
+    assert (out.double() - other.double()).abs().max().item() <= 2 * 2.25 * u * top
+    few = torch.isfinite(lse)
+    assert torch.equal(few, torch.isfinite(lse2)) and (lse.double() - lse2.double())[few].abs().max().item() <= 2.0 ** -23 * (d + 64) * (smax + 10)
+    rows = sorted({0, 1, new * seqs // 2, new * seqs - 1} | set(torch.randint(0, new * seqs, (20,), generator=g).tolist()))
+    at = [r // new for r in rows]
+    each = [lens[i] - new + r % new + 1 for i, r in zip(at, rows)]
+    want, want_lse = oracle.cache_attention(q[rows], kc, vc, ks, vs, wide[at], [max(0, n) for n in each], bs)
+    for r, n in zip(range(len(rows)), each):
+        if n <= 0:
+            want[r], want_lse[r] = 0.0, -math.inf
+    assert (out[rows].cpu().double() - want).abs().max().item() <= 2.25 * u * top
+    fin = torch.isfinite(want_lse)
+    got = lse[rows].cpu().double()
+    assert torch.equal(torch.isfinite(got), fin) and (got - want_lse)[fin].abs().max().item() <= 2.0 ** -24 * (d + 64) * (smax + 10)
