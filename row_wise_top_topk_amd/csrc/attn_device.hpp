@@ -136,8 +136,9 @@ __device__ __forceinline__ int32_t cu_at(const int32_t* cu, int num, int64_t tot
 
 // For a slot that is the same in the whole wavefront: 64 sequences are looked
 // at together, and what belongs to them is loaded beside them, so that a search
-// costs about one load's time for each 64 sequences up to the one it finds.  also(i) is loaded for sequence i; what it gave
-// for the one found, and for the next, come back in x0 and x1.
+// costs about one load's time for each 64 sequences up to the one it finds.
+// also(i) is loaded for sequence i; what it gave for the one found, and for the
+// next, come back in x0 and x1.
 template <typename F>
 __device__ __forceinline__ Place place_of(const int32_t* cu, int num, int64_t total, int64_t slot, int per, F also, int32_t& x0, int32_t& x1) {
   const uint32_t extra = per == 1 ? 0 : 1, wide = static_cast<uint32_t>(per);
