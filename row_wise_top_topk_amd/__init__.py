@@ -14,9 +14,10 @@ import threading
 
 import torch
 
-from . import attention
+from . import attention, serving
 from .attention import (block_attention, block_attention_backward, block_means, block_scores, kv8_append,
                         kv8_attention)
+from .serving import chunk_attention, pages_compact, pages_copy, pages_fork, pages_grow, penalize_logits
 
 __all__ = [
     "PATH_AUTO", "PATH_LOCAL", "PATH_SPLIT", "PATH_CHUNKS", "PATH_PERSIST", "PLAN_PERSIST",
@@ -24,6 +25,7 @@ __all__ = [
     "plan_describe", "debug_keys", "workspace_error", "status_string",
     "c128a_active_width", "c128a_topk_metadata",
     "block_means", "block_scores", "block_attention", "block_attention_backward", "kv8_append", "kv8_attention",
+    "chunk_attention", "pages_fork", "pages_grow", "pages_compact", "pages_copy", "penalize_logits",
 ]
 
 PATH_AUTO, PATH_LOCAL, PATH_SPLIT, PATH_CHUNKS, PATH_PERSIST = 0, 1, 2, 3, 4
@@ -79,6 +81,7 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.c128a_topk_metadata.argtypes = [vp, i64, i32, i64, vp, vp, i64, i32, vp, i64, vp, vp, i64, i32, vp]
     lib.c128a_topk_metadata.restype = ctypes.c_int
     attention.declare(lib)
+    serving.declare(lib)
     return lib
 
 

@@ -21,7 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("topk_kernels.hip", "c128a_metadata.hip", "block_scores.hip",
                                            "block_attention.hip", "block_attention_bwd.hip", "kv8_cache.hip",
-                                           "kv8_attention.hip")]
+                                           "kv8_attention.hip", "chunk_attention.hip", "pages.hip", "logits.hip")]
 LIB = os.path.join(PKG, "libmi_topk.so")
 LIB_O1 = os.path.join(PKG, "libmi_topk_O1.so")
 ARCH = "gfx950"

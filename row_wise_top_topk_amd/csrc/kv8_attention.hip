@@ -101,23 +101,6 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {  // 16-
   return D == 128 ? row * 128 + ((chunk ^ ((row >> 1) & 7u)) << 4) : row * 64 + ((chunk ^ ((row >> 2) & 3u)) << 4);
 }
 
-template <typename T>
-__device__ __forceinline__ u32x4 widen(u32x2 c) {  // 8 codes, exactly
-  u32x4 r;
-  if constexpr (__is_same(T, Bf16)) {
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, false));
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[0], 1.0f, true));
-    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, false));
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], 1.0f, true));
-  } else {
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], 1.0f, false));
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[0], 1.0f, true));
-    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], 1.0f, false));
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[1], 1.0f, true));
-  }
-  return r;
-}
-
 template <int D>
 struct DecodeShared {
   union {

@@ -1,0 +1,557 @@
+// The pages of a paged cache: forks, growth and compaction of a block table's
+// rows, and the copies of pages that they ask for.
+//
+// A page is free where its count of holders is not above 0.  A first kernel turns
+// the counts into one bit a page (a wavefront's ballot is a word) and a number of
+// free pages for each 4096; F(p), the number of free pages below p, is then a sum
+// of those numbers and of a few words' bits, so that the r-th free page is found
+// by one wavefront in two scans, and a page's own rank by two loads.  No kernel
+// waits for another workgroup, and only counts of holders are changed by atomics
+// (integers: their order does not matter).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attention/mi_block_attention.h"
+#include "serving/mi_pages.h"
+
+#define MI_PAGES_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWords = 64;              // words of free bits of a chunk
+constexpr int kChunk = kWords * 64;     // pages of a chunk
+
+struct PagesArgs {
+  int32_t* table;
+  int32_t* lengths;
+  int32_t* refs;
+  const int32_t* in;
+  int32_t* out;
+  uint64_t* words;   // [chunks * kWords] bit set: the page is free
+  int32_t* counts;   // [chunks] free pages
+  int32_t* before;   // compact: [chunks * kWords] free pages below the word's first one
+  int32_t* asks;     // fork, grow: [rows] pages that a row asks for
+  int32_t* source;   // fork: [rows] page to copy, -1: none
+  int32_t* length;   // fork: [rows] new lengths
+  int32_t* rows_new; // fork: [rows][cols] new entries
+  int64_t pages, stride, chunks;
+  int32_t rows, cols, lb;
+};
+
+__device__ __forceinline__ int wave_scan(int x) {  // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Sum over the workgroup; every thread gets it.
+__device__ __forceinline__ int block_sum(int x, int* box) {
+  x = wave_sum(x);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) all += box[w];
+  return all;
+}
+
+__device__ __forceinline__ int length_of(const PagesArgs& p, int row) {
+  const int64_t most = static_cast<int64_t>(p.cols) << p.lb;
+  const int n = p.lengths[row];
+  return n < 0 ? 0 : (n < most ? n : static_cast<int>(most));
+}
+
+__device__ __forceinline__ int pages_of(const PagesArgs& p, int64_t tokens) { return static_cast<int>((tokens + (1 << p.lb) - 1) >> p.lb); }
+
+// Free bits and their number of chunk `chunk`.
+__device__ __forceinline__ void free_bits(const PagesArgs& p, int64_t chunk, int* box) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kMine = kWords / (kThreads / 64);
+  const int64_t first = chunk * kChunk + wave * kMine * 64 + lane;
+  int32_t held[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) held[i] = first + i * 64 < p.pages ? p.refs[first + i * 64] : 1;
+  uint64_t mine = 0;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const uint64_t bits = __ballot(held[i] <= 0);
+    if (lane == i) mine = bits;
+    count += __popcll(bits);
+  }
+  if (lane < kMine) p.words[chunk * kWords + wave * kMine + lane] = mine;
+  const int all = block_sum(lane == 0 ? count : 0, box);
+  if (threadIdx.x == 0) p.counts[chunk] = all;
+}
+
+// The place of the free page with `rank` free ones before it: chunk, word and bit.
+// For one wavefront, whose lanes agree on rank; chunk is p.chunks where there is none.
+struct Spot {
+  int64_t chunk;
+  int word, bit;
+};
+
+__device__ __forceinline__ Spot find_free(const PagesArgs& p, int64_t rank) {
+  const int lane = threadIdx.x & 63;
+  Spot s{p.chunks, 0, 0};
+  for (int64_t c0 = 0; c0 < p.chunks; c0 += 64) {
+    const int n = c0 + lane < p.chunks ? p.counts[c0 + lane] : 0;
+    const int upto = wave_scan(n);
+    const int all = __builtin_amdgcn_readlane(upto, 63);
+    if (rank >= all) {
+      rank -= all;
+      continue;
+    }
+    const int at = __ffsll(static_cast<unsigned long long>(__ballot(rank < upto))) - 1;
+    rank -= __builtin_amdgcn_readlane(upto - n, at);
+    s.chunk = c0 + at;
+    break;
+  }
+  if (s.chunk >= p.chunks) return s;
+  const uint64_t word = p.words[s.chunk * kWords + lane];
+  const int n = __popcll(word), upto = wave_scan(n);
+  const uint64_t reach = __ballot(rank < upto);
+  if (reach == 0) {  // the words are not those that were counted: another call wrote into this workspace
+    s.chunk = p.chunks;
+    return s;
+  }
+  s.word = __ffsll(static_cast<unsigned long long>(reach)) - 1;
+  const int left = static_cast<int>(rank) - __builtin_amdgcn_readlane(upto - n, s.word);
+  const uint64_t bits = static_cast<uint64_t>(__builtin_amdgcn_readlane(static_cast<int>(word), s.word)) & 0xffffffffu;
+  const uint64_t high = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(word >> 32), s.word)));
+  const uint64_t both = bits | (high << 32);
+  const bool it = ((both >> lane) & 1) && __popcll(both & ((1ull << lane) - 1)) == left;
+  s.bit = __ffsll(static_cast<unsigned long long>(__ballot(it))) - 1;
+  return s;
+}
+
+// Fork, first step: what each row becomes, beside the table, since others may
+// still read what it was.  One workgroup a row.
+__global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
+  __shared__ int s_first;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int parent = p.in[row];
+  if (parent == row) {
+    if (tid == 0) {
+      p.asks[row] = 0;
+      p.source[row] = -1;
+    }
+    return;
+  }
+  const bool ends = parent < 0 || parent >= p.rows;
+  const int length = ends ? 0 : length_of(p, parent);
+  const int whole = length >> p.lb;
+  bool part = (length & ((1 << p.lb) - 1)) != 0, holds = false;
+  int32_t* mine = p.table + row * p.stride;
+  const int32_t* from = p.table + (ends ? row : parent) * p.stride;
+  int source = -1;
+  if (part) {
+    // who keeps the parent's last page: the parent, or the first of its forks
+    if (tid == 0) s_first = p.in[parent] == parent ? -1 : row;
+    __syncthreads();
+    if (s_first >= 0) {
+      for (int i = tid; i < row; i += kThreads)
+        if (p.in[i] == parent) {
+          atomicMin(&s_first, i);
+          break;
+        }
+      __syncthreads();
+    }
+    holds = s_first == row;
+    source = from[whole];
+    if (source < 0 || source >= p.pages) {  // not there: handed on as it is
+      holds = true;
+      source = -1;
+    }
+  }
+  const int had = pages_of(p, length_of(p, row)), has = whole + (part && holds ? 1 : 0);
+  for (int c = tid; c < p.cols; c += kThreads) {
+    const int old = c < had ? mine[c] : -1, now = c < has ? from[c] : -1;
+    if (old >= 0 && old < p.pages) atomicAdd(p.refs + old, -1);
+    if (now >= 0 && now < p.pages) atomicAdd(p.refs + now, 1);
+    p.rows_new[static_cast<int64_t>(row) * p.cols + c] = now;
+  }
+  if (tid == 0) {
+    p.asks[row] = part && !holds;
+    p.source[row] = part && !holds ? source : -1;
+    p.length[row] = length;
+  }
+}
+
+// Fork, second step: the free pages, and the rows' new entries to the table.
+__global__ void __launch_bounds__(kThreads) fork_write_kernel(PagesArgs p) {
+  __shared__ int box[kThreads / 64];
+  if (blockIdx.x < p.chunks) {
+    free_bits(p, blockIdx.x, box);
+    return;
+  }
+  const int row = static_cast<int>(blockIdx.x - p.chunks);
+  if (p.in[row] == row) return;
+  for (int c = threadIdx.x; c < p.cols; c += kThreads)
+    p.table[row * p.stride + c] = p.rows_new[static_cast<int64_t>(row) * p.cols + c];
+}
+
+// Fork, third step: pages for the forks' last tokens, and lengths.  A wavefront a row.
+__global__ void __launch_bounds__(kThreads) fork_last_kernel(PagesArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const bool stays = p.in[row] == row;
+  int source = -1, page = -1;
+  int length = stays ? 0 : p.length[row];
+  if (p.asks[row] != 0) {
+    int64_t rank = 0;
+    for (int64_t i = lane; i < row; i += 64) rank += p.asks[i];
+    rank = wave_sum(static_cast<int>(rank));
+    const Spot s = find_free(p, rank);
+    source = p.source[row];
+    const int whole = length >> p.lb;
+    if (s.chunk < p.chunks) {
+      page = static_cast<int>(s.chunk * kChunk + s.word * 64 + s.bit);
+      if (lane == 0) {
+        p.refs[page] = 1;
+        p.table[row * p.stride + whole] = page;
+      }
+    } else {
+      length = whole << p.lb;
+    }
+  }
+  if (lane == 0) {
+    if (!stays) p.lengths[row] = length;
+    p.out[row * 2] = source;
+    p.out[row * 2 + 1] = page;
+  }
+}
+
+// Grow, first step: the free pages, and what each row asks for (-1: its table is
+// too narrow).
+__global__ void __launch_bounds__(kThreads) grow_ask_kernel(PagesArgs p) {
+  __shared__ int box[kThreads / 64];
+  if (blockIdx.x < p.chunks) {
+    free_bits(p, blockIdx.x, box);
+    return;
+  }
+  const int64_t row = (blockIdx.x - p.chunks) * kThreads + threadIdx.x;
+  if (row >= p.rows) return;
+  const int64_t more = p.in[row] < 0 ? 0 : p.in[row], length = length_of(p, static_cast<int>(row));
+  const int64_t want = (length + more + (1 << p.lb) - 1) >> p.lb;
+  p.asks[row] = want > p.cols ? -1 : static_cast<int>(want) - pages_of(p, length);
+}
+
+// Grow, second step: one workgroup a row, whose wavefronts share the pages that it
+// asks for.
+__global__ void __launch_bounds__(kThreads) grow_kernel(PagesArgs p) {
+  __shared__ int box[kThreads / 64];
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int asks = p.asks[row];
+  int64_t rank = 0;
+  bool fits = asks == 0;
+  if (asks > 0) {
+    int64_t sum = 0;  // (a table's entries: rows * cols can pass 32 bits, pages cannot)
+    for (int i = tid; i < row; i += kThreads) sum += max(0, p.asks[i]);
+    // saturated: what passes the number of pages fits nowhere
+    rank = block_sum(static_cast<int>(sum < p.pages ? sum : p.pages) >> 8, box);
+    const int low = block_sum(static_cast<int>(sum < p.pages ? sum : p.pages) & 255, box);
+    rank = rank * 256 + low;
+    int64_t free = 0;
+    for (int64_t c = tid; c < p.chunks; c += kThreads) free += p.counts[c];
+    free = block_sum(static_cast<int>(free), box);
+    fits = rank + asks <= free;
+  }
+  const int length = length_of(p, row), had = pages_of(p, length);
+  if (tid == 0) {
+    const int more = p.in[row] < 0 || !fits ? 0 : p.in[row];
+    p.out[row] = more;
+  }
+  __syncthreads();  // all have read the length
+  if (tid == 0 && p.out[row] > 0) p.lengths[row] = length + p.out[row];
+  if (asks <= 0 || !fits) return;
+  const int share = (asks + kThreads / 64 - 1) / (kThreads / 64);
+  int at = wave * share;
+  const int to = min(asks, at + share);
+  if (at >= to) return;
+  Spot s = find_free(p, rank + at);
+  const int64_t words_end = p.chunks * kWords;
+  int32_t* mine = p.table + row * p.stride + had;
+  for (int64_t w0 = s.chunk * kWords + s.word; at < to && w0 < words_end; w0 += 64) {
+    const uint64_t words = w0 + lane < words_end ? p.words[w0 + lane] : 0;
+    for (int i = 0; i < 64 && at < to; ++i) {
+      uint64_t bits = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(words), i))) |
+                      static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(words >> 32), i))) << 32;
+      bits &= ~0ull << s.bit;  // the first word from its place on
+      s.bit = 0;
+      const int mine_at = at + __popcll(bits & ((1ull << lane) - 1));
+      if (((bits >> lane) & 1) && mine_at < to) {
+        const int page = static_cast<int>((w0 + i) * 64 + lane);
+        mine[mine_at] = page;
+        p.refs[page] = 1;
+      }
+      at += __popcll(bits);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) free_kernel(PagesArgs p) {
+  __shared__ int box[kThreads / 64];
+  free_bits(p, blockIdx.x, box);
+}
+
+// Compact, second step: with n pages in use, page q >= n in use has the rank
+// (q - F(q)) - (n - F(n)) among those that move, a free page q < n the rank F(q)
+// among those that they move to: each writes its place in the list of moves.
+__global__ void __launch_bounds__(kThreads) compact_list_kernel(PagesArgs p) {
+  __shared__ int box[kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t chunk = blockIdx.x;
+  int lower = 0, all = 0;
+  for (int64_t c = tid; c < p.chunks; c += kThreads) {
+    const int n = p.counts[c];
+    all += n;
+    if (c < chunk) lower += n;
+  }
+  all = block_sum(all, box);
+  lower = block_sum(lower, box);
+  const int64_t used = p.pages - all;
+  const int64_t cut_chunk = used / kChunk;
+  int below = 0;  // F(used)
+  for (int64_t c = tid; c < cut_chunk; c += kThreads) below += p.counts[c];
+  if (tid < kWords && cut_chunk < p.chunks) {
+    const int64_t first = cut_chunk * kChunk + tid * 64;
+    uint64_t bits = p.words[cut_chunk * kWords + tid];
+    if (used <= first) bits = 0;
+    else if (used < first + 64) bits &= (1ull << (used - first)) - 1;
+    below += __popcll(bits);
+  }
+  below = block_sum(below, box);
+  const int64_t still = used - below;  // in use and below the cut
+  const uint64_t own = p.words[chunk * kWords + lane];
+  const int count = __popcll(own), start = wave_scan(count) - count + lower;
+  if (wave == 0) p.before[chunk * kWords + lane] = start;
+  constexpr int kMine = kWords / (kThreads / 64);
+  for (int i = 0; i < kMine; ++i) {
+    const int w = wave * kMine + i;
+    const uint64_t bits = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(own), w))) |
+                          static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(own >> 32), w))) << 32;
+    const int64_t q = chunk * kChunk + w * 64 + lane;
+    const int64_t f = __builtin_amdgcn_readlane(start, w) + __popcll(bits & ((1ull << lane) - 1));
+    const bool is_free = (bits >> lane) & 1;
+    if (q < p.pages && !is_free && q >= used) p.out[(q - f - still) * 2] = static_cast<int>(q);
+    if (q < used && is_free) p.out[f * 2 + 1] = static_cast<int>(q);
+  }
+  if (chunk == 0 && tid == 0) p.counts[p.chunks] = below;  // the number of moves
+}
+
+// Compact, third step: counts of holders, the list's end, and the rows' entries.
+__global__ void __launch_bounds__(kThreads) compact_rows_kernel(PagesArgs p, int64_t pair_blocks) {
+  const int tid = threadIdx.x;
+  const int64_t moves = p.counts[p.chunks];
+  if (blockIdx.x < pair_blocks) {
+    const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + tid;
+    if (i >= p.pages / 2) return;
+    if (i >= moves) {
+      p.out[i * 2] = p.out[i * 2 + 1] = -1;
+      return;
+    }
+    const int from = p.out[i * 2], to = p.out[i * 2 + 1];
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+    return;
+  }
+  const int row = static_cast<int>(blockIdx.x - pair_blocks);
+  if (moves == 0) return;
+  const int n = pages_of(p, length_of(p, row));
+  // the first page that moved, and its rank among the pages in use
+  const int first = p.out[0];
+  const int64_t still = first - p.before[first >> 6] - __popcll(p.words[first >> 6] & ((1ull << (first & 63)) - 1));
+  for (int c = tid; c < n; c += kThreads) {
+    const int q = p.table[row * p.stride + c];
+    if (q < first || q >= p.pages) continue;
+    const uint64_t word = p.words[q >> 6];
+    if ((word >> (q & 63)) & 1) continue;  // named, but nothing counts it
+    const int64_t f = p.before[q >> 6] + __popcll(word & ((1ull << (q & 63)) - 1));
+    p.table[row * p.stride + c] = p.out[(q - f - still) * 2 + 1];
+  }
+}
+
+struct CopyArgs {
+  char* cache[2];
+  float* scale[2];
+  float* mean;
+  const int32_t* copies;
+  int64_t num, pages, page_bytes;
+  int32_t heads, mean_floats, parts;
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// `parts` workgroups share a pair, and go on to the pair `gridDim / parts` behind it.
+__global__ void __launch_bounds__(kThreads) copy_kernel(CopyArgs p) {
+  const int tid = threadIdx.x, part = blockIdx.x % p.parts;
+  const int64_t step = gridDim.x / p.parts;
+  const int64_t each = (2 * p.page_bytes / 16 + p.parts - 1) / p.parts;  // 16-byte pieces of keys and values of a part
+  for (int64_t i = blockIdx.x / p.parts; i < p.num; i += step) {
+    const int from = p.copies[2 * i], to = p.copies[2 * i + 1];
+    if (from < 0 || from >= p.pages || to < 0 || to >= p.pages) continue;
+    const int64_t per = p.page_bytes / 16, end = min((part + 1) * each, 2 * per);
+    for (int64_t a = part * each; a < end; a += kThreads * 4) {
+      u32x4 x[4];
+      int64_t at[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        at[j] = a + j * kThreads + tid;
+        if (at[j] < end) {
+          const int v = at[j] >= per;
+          x[j] = *reinterpret_cast<const u32x4*>(p.cache[v] + from * p.page_bytes + (at[j] - v * per) * 16);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at[j] < end) {
+          const int v = at[j] >= per;
+          *reinterpret_cast<u32x4*>(p.cache[v] + to * p.page_bytes + (at[j] - v * per) * 16) = x[j];
+        }
+    }
+    if (part == 0) {
+      for (int h = tid; h < 2 * p.heads; h += kThreads) {
+        float* s = p.scale[h >= p.heads];
+        const int64_t k = h >= p.heads ? h - p.heads : h;
+        s[static_cast<int64_t>(to) * p.heads + k] = s[static_cast<int64_t>(from) * p.heads + k];
+      }
+      for (int d = tid; d < p.mean_floats; d += kThreads)
+        p.mean[static_cast<int64_t>(to) * p.mean_floats + d] = p.mean[static_cast<int64_t>(from) * p.mean_floats + d];
+    }
+  }
+}
+
+bool block_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check(const mi_pages_args* a) {
+  if (a == nullptr || !block_ok(a->block_size) || a->op < MI_PAGES_FORK || a->op > MI_PAGES_COMPACT || a->rows < 0 ||
+      a->block_table_cols < 0 || a->block_table_stride < a->block_table_cols || a->num_pages < 0 || a->num_pages > INT32_MAX ||
+      static_cast<int64_t>(a->block_table_cols) * a->block_size >= (1 << 30))
+    return MI_ATTN_EINVAL;
+  return MI_ATTN_OK;
+}
+
+int64_t chunks_of(const mi_pages_args* a) { return (a->num_pages + kChunk - 1) / kChunk; }
+
+uint64_t up16(uint64_t n) { return (n + 15) & ~uint64_t{15}; }
+
+// Lays the workspace out from `at` (which may be null); returns its size.
+uint64_t lay_out(const mi_pages_args* a, char* at, PagesArgs* p) {
+  const uint64_t chunks = chunks_of(a), rows = a->rows;
+  uint64_t n = 0;
+  auto take = [&](uint64_t bytes) {
+    char* x = at == nullptr ? nullptr : at + n;
+    n += up16(bytes);
+    return x;
+  };
+  PagesArgs none;
+  PagesArgs& q = p == nullptr ? none : *p;
+  q.words = reinterpret_cast<uint64_t*>(take(chunks * kWords * 8));
+  q.counts = reinterpret_cast<int32_t*>(take((chunks + 1) * 4));
+  q.before = nullptr;
+  q.asks = q.source = q.length = q.rows_new = nullptr;
+  if (a->op == MI_PAGES_COMPACT) q.before = reinterpret_cast<int32_t*>(take(chunks * kWords * 4));
+  else q.asks = reinterpret_cast<int32_t*>(take(rows * 4));
+  if (a->op == MI_PAGES_FORK) {
+    q.source = reinterpret_cast<int32_t*>(take(rows * 4));
+    q.length = reinterpret_cast<int32_t*>(take(rows * 4));
+    q.rows_new = reinterpret_cast<int32_t*>(take(rows * a->block_table_cols * 4));
+  }
+  return n;
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH; }
+
+}  // namespace
+
+MI_PAGES_EXPORT uint64_t pages_workspace(const mi_pages_args* args) {
+  return check(args) == MI_ATTN_OK ? lay_out(args, nullptr, nullptr) : 0;
+}
+
+MI_PAGES_EXPORT int pages_update(const mi_pages_args* a, hipStream_t stream) {
+  if (check(a) != MI_ATTN_OK) return MI_ATTN_EINVAL;
+  const bool compact = a->op == MI_PAGES_COMPACT;
+  const bool entries = a->rows > 0 && a->block_table_cols > 0;
+  if ((a->rows > 0 && (a->lengths == nullptr || (!compact && (a->given == nullptr || a->out == nullptr)))) ||
+      (entries && a->block_table == nullptr) || (a->num_pages > 0 && a->refs == nullptr) ||
+      (compact && a->num_pages > 1 && a->out == nullptr))
+    return MI_ATTN_EINVAL;
+  const void* words[] = {a->block_table, a->lengths, a->refs, a->given, a->out};
+  for (const void* x : words)
+    if (!aligned(x, 4)) return MI_ATTN_EINVAL;
+  if (!aligned(a->workspace, 16)) return MI_ATTN_EINVAL;
+  if (compact ? a->num_pages < 2 : a->rows == 0) return MI_ATTN_OK;
+  PagesArgs p;
+  const uint64_t need = lay_out(a, static_cast<char*>(a->workspace), &p);
+  if (a->workspace == nullptr || a->workspace_bytes < need) return MI_ATTN_EWORKSPACE;
+  p.table = a->block_table; p.lengths = a->lengths; p.refs = a->refs; p.in = a->given; p.out = a->out;
+  p.pages = a->num_pages; p.stride = a->block_table_stride; p.chunks = chunks_of(a);
+  p.rows = a->rows; p.cols = a->block_table_cols; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
+  const dim3 b(kThreads);
+  auto blocks = [](int64_t n) { return dim3(static_cast<unsigned>(n)); };
+  if (a->op == MI_PAGES_FORK) {
+    if (p.chunks + p.rows > INT32_MAX) return MI_ATTN_EINVAL;
+    fork_rows_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
+    fork_write_kernel<<<blocks(p.chunks + p.rows), b, 0, stream>>>(p);
+    fork_last_kernel<<<blocks((static_cast<int64_t>(p.rows) + 3) / 4), b, 0, stream>>>(p);
+  } else if (a->op == MI_PAGES_GROW) {
+    grow_ask_kernel<<<blocks(p.chunks + (static_cast<int64_t>(p.rows) + kThreads - 1) / kThreads), b, 0, stream>>>(p);
+    grow_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
+  } else {
+    const int64_t pairs = (p.pages / 2 + kThreads - 1) / kThreads;
+    if (pairs + p.rows > INT32_MAX) return MI_ATTN_EINVAL;
+    free_kernel<<<blocks(p.chunks), b, 0, stream>>>(p);
+    compact_list_kernel<<<blocks(p.chunks), b, 0, stream>>>(p);
+    compact_rows_kernel<<<blocks(pairs + (entries ? p.rows : 0)), b, 0, stream>>>(p, pairs);
+  }
+  return launched();
+}
+
+MI_PAGES_EXPORT int pages_copy(const mi_pages_copy_args* a, hipStream_t stream) {
+  if (a == nullptr || !block_ok(a->block_size) || (a->dim != 64 && a->dim != 128) || a->kv_heads < 1 || a->num < 0 ||
+      a->num > INT32_MAX || a->num_pages < 0 || a->num_pages > INT32_MAX ||
+      static_cast<int64_t>(a->kv_heads) * a->block_size * a->dim > INT32_MAX)
+    return MI_ATTN_EINVAL;
+  if ((a->num > 0 && a->copies == nullptr) ||
+      (a->num_pages > 0 && (a->k_cache == nullptr || a->v_cache == nullptr || a->k_scale == nullptr || a->v_scale == nullptr)))
+    return MI_ATTN_EINVAL;
+  if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->k_scale, 4) || !aligned(a->v_scale, 4) ||
+      !aligned(a->k_mean, 4) || !aligned(a->copies, 4))
+    return MI_ATTN_EINVAL;
+  if (a->num == 0 || a->num_pages == 0) return MI_ATTN_OK;
+  CopyArgs p;
+  p.cache[0] = static_cast<char*>(a->k_cache);
+  p.cache[1] = static_cast<char*>(a->v_cache);
+  p.scale[0] = a->k_scale;
+  p.scale[1] = a->v_scale;
+  p.mean = a->k_mean;
+  p.copies = a->copies;
+  p.num = a->num;
+  p.pages = a->num_pages;
+  p.page_bytes = static_cast<int64_t>(a->kv_heads) * a->block_size * a->dim;
+  p.heads = a->kv_heads;
+  p.mean_floats = a->k_mean == nullptr ? 0 : a->kv_heads * a->dim;
+  const int64_t pieces = (2 * p.page_bytes + 16 * kThreads - 1) / (16 * kThreads);  // a part has 4 KB at least
+  int64_t parts = (2048 + p.num - 1) / p.num;
+  if (parts > pieces) parts = pieces;
+  p.parts = static_cast<int>(parts);
+  const int64_t grid = (p.num * parts < 4096 ? p.num : (4096 + parts - 1) / parts) * parts;
+  copy_kernel<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream>>>(p);
+  return launched();
+}
