@@ -95,85 +95,119 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w, bool& odd) {
   return w;
 }
 
+// Codes of a page that is not there.
+__device__ u32x4 nothing[kTile * 128 / 16];
+
 // A tile of the context on its way to LDS: 64 keys' codes and 64 values' over
-// NW wavefronts, in registers while the tile before it is worked on.
+// NW wavefronts, in registers while the tile before it is worked on; the pages of
+// the tile behind it are looked up meanwhile.  A thread has 16 codes of each of
+// kPer rows, kStep rows apart, of the keys and of the values (or of one of them).
 template <typename T, int D, int NW, bool kWide>
 struct Codes {
-  static constexpr int kThreads = NW * 64, kLanes = D / 16, kHalf = kTile * kLanes, kUnits = 2 * kHalf / kThreads;
-  static_assert(kUnits * kThreads == 2 * kHalf, "");
-  u32x4 x[kUnits];
+  static constexpr int kThreads = NW * 64, kLanes = D / 16, kUnits = 2 * kTile * kLanes / kThreads;
+  static constexpr int kHalves = kUnits >= 2 ? 2 : 1, kPer = kUnits / kHalves, kStep = kThreads / kLanes;
+  static constexpr int kPages = kWide ? 1 : kPer;
+  static constexpr int kBuf = kTile * 2 * D;
+  static_assert(kUnits * kThreads == 2 * kTile * kLanes && kStep % 16 == 0, "");
+  u32x4 x[kHalves][kPer];
+  int32_t page[kPages];
+  uint32_t to;    // where the thread's first 8 elements go in the first buffer
+  int row;        // its first row
+  uint32_t lane;  // byte of its codes in a row
 
+  __device__ __forceinline__ explicit Codes(uint32_t base) {
+    const int tid = threadIdx.x;
+    row = (tid / kLanes) % kTile;
+    lane = (tid % kLanes) * 16;
+    to = base + tile_at<D>(row, 2 * (tid % kLanes));
+    if constexpr (kHalves == 1) to += tid / kLanes < kTile ? 0 : 2 * kBuf;
+  }
   // `at`: the tile's first key, from the first of the ne blocks that pages[] is of;
   // blocks behind the last one stand for it.
-  __device__ __forceinline__ void load(const ChunkArgs& p, int hk, const int32_t* pages, int ne, int at) {
-    const int tid = threadIdx.x;
-    int64_t base = 0;
+  __device__ __forceinline__ void look(const ChunkArgs& p, const int32_t* pages, int ne, int at) {
+#pragma unroll
+    for (int j = 0; j < kPages; ++j) page[j] = pages[min((at + (kWide ? 0 : row + j * kStep)) >> p.lb, ne - 1)];
+  }
+  // The tile has `left` keys; rows behind them stand for the last one, which all
+  // queries see.
+  __device__ __forceinline__ void load(const ChunkArgs& p, int hk, int at, int left) {
+    const int is_v = kHalves == 1 ? (__builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x)) / kLanes < kTile ? 0 : 1) : 0;
+    const uint8_t* base[kHalves];
+    const int pg0 = __builtin_amdgcn_readfirstlane(page[0]);
     if constexpr (kWide) {
-      const int64_t pg = max(0, __builtin_amdgcn_readfirstlane(pages[min(at >> p.lb, ne - 1)]));
-      base = (((pg * p.kv_heads + hk) << p.lb) + (at & (p.bs - 1))) * D;
+      const int64_t first = (((static_cast<int64_t>(pg0) * p.kv_heads + hk) << p.lb) + (at & (p.bs - 1))) * D;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) base[h] = pg0 < 0 ? reinterpret_cast<const uint8_t*>(nothing) : p.cache[is_v + h] + first;
     }
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int u = j * kThreads + tid, is_v = u / kHalf;
-      const int row = (u / kLanes) % kTile, chunk = u % kLanes;
-      if constexpr (!kWide) {
-        const int a = at + row;
-        const int64_t pg = max(0, pages[min(a >> p.lb, ne - 1)]);
-        base = (((pg * p.kv_heads + hk) << p.lb) + ((a & (p.bs - 1)) - row)) * D;
+    for (int j = 0; j < kPer; ++j) {
+      const int r = min(row + j * kStep, left - 1);
+      if constexpr (kWide) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) x[h][j] = *reinterpret_cast<const u32x4*>(base[h] + (static_cast<uint32_t>(r) * D + lane));
+      } else {
+        const int64_t first = ((static_cast<int64_t>(page[j]) * p.kv_heads + hk) << p.lb) * D;
+        const uint32_t off = static_cast<uint32_t>((at + r) & (p.bs - 1)) * D + lane;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          x[h][j] = *reinterpret_cast<const u32x4*>((page[j] < 0 ? reinterpret_cast<const uint8_t*>(nothing) : p.cache[is_v + h] + first) + off);
       }
-      x[j] = *reinterpret_cast<const u32x4*>(p.cache[is_v] + (base + (row * D + chunk * 16)));
     }
   }
-  // `left`: keys of the tile that there are; the others, and those of pages that
-  // are not there, become 0.
-  __device__ __forceinline__ void store(const ChunkArgs& p, char* k, char* v, const int32_t* pages, int ne, int at, int left) const {
-    const int tid = threadIdx.x;
+  template <int buf>
+  __device__ __forceinline__ void store() const {
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int u = j * kThreads + tid;
-      const int row = (u / kLanes) % kTile, chunk = u % kLanes;
-      u32x4 c = x[j];
-      const int e = (at + (kWide ? 0 : row)) >> p.lb;
-      if (row >= left || e >= ne || pages[min(e, ne - 1)] < 0) c = u32x4{0, 0, 0, 0};
-      char* to = u / kHalf ? v : k;
-      *reinterpret_cast<u32x4*>(to + tile_at<D>(row, 2 * chunk)) = widen<T>(u32x2{c[0], c[1]});
-      *reinterpret_cast<u32x4*>(to + tile_at<D>(row, 2 * chunk + 1)) = widen<T>(u32x2{c[2], c[3]});
-    }
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        constexpr int kApart = kStep * 2 * D;
+        *reinterpret_cast<MI_LDS u32x4*>(to + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][0], x[h][j][1]});
+        *reinterpret_cast<MI_LDS u32x4*>((to ^ 16) + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][2], x[h][j][3]});
+      }
   }
 };
 
 // A tile of the new tokens likewise.
 template <typename T, int D, int NW>
 struct Fresh {
-  static constexpr int kThreads = NW * 64, kLanes = D / 8, kHalf = kTile * kLanes, kUnits = 2 * kHalf / kThreads;
-  u32x4 x[kUnits];
+  static constexpr int kThreads = NW * 64, kLanes = D / 8, kPer = kTile * kLanes / kThreads, kStep = kThreads / kLanes;
+  static constexpr int kBuf = kTile * 2 * D;
+  static_assert(kPer * kThreads == kTile * kLanes && kStep % 16 == 0, "");
+  u32x4 x[2][kPer];
+  uint32_t to, lane;
+  int row;
 
+  __device__ __forceinline__ explicit Fresh(uint32_t base) {
+    const int tid = threadIdx.x;
+    row = tid / kLanes;
+    lane = (tid % kLanes) * 16;
+    to = base + tile_at<D>(row, tid % kLanes);
+  }
   // rows behind the chunk's last one stand for it
   __device__ __forceinline__ void load(const ChunkArgs& p, int hk, const ChunkRows& rw, int first) {
-    const int tid = threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int u = j * kThreads + tid, is_v = u / kHalf;
-      const int row = (u / kLanes) % kTile, chunk = u % kLanes;
-      const int64_t token = rw.begin + min(first + row, rw.n - 1);
-      x[j] = *reinterpret_cast<const u32x4*>(p.x[is_v] + (token * p.x_t[is_v] + hk * p.x_h[is_v]) * 2 + chunk * 16);
+    for (int h = 0; h < 2; ++h) {
+      const char* base = p.x[h] + ((rw.begin + first) * p.x_t[h] + hk * p.x_h[h]) * 2;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        x[h][j] = *reinterpret_cast<const u32x4*>(base + (__umul24(min(row + j * kStep, rw.n - 1 - first), static_cast<uint32_t>(p.x_t[h] * 2)) + lane));
     }
   }
-  // hide: some row does not see all of the tile, so that infinities and NaN among
+  // kHide: some row does not see all of the tile, so that infinities and NaN among
   // the values become 0 and are marked
-  __device__ __forceinline__ void store(char* k, char* v, bool hide, bool& odd) const {
-    const int tid = threadIdx.x;
+  template <int buf, bool kHide>
+  __device__ __forceinline__ void store(bool& odd) const {
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const int u = j * kThreads + tid;
-      const int row = (u / kLanes) % kTile, chunk = u % kLanes;
-      u32x4 c = x[j];
-      if (hide && u / kHalf) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) c[z] = finite_only<T>(c[z], odd);
+      for (int j = 0; j < kPer; ++j) {
+        u32x4 c = x[h][j];
+        if (kHide && h == 1) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) c[z] = finite_only<T>(c[z], odd);
+        }
+        *reinterpret_cast<MI_LDS u32x4*>(to + (2 * h + buf) * kBuf + j * (kStep * 2 * D)) = c;
       }
-      *reinterpret_cast<u32x4*>((u / kHalf ? v : k) + tile_at<D>(row, chunk)) = c;
-    }
   }
 };
 
@@ -246,26 +280,50 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
   constexpr float kLag = __is_same(T, Fp16) ? 3.f : 8.f, kLower = __is_same(T, Fp16) ? 12.f : 0.f;
   constexpr int kScales = kWide ? 1 : 4;
 
-  // One tile, in LDS buffer `buf`.  A row sees its keys low .. high, of the 16-key
-  // groups whose bit is set in `groups`; `part`: some row sees a part only.
-  auto work = [&](auto which, bool part, int low, int high, int groups, const float (&ck)[kScales], const float (&lv)[kScales],
-                  const float (&iv)[kScales]) {
-    constexpr int buf = decltype(which)::value;
+  // One tile, in LDS buffer `buf`.  With kPart, if `part`, a row sees its keys low ..
+  // high only.  put() writes the next tile to the other buffer (kWrites writes), get()
+  // loads the one behind it: both are spread over the step.
+  auto work = [&](auto which, auto parts, auto writes, bool part, int low, int high, const float (&ck)[kScales], const float (&lv)[kScales],
+                  const float (&iv)[kScales], auto put, auto get) {
+    constexpr int buf = decltype(which)::value, kWrites = decltype(writes)::value;
+    constexpr bool kPart = decltype(parts)::value != 0;
     f32x16 s[2];
+    {
+      u32x4 ka[2][D / 16];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
+        for (int i = 0; i < D / 16; ++i) ka[mt][i] = rd.row(buf * kBuf, mt * 32, i);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s[mt] = T::mfma32(rd.row(buf * kBuf, mt * 32, i), q[i], s[mt]);
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[mt][r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) s[mt] = T::mfma32(ka[mt][i], q[i], s[mt]);
+      }
+      put();
+      // reads of the first products' operands, then a product and a read in turn,
+      // then products and the other buffer's writes
+      constexpr int kAhead = 4, kProducts = D / 8;
+      __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+      for (int i = 0; i < kProducts - kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, (kWrites + kAhead - 1) / kAhead, 0);
+      }
     }
-    if (part) {
+    if (kPart && part) {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int at = 32 * mt + 8 * (r >> 2) + (r & 3) + 4 * half;
-          if (at < low || at > high || !((groups >> (2 * mt + (r >> 3))) & 1)) s[mt][r] = -kInf;
+          const int at = 32 * mt + 8 * (r >> 2) + (r & 3);
+          if (at < low - 4 * half || at > high - 4 * half) s[mt][r] = -kInf;
         }
     }
     float top = -kInf;
@@ -273,9 +331,9 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     for (int i = 0; i < 4; ++i) {
       float t = s[i >> 1][8 * (i & 1)];
 #pragma unroll
-      for (int r = 1; r < 8; ++r) t = fmaxf(t, s[i >> 1][8 * (i & 1) + r]);
-      if constexpr (!kWide) top = fmaxf(top, fmaf(t, ck[i], lv[i]));
-      else top = fmaxf(top, t);
+      for (int r = 1; r < 8; ++r) t = __builtin_elementwise_maximum(t, s[i >> 1][8 * (i & 1) + r]);
+      if constexpr (!kWide) t = fmaf(t, ck[i], lv[i]);
+      top = __builtin_elementwise_maximum(top, t);
     }
     if constexpr (kWide) top = fmaf(top, ck[0], lv[0]);
     top = half_max(top);
@@ -289,6 +347,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][r] *= shrink;
     }
+    get();
     const float base = m == -kInf ? 0.f : m - kLower;
     u32x4 pr[4];
 #pragma unroll
@@ -301,10 +360,16 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       for (int r = 0; r < 4; ++r) pr[i][r] = T::pack(w[2 * r], w[2 * r + 1]);
       sum = fmaf(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])), iv[kWide ? 0 : i], sum);
     }
+    u32x4 va[D / 32][4];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(rd.column((2 + buf) * kBuf, 16 * st, i), pr[st], acc[i]);
+      for (int st = 0; st < 4; ++st) va[i][st] = rd.column((2 + buf) * kBuf, 16 * st, i);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
+    read_ahead<D / 8, 4, 2>();
   };
 
   // The context, kSeg blocks' tiles at a time.
@@ -323,35 +388,36 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       const float vs = pg < 0 ? 1.f : fminf(fmaxf(p.scales[1][at], kLeast), kMost);
       sh.page[b] = pg;
       sh.ks[b] = pg < 0 ? 1.f : fmaxf(p.scales[0][at] * c, 0x1p-149f);
-      sh.lv[b] = __builtin_amdgcn_logf(vs);
+      sh.lv[b] = pg < 0 ? -kInf : __builtin_amdgcn_logf(vs);  // no weight
       sh.iv[b] = 1.f / vs;
     }
     __syncthreads();
-    Codes<T, D, NW, kWide> in;
-    auto at_of = [&](int t) { return (t - s0) * kTile + shift; };
-    auto left_of = [&](int t) { return rw.context - t * kTile; };
-    in.load(p, hk, sh.page, ne, at_of(s0));
-    in.store(p, sh.k[0], sh.v[0], sh.page, ne, at_of(s0), left_of(s0));
-    in.load(p, hk, sh.page, ne, at_of(min(s0 + 1, s1 - 1)));
+    Codes<T, D, NW, kWide> in(lds_offset(sh.k[0]));
+    auto at_of = [&](int t) { return (min(t, s1 - 1) - s0) * kTile + shift; };
+    auto left_of = [&](int t) { return rw.context - min(t, s1 - 1) * kTile; };
+    in.look(p, sh.page, ne, at_of(s0));
+    in.load(p, hk, at_of(s0), left_of(s0));
+    in.look(p, sh.page, ne, at_of(s0 + 1));
+    in.template store<0>();
+    in.load(p, hk, at_of(s0 + 1), left_of(s0 + 1));
+    in.look(p, sh.page, ne, at_of(s0 + 2));
     __syncthreads();
     auto step = [&](auto which, int t) {
       constexpr int buf = decltype(which)::value;
       float ck[kScales], lv[kScales], iv[kScales];
-      int groups = 0;
 #pragma unroll
       for (int i = 0; i < kScales; ++i) {
         const int e = min((at_of(t) + 16 * i) >> p.lb, ne - 1);
         ck[i] = sh.ks[e];
         lv[i] = sh.lv[e];
         iv[i] = sh.iv[e];
-        groups |= (sh.page[e] >= 0 ? 1 : 0) << i;
       }
-      groups = __builtin_amdgcn_readfirstlane(groups);
-      if (kWide && groups) groups = 15;
-      const int left = left_of(t), next = min(t + 1, s1 - 1);
-      if (groups != 0) work(which, left < kTile || groups != 15, 0, left - 1, groups, ck, lv, iv);
-      in.store(p, sh.k[buf ^ 1], sh.v[buf ^ 1], sh.page, ne, at_of(next), left_of(next));
-      in.load(p, hk, sh.page, ne, at_of(min(t + 2, s1 - 1)));
+      const int left = left_of(t);
+      work(which, Int<1>{}, Int<2 * decltype(in)::kUnits>{}, left < kTile, 0, left - 1, ck, lv, iv, [&] { in.template store<buf ^ 1>(); },
+           [&] {
+             in.load(p, hk, at_of(t + 2), left_of(t + 2));
+             in.look(p, sh.page, ne, at_of(t + 3));
+           });
     };
     for (int t = s0; t < s1; t += 2) {
       step(Int<0>{}, t);
@@ -364,42 +430,60 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     s0 = s1;
   }
 
-  // The new tokens.
+  // The new tokens: tiles that all rows see, and tiles that some row sees a part of.
   const int n0 = max(e0, rw.tiles_context);
   bool odd = false;
   const int least = max(rw.r0, rw.hidden);  // the first token here that sees anything
   auto first_of = [&](int t) { return (rw.first_new + t - rw.tiles_context) * kTile; };
   auto hides = [&](int t) { return first_of(t) + kTile - 1 > least || first_of(t) < rw.hidden; };
-  if (n0 < e1) {
-    Fresh<T, D, NW> in;
-    in.load(p, hk, rw, first_of(n0));
+  auto walk = [&](auto hide, int from, int to) {
+    constexpr bool kHide = decltype(hide)::value != 0;
+    Fresh<T, D, NW> in(lds_offset(sh.k[0]));
+    in.load(p, hk, rw, first_of(from));
     __syncthreads();
-    in.store(sh.k[0], sh.v[0], hides(n0), odd);
-    in.load(p, hk, rw, first_of(min(n0 + 1, e1 - 1)));
+    in.template store<0, kHide>(odd);
+    in.load(p, hk, rw, first_of(min(from + 1, to - 1)));
     __syncthreads();
     auto step = [&](auto which, int t) {
       constexpr int buf = decltype(which)::value;
-      const float ones[4] = {1.f, 1.f, 1.f, 1.f}, zeros[4] = {0.f, 0.f, 0.f, 0.f}, cs[4] = {c, c, c, c};
       float ck[kScales], lv[kScales], iv[kScales];
 #pragma unroll
       for (int i = 0; i < kScales; ++i) {
-        ck[i] = cs[i];
-        lv[i] = zeros[i];
-        iv[i] = ones[i];
+        ck[i] = c;
+        lv[i] = 0.f;
+        iv[i] = 1.f;
       }
-      const int first = first_of(t), high = sees ? mine - first : -1, next = min(t + 1, e1 - 1);
-      if (__any(high >= 0)) work(which, hides(t), rw.hidden - first, high, 15, ck, lv, iv);
-      in.store(sh.k[buf ^ 1], sh.v[buf ^ 1], hides(next), odd);
-      in.load(p, hk, rw, first_of(min(t + 2, e1 - 1)));
+      const int first = first_of(t), high = sees ? mine - first : -1;
+      auto put = [&] { in.template store<buf ^ 1, kHide>(odd); };
+      auto get = [&] { in.load(p, hk, rw, first_of(min(t + 2, to - 1))); };
+      if constexpr (kHide) {
+        auto none = [] {};
+        if (__any(high >= 0)) work(which, hide, Int<0>{}, true, rw.hidden - first, high, ck, lv, iv, none, none);
+        put();
+        get();
+      } else {
+        work(which, hide, Int<2 * decltype(in)::kPer>{}, false, 0, 0, ck, lv, iv, put, get);
+      }
     };
-    for (int t = n0; t < e1; t += 2) {
+    for (int t = from; t < to; t += 2) {
       step(Int<0>{}, t);
       __syncthreads();
-      if (t + 1 < e1) {
+      if (t + 1 < to) {
         step(Int<1>{}, t + 1);
         __syncthreads();
       }
     }
+  };
+  if (n0 < e1) {
+    // the first tile can hold hidden tokens; the last ones are not seen by the first rows
+    int from = n0, to = e1;
+    while (from < to && hides(to - 1)) --to;
+    if (from < to && hides(from)) {
+      walk(Int<1>{}, from, from + 1);
+      ++from;
+    }
+    if (from < to) walk(Int<0>{}, from, to);
+    if (to < e1) walk(Int<1>{}, to, e1);
   }
   // Infinities and NaN among the values that were left out, to the rows that see them
   if (__syncthreads_or(odd)) {
