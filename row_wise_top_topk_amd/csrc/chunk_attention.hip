@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       put();
       // reads of the first products' operands, then a product and a read in turn,
       // then products and the other buffer's writes
-      constexpr int kAhead = 4, kProducts = D / 8;
+      constexpr int kAhead = 6, kProducts = D / 8;
       __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
       for (int i = 0; i < kProducts - kAhead; ++i) {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int st = 0; st < 4; ++st) acc[i] = T::mfma32(va[i][st], pr[st], acc[i]);
-    read_ahead<D / 8, 4, 2>();
+    read_ahead<D / 8, 6, 2>();
   };
 
   // The context, kSeg blocks' tiles at a time.
@@ -526,89 +526,163 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
   }
 }
 
-// Joins the parts of a row's walk: one wavefront a row.
+// Joins the parts of the rows' walks: a wavefront takes four rows, 16 parts of each
+// at a time to work out their weights, then adds the parts up in order.
+constexpr int kJoin = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_per) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t index = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kJoin;
   const int64_t item = index / rows_per;  // slot (from the last one) and key head
-  const int row = static_cast<int>(index % rows_per);
+  const int row0 = static_cast<int>(index % rows_per);
   if (item >= p.slots * p.kv_heads) return;
   const int hk = static_cast<int>(item % p.kv_heads);
   const int64_t from_last = item / p.kv_heads;
   const ChunkRows rw = rows_of(p, p.slots - 1 - from_last);
-  const int tl = row / p.group, head = hk * p.group + row % p.group;
-  if (tl >= rw.tokens) return;
-  const bool sees = rw.r0 + tl >= rw.hidden;
+  const int rows = rw.tokens * p.group;  // those there are
+  if (row0 >= rows) return;
   const int used = min(p.splits, max(1, (rw.tiles + p.chunk - 1) / p.chunk));
-  auto at = [&](int s) { return ((from_last * p.splits + s) * p.kv_heads + hk) * rows_per + row; };
-  float base = -kInf, l = 0.f;
-  if (lane < used) {
-    base = p.part_ml[at(lane) * 2];
-    l = p.part_ml[at(lane) * 2 + 1];
-  }
-  float top = base;
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float f = base == -kInf ? 0.f : exp2_fast(base - top);
-  l *= f;
-  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-  float o[D / 64];
+  const int64_t first = (from_last * p.splits * p.kv_heads + hk) * rows_per + row0, step = static_cast<int64_t>(p.kv_heads) * rows_per;
+  const int mine = lane >> 4;  // the lane's row where weights are worked out
+  const float* ml = p.part_ml + (first + min(mine, rows - 1 - row0)) * 2;
+  float base[kSplits / 16], f[kSplits / 16], top = -kInf, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) o[i] = 0.f;
-  for (int s = 0; s < used; ++s) {
-    const float fs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) o[i] += p.part[at(s) * D + lane * (D / 64) + i] * fs;
+  for (int c = 0; c < kSplits / 16; ++c) {
+    const int s = c * 16 + (lane & 15);
+    base[c] = s < used ? ml[s * step * 2] : -kInf;
+    f[c] = s < used ? ml[s * step * 2 + 1] : 0.f;  // the sum, for now
+    top = fmaxf(top, base[c]);
   }
-  const int64_t tok = rw.begin + rw.r0 + tl;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  char* to = p.out + ((tok * p.heads + head) * D + lane * (D / 64)) * 2;
-  if constexpr (D == 128) *reinterpret_cast<uint32_t*>(to) = sees ? T::pack(o[0] * inv, o[1] * inv) : 0;
-  else *reinterpret_cast<uint16_t*>(to) = sees ? static_cast<uint16_t>(T::pack(o[0] * inv, 0.f)) : 0;
-  if (lane == 0) p.lse[tok * p.heads + head] = !sees || l == 0.f ? -kInf : (top == kInf ? kInf : (top + __builtin_amdgcn_logf(l)) * kLn2);
+  for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+#pragma unroll
+  for (int c = 0; c < kSplits / 16; ++c) {
+    const float w = base[c] == -kInf ? 0.f : exp2_fast(base[c] - top);
+    l += f[c] * w;
+    f[c] = w;
+  }
+  for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
+  float o[kJoin][D / 64];
+#pragma unroll
+  for (int r = 0; r < kJoin; ++r)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) o[r][i] = 0.f;
+  const float* values = p.part + first * D + lane * (D / 64);
+#pragma unroll
+  for (int c = 0; c < kSplits / 16; ++c) {
+    if (c * 16 >= used) break;
+    for (int s = c * 16; s < min(used, c * 16 + 16); s += 2) {
+      float x[2][kJoin][D / 64];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < kJoin; ++r)
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) x[u][r][i] = values[(min(s + u, used - 1) * step + min(r, rows - 1 - row0)) * D + i];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < kJoin; ++r) {
+          const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[c]), r * 16 + ((s + u) & 15)));
+          if (s + u < used)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) o[r][i] += x[u][r][i] * w;
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kJoin; ++r) {
+    const int row = row0 + r;
+    if (row >= rows) break;
+    const int tl = row / p.group, head = hk * p.group + row % p.group;
+    const bool sees = rw.r0 + tl >= rw.hidden;
+    const float lr = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l), r * 16));
+    const float base_r = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), r * 16));
+    const int64_t tok = rw.begin + rw.r0 + tl;
+    const float inv = lr == 0.f ? 0.f : 1.f / lr;
+    char* to = p.out + ((tok * p.heads + head) * D + lane * (D / 64)) * 2;
+    if constexpr (D == 128) *reinterpret_cast<uint32_t*>(to) = sees ? T::pack(o[r][0] * inv, o[r][1] * inv) : 0;
+    else *reinterpret_cast<uint16_t*>(to) = sees ? static_cast<uint16_t>(T::pack(o[r][0] * inv, 0.f)) : 0;
+    if (lane == 0)
+      p.lse[tok * p.heads + head] = !sees || lr == 0.f ? -kInf : (base_r == kInf ? kInf : (base_r + __builtin_amdgcn_logf(lr)) * kLn2);
+  }
 }
 
 template <typename T, int D, int NW>
-int launch_chunk(const ChunkArgs& p, hipStream_t stream) {
+void launch_walk(const ChunkArgs& p, unsigned grid, hipStream_t stream) {
+  const size_t lds = sizeof(ChunkShared<D>);
+  if (p.lb >= 6) chunk_attention_kernel<T, D, true, NW><<<dim3(grid), dim3(NW * 64), lds, stream>>>(p);
+  else chunk_attention_kernel<T, D, false, NW><<<dim3(grid), dim3(NW * 64), lds, stream>>>(p);
+}
+
+template <typename T, int D>
+int launch_chunk(const ChunkArgs& p, int waves, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads * p.splits;
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
-  const dim3 g(static_cast<unsigned>(grid)), b(NW * 64);
-  const size_t lds = sizeof(ChunkShared<D>);
-  if (p.lb >= 6) chunk_attention_kernel<T, D, true, NW><<<g, b, lds, stream>>>(p);
-  else chunk_attention_kernel<T, D, false, NW><<<g, b, lds, stream>>>(p);
+  if (waves == 8) launch_walk<T, D, 8>(p, static_cast<unsigned>(grid), stream);
+  else launch_walk<T, D, 4>(p, static_cast<unsigned>(grid), stream);
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   if (p.splits > 1) {
-    const int64_t joins = p.slots * p.kv_heads * NW * 8;
+    const int64_t joins = p.slots * p.kv_heads * waves * 8 / kJoin;
     if (joins > INT32_MAX) return MI_ATTN_EINVAL;
-    chunk_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, NW * 32);
+    chunk_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, waves * 32);
     if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   }
   return MI_ATTN_OK;
 }
 
-constexpr int kWaves = 4;
-
 struct ChunkPlan {
-  int tokens_per, splits, chunk;
+  int waves, tokens_per, splits, chunk;
   int64_t slots;
   uint64_t rows;  // rows of partial results
 };
 
+// A walk of `tiles` tiles of each of `items` workgroups, in how many parts, `most` at
+// most: the card works on `at_once` workgroups, so that their rounds count.  A
+// workgroup's start costs what kStart tiles do, the join and its launch kJoinCost.
+constexpr int kStart = 4, kJoinCost = 8;
+int parts_of(int64_t items, int64_t tiles, int64_t at_once, int64_t most) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= kSplits && (s == 1 || (s <= most && tiles >= 2 * s)); ++s) {
+    const int64_t cost = ((items * s + at_once - 1) / at_once) * ((tiles + s - 1) / s + kStart) + (s == 1 ? 0 : kJoinCost);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 ChunkPlan plan_of(const mi_chunk_attention_args* a) {
   ChunkPlan p;
-  p.tokens_per = a->cu == nullptr ? 1 : kWaves * 32 / (a->heads / a->kv_heads);
-  p.slots = slots_of(a->total, a->num_seqs, p.tokens_per);
-  const int64_t items = p.slots * a->kv_heads;
+  const int group = a->heads / a->kv_heads;
   int64_t most = (static_cast<int64_t>(a->block_table_cols) * a->block_size) + a->total;  // what a row can see
   if (a->max_length < most) most = a->max_length;
   const int64_t tiles = most / kTile + 2;
-  int64_t splits = items > 0 ? 512 / items : 1;
-  if (splits > kSplits) splits = kSplits;
-  if (splits > tiles / 4) splits = tiles / 4;
-  if (splits < 1) splits = 1;
+  auto with = [&](int waves) {
+    p.waves = waves;
+    p.tokens_per = a->cu == nullptr ? 1 : waves * 32 / group;
+    p.slots = slots_of(a->total, a->num_seqs, p.tokens_per);
+    // workgroups that have rows (of each sequence one more than whole ones, at most)
+    return (a->total / p.tokens_per + (a->total < a->num_seqs ? a->total : a->num_seqs)) * a->kv_heads;
+  };
+  const bool wide = a->dim == 128;
+  // Eight wavefronts a workgroup widen the codes once for 256 rows.  With many short
+  // sequences the rows of their last workgroups are empty, half of them in the mean:
+  // from a third as many sequences as whole workgroups on, four wavefronts.  Measured
+  // (us, eight against four): one sequence, 2048 tokens behind 16000, 32/4 heads of
+  // 64: 376, 393; 96 behind 100003, 32/2 of 128: 178, 202; four of 200 behind 900,
+  // 16/4 of 64: 26.5, 29.3; five of 890 in all, 12/3 of 64: 55.7, 49.1; 64 single
+  // tokens and 512, 32/8 of 128: 154, 100.
+  int64_t items = with(8);
+  if (a->num_seqs > 1 && 3 * static_cast<int64_t>(a->num_seqs) > a->total / p.tokens_per) items = with(4);
+  const int64_t at_once = p.waves == 8 ? 256 : (wide ? 512 : 768);
+  // partial results of 2^17 rows at most (68 MB with 128 columns)
+  const int64_t rows = p.slots * a->kv_heads * p.waves * 32;
+  const int64_t splits = items > 0 ? parts_of(items, tiles, at_once, (int64_t{1} << 17) / rows) : 1;
   p.chunk = static_cast<int>((tiles + splits - 1) / splits);
   p.splits = static_cast<int>((tiles + p.chunk - 1) / p.chunk);
-  p.rows = p.splits > 1 ? static_cast<uint64_t>(items) * p.splits * kWaves * 32 : 0;
+  p.rows = p.splits > 1 ? static_cast<uint64_t>(p.slots) * a->kv_heads * p.splits * p.waves * 32 : 0;
   return p;
 }
 
@@ -673,6 +747,6 @@ MI_ATTN_EXPORT int chunk_attention(const mi_chunk_attention_args* a, hipStream_t
   p.num_seqs = a->num_seqs; p.heads = a->heads; p.kv_heads = a->kv_heads; p.group = a->heads / a->kv_heads;
   p.bs = a->block_size; p.lb = __builtin_ctz(static_cast<unsigned>(a->block_size));
   p.tokens_per = plan.tokens_per; p.splits = plan.splits; p.chunk = plan.chunk; p.scale = a->scale;
-  if (a->dtype == MI_ATTN_BF16) return a->dim == 128 ? launch_chunk<Bf16, 128, kWaves>(p, stream) : launch_chunk<Bf16, 64, kWaves>(p, stream);
-  return a->dim == 128 ? launch_chunk<Fp16, 128, kWaves>(p, stream) : launch_chunk<Fp16, 64, kWaves>(p, stream);
+  if (a->dtype == MI_ATTN_BF16) return a->dim == 128 ? launch_chunk<Bf16, 128>(p, plan.waves, stream) : launch_chunk<Bf16, 64>(p, plan.waves, stream);
+  return a->dim == 128 ? launch_chunk<Fp16, 128>(p, plan.waves, stream) : launch_chunk<Fp16, 64>(p, plan.waves, stream);
 }

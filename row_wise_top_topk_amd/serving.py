@@ -99,20 +99,19 @@ def chunk_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: 
     lse)`` as ``kv8_attention`` does: ``[tokens, heads, dim]`` of q's type, and
     float32 ``[tokens, heads]``; a query that sees no key, and a row behind the
     last sequence, has 0 and -inf.  Neither is differentiable."""
-    a = _ChunkArgs()
-    total, heads, dim, a.q_stride_t, a.q_stride_h = _heads(q, "q")
+    total, heads, dim, q_t, q_h = _heads(q, "q")
     device = q.device
-    total_k, hk, _, a.k_stride_t, a.k_stride_h = _heads(k, "k", device, q.dtype, dim)
-    _, _, _, a.v_stride_t, a.v_stride_h = _heads(v, "v", device, q.dtype, dim)
+    total_k, hk, _, k_t, k_h = _heads(k, "k", device, q.dtype, dim)
+    _, _, _, v_t, v_h = _heads(v, "v", device, q.dtype, dim)
     if k.shape != v.shape or total_k != total:
         raise ValueError("k and v must have the same shape, with a row for each of q's")
-    if a.k_stride_t >= 1 << 23 or a.v_stride_t >= 1 << 23:
+    if k_t >= 1 << 23 or v_t >= 1 << 23:
         raise ValueError("k and v must have token strides below 2^23 elements")
     _groups(heads, hk)
     pages, _, bs, _ = _cache(k_cache, v_cache, k_scale, v_scale, device, hk, dim)
-    n, a.block_table_cols, a.block_table_stride = _table(block_table, device)
+    n, cols, table_at = _table(block_table, device)
     _cache_sequences(cu_seqlens, lengths, n, total, device)
-    most = a.block_table_cols * bs
+    most = cols * bs
     if most >= 1 << 30:
         raise ValueError("a sequence can hold less than 2^30 tokens")
     if max_length is not None and max_length < 0:
@@ -120,12 +119,11 @@ def chunk_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: 
     most += total
     out = _like(q) if out is None else _output(out, q.shape, q.dtype, device, "out")
     lse = q.new_empty((total, heads), dtype=torch.float32)
-    a.q, a.k, a.v, a.k_cache, a.v_cache = (t.data_ptr() for t in (q, k, v, k_cache, v_cache))
-    a.k_scale, a.v_scale, a.block_table, a.lengths = (t.data_ptr() for t in (k_scale, v_scale, block_table, lengths))
-    a.cu, a.out, a.lse = _ptr(cu_seqlens), out.data_ptr(), lse.data_ptr()
-    a.total, a.num_pages, a.num_seqs = total, pages, n
-    a.max_length = min(most if max_length is None else int(max_length), most, (1 << 31) - 1)
-    a.dtype, a.heads, a.kv_heads, a.dim, a.block_size, a.scale = _DTYPES[q.dtype], heads, hk, dim, bs, _scale(scale, dim)
+    a = _ChunkArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                   v_scale.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                   out.data_ptr(), lse.data_ptr(), None, 0, q_t, q_h, k_t, k_h, v_t, v_h, total, pages, table_at,
+                   min(most if max_length is None else int(max_length), most, (1 << 31) - 1), cols, _DTYPES[q.dtype], n, heads, hk, dim,
+                   bs, _scale(scale, dim))
     lib = _lib()
     a.workspace_bytes = lib.chunk_attention_workspace(ctypes.byref(a))
     if a.workspace_bytes:
@@ -140,17 +138,17 @@ def _pages(op: int, what: str, block_table, lengths, refs, given, given_what, ou
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
         raise ValueError("block_table must be on a GPU")
     device = block_table.device
-    a = _PagesArgs()
-    a.rows, a.block_table_cols, a.block_table_stride = _table(block_table, device)
-    if a.block_table_cols * bs >= 1 << 30:
+    rows, cols, table_at = _table(block_table, device)
+    if cols * bs >= 1 << 30:
         raise ValueError("a sequence can hold less than 2^30 tokens")
-    _ints(lengths, "lengths", device, 1, (a.rows,))
+    _ints(lengths, "lengths", device, 1, (rows,))
     _ints(refs, "refs", device, 1)
     if given is not None or given_what:
-        _ints(given, given_what, device, 1, (a.rows,))
-    out = block_table.new_empty(out_shape(a.rows, refs.shape[0]))
-    a.block_table, a.lengths, a.refs, a.given, a.out = (_ptr(t) for t in (block_table, lengths, refs, given, out))
-    a.num_pages, a.block_size, a.op = refs.shape[0], bs, op
+        _ints(given, given_what, device, 1, (rows,))
+    pages = refs.shape[0]
+    out = block_table.new_empty(out_shape(rows, pages))
+    a = _PagesArgs(block_table.data_ptr(), lengths.data_ptr(), refs.data_ptr(), _ptr(given), out.data_ptr(), None, 0, pages, table_at, rows,
+                   cols, bs, op)
     lib = _lib()
     a.workspace_bytes = lib.pages_workspace(ctypes.byref(a))
     workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
@@ -214,25 +212,36 @@ def pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tens
     if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
         raise ValueError("k_cache must be on a GPU")
     device = k_cache.device
-    a = _CopyArgs()
-    a.num_pages, a.kv_heads, a.block_size, a.dim = _cache(k_cache, v_cache, k_scale, v_scale, device)
+    pages, hk, bs, dim = _cache(k_cache, v_cache, k_scale, v_scale, device)
     _ints(copies, "copies", device, 2)
     if copies.shape[1] != 2:
         raise ValueError("copies must have the shape [n, 2]")
     if k_mean is not None:
-        _output(k_mean, (a.num_pages, a.kv_heads, a.dim), torch.float32, device, "k_mean")
-    a.k_cache, a.v_cache, a.k_scale, a.v_scale = (t.data_ptr() for t in (k_cache, v_cache, k_scale, v_scale))
-    a.k_mean, a.copies, a.num = _ptr(k_mean), copies.data_ptr(), copies.shape[0]
+        _output(k_mean, (pages, hk, dim), torch.float32, device, "k_mean")
+    a = _CopyArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_mean), copies.data_ptr(),
+                  copies.shape[0], pages, hk, dim, bs)
     _run(device, "pages_copy", _lib().pages_copy, ctypes.byref(a))
 
 
 def _matrix(t, what: str, dtype, device, rows: int):
     """(columns, row stride) of a 2-D operand with unit stride along its last axis."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2 or t.device != device or t.shape[0] != rows:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows:
         raise ValueError(f"{what} must be a 2-D {dtype} tensor with a row for each of the logits, on their device")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    cols = t.shape[1]
+    at, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what} must have unit stride along its last axis")
-    return int(t.shape[1]), int(t.stride(0)) if rows > 1 else 0
+    return cols, at if rows > 1 else 0
+
+
+def _row(t, what: str, dtype, device, rows: int):
+    """Address of a 1-D operand with an entry for each row, None where it is not given."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != rows
+            or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous 1-D {dtype} tensor with an entry for each row, on the logits' device")
+    return t.data_ptr()
 
 
 def penalize_logits(logits: torch.Tensor, tokens: torch.Tensor = None, lengths: torch.Tensor = None,
@@ -267,44 +276,39 @@ def penalize_logits(logits: torch.Tensor, tokens: torch.Tensor = None, lengths: 
     if not logits.is_cuda:
         raise ValueError("logits must be on a GPU")
     device = logits.device
-    a = _PenalizeArgs()
-    rows = a.rows = int(logits.shape[0])
-    a.vocab, a.logits_stride = _matrix(logits, "logits", logits.dtype, device, rows)
-    if a.logits_stride < 0:
-        raise ValueError("logits must not have a negative stride")
+    rows = logits.shape[0]
+    vocab, logits_at = _matrix(logits, "logits", logits.dtype, device, rows)
     if out is None:
-        out = torch.empty((rows, a.vocab), dtype=torch.float32, device=device)
-    elif not isinstance(out, torch.Tensor) or out.shape != logits.shape or (rows > 1 and out.stride(0) < a.vocab):
-        raise ValueError("out must be a float32 tensor of the logits' shape whose rows do not overlap")
-    _, a.out_stride = _matrix(out, "out", torch.float32, device, rows)
-    if out.data_ptr() == logits.data_ptr() and rows > 1 and a.vocab and (out.dtype != logits.dtype or a.out_stride != a.logits_stride):
-        raise ValueError("out may be the logits themselves only where both have one type and stride")
+        out = torch.empty((rows, vocab), dtype=torch.float32, device=device)
+        out_at = vocab
+    else:
+        cols, out_at = _matrix(out, "out", torch.float32, device, rows)
+        if cols != vocab or (rows > 1 and out_at < vocab):
+            raise ValueError("out must have the logits' shape, and rows that do not overlap")
+        if out.data_ptr() == logits.data_ptr() and rows > 1 and vocab and (out.dtype != logits.dtype or out_at != logits_at):
+            raise ValueError("out may be the logits themselves only where both have one type and stride")
+    said = said_at = ids = ids_at = words_at = 0
     if tokens is not None:
-        a.token_cols, a.tokens_stride = _matrix(tokens, "tokens", torch.int32, device, rows)
-        if a.token_cols > MAX_TOKENS:
+        said, said_at = _matrix(tokens, "tokens", torch.int32, device, rows)
+        if said > MAX_TOKENS:
             raise ValueError(f"tokens must have {MAX_TOKENS} columns at most")
-    elif lengths is not None or prompt_lengths is not None:
-        raise ValueError("lengths and prompt_lengths go with tokens")
-    for t, what in ((lengths, "lengths"), (prompt_lengths, "prompt_lengths")):
-        if t is not None:
-            _ints(t, what, device, 1, (rows,))
-    for t, what in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        if t is not None:
-            if tokens is None:
-                raise ValueError(f"{what} goes with tokens")
-            _output(t, (rows,), torch.float32, device, what)
+    elif not (lengths is None and prompt_lengths is None and repetition is None and presence is None and frequency is None):
+        raise ValueError("lengths, prompt_lengths, repetition, presence and frequency go with tokens")
     if (bias is None) != (bias_ids is None):
         raise ValueError("bias and bias_ids go together")
     if bias is not None:
-        a.bias_cols, a.bias_stride = _matrix(bias_ids, "bias_ids", torch.int32, device, rows)
-        if a.bias_cols > MAX_BIAS or _matrix(bias, "bias", torch.float32, device, rows) != (a.bias_cols, a.bias_stride):
+        ids, ids_at = _matrix(bias_ids, "bias_ids", torch.int32, device, rows)
+        if ids > MAX_BIAS or _matrix(bias, "bias", torch.float32, device, rows) != (ids, ids_at):
             raise ValueError(f"bias and bias_ids must have one shape and strides, with {MAX_BIAS} columns at most")
     if mask is not None:
-        words, a.mask_stride = _matrix(mask, "mask", torch.int32, device, rows)
-        if words != (a.vocab + 31) // 32:
+        words, words_at = _matrix(mask, "mask", torch.int32, device, rows)
+        if words != (vocab + 31) // 32:
             raise ValueError("mask must have (vocab + 31) // 32 columns")
-    a.logits, a.out, a.tokens, a.lengths, a.prompt_lengths = (_ptr(t) for t in (logits, out, tokens, lengths, prompt_lengths))
-    a.repetition, a.frequency, a.presence = _ptr(repetition), _ptr(frequency), _ptr(presence)
-    a.bias_ids, a.bias, a.mask, a.dtype = _ptr(bias_ids), _ptr(bias), _ptr(mask), _LOGITS[logits.dtype]
+    a = _PenalizeArgs(logits.data_ptr(), out.data_ptr(), _ptr(tokens), _row(lengths, "lengths", torch.int32, device, rows),
+                      _row(prompt_lengths, "prompt_lengths", torch.int32, device, rows),
+                      _row(repetition, "repetition", torch.float32, device, rows),
+                      _row(frequency, "frequency", torch.float32, device, rows),
+                      _row(presence, "presence", torch.float32, device, rows), _ptr(bias_ids), _ptr(bias), _ptr(mask), rows, vocab,
+                      logits_at, out_at, said_at, ids_at, words_at, said, ids, _LOGITS[logits.dtype])
     _run(device, "penalize_logits", _lib().logits_penalize, ctypes.byref(a))
     return out
