@@ -372,6 +372,79 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     read_ahead<D / 8, 6, 2>();
   };
 
+  // Number of the page of block `b` of the segment that begins with tile t; -1 where
+  // there is none.
+  auto page_at = [&](int t, int b) {
+    const int block = ((t * kTile) >> p.lb) + b;
+    if (b >= kSeg || block >= (rw.context + p.bs - 1) >> p.lb) return -1;
+    const int pg = p.table[rw.seq * p.table_stride + block];
+    return pg >= 0 && pg < p.num_pages ? pg : -1;
+  };
+  // on its way while the new tokens are worked on
+  const int first_page = e0 < rw.tiles_context ? page_at(e0, tid) : -1;
+
+  // The new tokens: tiles that all rows see, and tiles that some row sees a part of.
+  const int n0 = max(e0, rw.tiles_context);
+  bool odd = false;
+  const int least = max(rw.r0, rw.hidden);  // the first token here that sees anything
+  auto first_of = [&](int t) { return (rw.first_new + t - rw.tiles_context) * kTile; };
+  auto hides = [&](int t) { return first_of(t) + kTile - 1 > least || first_of(t) < rw.hidden; };
+  struct {
+    float ck[kScales], lv[kScales], iv[kScales];
+  } plain;
+#pragma unroll
+  for (int i = 0; i < kScales; ++i) {
+    plain.ck[i] = c;
+    plain.lv[i] = 0.f;
+    plain.iv[i] = 1.f;
+  }
+  auto walk_part = [&](int from, int to) {
+    Fresh<T, D, NW> in(lds_offset(sh.k[0]));
+    in.load(p, hk, rw, first_of(from));
+    for (int t = from; t < to; ++t) {
+      __syncthreads();
+      in.template store<0, true>(odd);
+      if (t + 1 < to) in.load(p, hk, rw, first_of(t + 1));
+      __syncthreads();
+      const int first = first_of(t), high = sees ? mine - first : -1;
+      auto none = [] {};
+      if (__any(high >= 0)) work(Int<0>{}, Int<1>{}, Int<0>{}, true, rw.hidden - first, high, plain.ck, plain.lv, plain.iv, none, none);
+    }
+    __syncthreads();
+  };
+  auto walk = [&](int from, int to) {
+    Fresh<T, D, NW> in(lds_offset(sh.k[0]));
+    in.load(p, hk, rw, first_of(from));
+    __syncthreads();
+    in.template store<0, false>(odd);
+    in.load(p, hk, rw, first_of(min(from + 1, to - 1)));
+    __syncthreads();
+    auto step = [&](auto which, int t) {
+      constexpr int buf = decltype(which)::value;
+      work(which, Int<0>{}, Int<2 * decltype(in)::kPer>{}, false, 0, 0, plain.ck, plain.lv, plain.iv,
+           [&] { in.template store<buf ^ 1, false>(odd); }, [&] { in.load(p, hk, rw, first_of(min(t + 2, to - 1))); });
+    };
+    for (int t = from; t < to; t += 2) {
+      step(Int<0>{}, t);
+      __syncthreads();
+      if (t + 1 < to) {
+        step(Int<1>{}, t + 1);
+        __syncthreads();
+      }
+    }
+  };
+  if (n0 < e1) {
+    // the first tile can hold hidden tokens; the last ones are not seen by the first rows
+    int from = n0, to = e1;
+    while (from < to && hides(to - 1)) --to;
+    if (from < to && hides(from)) {
+      walk_part(from, from + 1);
+      ++from;
+    }
+    if (from < to) walk(from, to);
+    if (to < e1) walk_part(to, e1);
+  }
+
   // The context, kSeg blocks' tiles at a time.
   const int c1 = min(e1, rw.tiles_context);
   for (int s0 = e0; s0 < c1;) {
@@ -380,23 +453,22 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     const int blocks = (rw.context + p.bs - 1) >> p.lb;
     const int s1 = min(c1, (((block0 + kSeg) << p.lb) / kTile));
     const int ne = min(kSeg, blocks - block0);
+    const int pg = s0 == e0 ? first_page : page_at(s0, tid);
     __syncthreads();
-    for (int b = tid; b < ne; b += NW * 64) {
-      int pg = p.table[rw.seq * p.table_stride + block0 + b];
-      if (pg < 0 || pg >= p.num_pages) pg = -1;
-      const int64_t at = static_cast<int64_t>(max(0, pg)) * p.kv_heads + hk;
-      const float vs = pg < 0 ? 1.f : fminf(fmaxf(p.scales[1][at], kLeast), kMost);
-      sh.page[b] = pg;
-      sh.ks[b] = pg < 0 ? 1.f : fmaxf(p.scales[0][at] * c, 0x1p-149f);
-      sh.lv[b] = pg < 0 ? -kInf : __builtin_amdgcn_logf(vs);  // no weight
-      sh.iv[b] = 1.f / vs;
-    }
+    if (tid < ne) sh.page[tid] = pg;
     __syncthreads();
     Codes<T, D, NW, kWide> in(lds_offset(sh.k[0]));
     auto at_of = [&](int t) { return (min(t, s1 - 1) - s0) * kTile + shift; };
     auto left_of = [&](int t) { return rw.context - min(t, s1 - 1) * kTile; };
     in.look(p, sh.page, ne, at_of(s0));
     in.load(p, hk, at_of(s0), left_of(s0));
+    if (tid < ne) {  // the scales come while the first codes do
+      const int64_t at = static_cast<int64_t>(max(0, pg)) * p.kv_heads + hk;
+      const float ks = p.scales[0][at], vs = pg < 0 ? 1.f : fminf(fmaxf(p.scales[1][at], kLeast), kMost);
+      sh.ks[tid] = pg < 0 ? 1.f : fmaxf(ks * c, 0x1p-149f);
+      sh.lv[tid] = pg < 0 ? -kInf : __builtin_amdgcn_logf(vs);  // no weight
+      sh.iv[tid] = 1.f / vs;
+    }
     in.look(p, sh.page, ne, at_of(s0 + 1));
     in.template store<0>();
     in.load(p, hk, at_of(s0 + 1), left_of(s0 + 1));
@@ -428,62 +500,6 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       }
     }
     s0 = s1;
-  }
-
-  // The new tokens: tiles that all rows see, and tiles that some row sees a part of.
-  const int n0 = max(e0, rw.tiles_context);
-  bool odd = false;
-  const int least = max(rw.r0, rw.hidden);  // the first token here that sees anything
-  auto first_of = [&](int t) { return (rw.first_new + t - rw.tiles_context) * kTile; };
-  auto hides = [&](int t) { return first_of(t) + kTile - 1 > least || first_of(t) < rw.hidden; };
-  auto walk = [&](auto hide, int from, int to) {
-    constexpr bool kHide = decltype(hide)::value != 0;
-    Fresh<T, D, NW> in(lds_offset(sh.k[0]));
-    in.load(p, hk, rw, first_of(from));
-    __syncthreads();
-    in.template store<0, kHide>(odd);
-    in.load(p, hk, rw, first_of(min(from + 1, to - 1)));
-    __syncthreads();
-    auto step = [&](auto which, int t) {
-      constexpr int buf = decltype(which)::value;
-      float ck[kScales], lv[kScales], iv[kScales];
-#pragma unroll
-      for (int i = 0; i < kScales; ++i) {
-        ck[i] = c;
-        lv[i] = 0.f;
-        iv[i] = 1.f;
-      }
-      const int first = first_of(t), high = sees ? mine - first : -1;
-      auto put = [&] { in.template store<buf ^ 1, kHide>(odd); };
-      auto get = [&] { in.load(p, hk, rw, first_of(min(t + 2, to - 1))); };
-      if constexpr (kHide) {
-        auto none = [] {};
-        if (__any(high >= 0)) work(which, hide, Int<0>{}, true, rw.hidden - first, high, ck, lv, iv, none, none);
-        put();
-        get();
-      } else {
-        work(which, hide, Int<2 * decltype(in)::kPer>{}, false, 0, 0, ck, lv, iv, put, get);
-      }
-    };
-    for (int t = from; t < to; t += 2) {
-      step(Int<0>{}, t);
-      __syncthreads();
-      if (t + 1 < to) {
-        step(Int<1>{}, t + 1);
-        __syncthreads();
-      }
-    }
-  };
-  if (n0 < e1) {
-    // the first tile can hold hidden tokens; the last ones are not seen by the first rows
-    int from = n0, to = e1;
-    while (from < to && hides(to - 1)) --to;
-    if (from < to && hides(from)) {
-      walk(Int<1>{}, from, from + 1);
-      ++from;
-    }
-    if (from < to) walk(Int<0>{}, from, to);
-    if (to < e1) walk(Int<1>{}, to, e1);
   }
   // Infinities and NaN among the values that were left out, to the rows that see them
   if (__syncthreads_or(odd)) {
@@ -538,19 +554,25 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_p
   if (item >= p.slots * p.kv_heads) return;
   const int hk = static_cast<int>(item % p.kv_heads);
   const int64_t from_last = item / p.kv_heads;
+  const int64_t first = (from_last * p.splits * p.kv_heads + hk) * rows_per + row0, step = static_cast<int64_t>(p.kv_heads) * rows_per;
+  // maxima and sums are loaded before it is known which of them were written
+  const float* ml = p.part_ml + (first + (lane >> 4)) * 2;  // the lane's row where weights are worked out
+  f32x2 both[kSplits / 16];
+#pragma unroll
+  for (int c = 0; c < kSplits / 16; ++c) {
+    const int s = c * 16 + (lane & 15);
+    both[c] = s < p.splits ? *reinterpret_cast<const f32x2*>(ml + s * step * 2) : f32x2{-kInf, 0.f};
+  }
   const ChunkRows rw = rows_of(p, p.slots - 1 - from_last);
   const int rows = rw.tokens * p.group;  // those there are
   if (row0 >= rows) return;
   const int used = min(p.splits, max(1, (rw.tiles + p.chunk - 1) / p.chunk));
-  const int64_t first = (from_last * p.splits * p.kv_heads + hk) * rows_per + row0, step = static_cast<int64_t>(p.kv_heads) * rows_per;
-  const int mine = lane >> 4;  // the lane's row where weights are worked out
-  const float* ml = p.part_ml + (first + min(mine, rows - 1 - row0)) * 2;
   float base[kSplits / 16], f[kSplits / 16], top = -kInf, l = 0.f;
 #pragma unroll
   for (int c = 0; c < kSplits / 16; ++c) {
-    const int s = c * 16 + (lane & 15);
-    base[c] = s < used ? ml[s * step * 2] : -kInf;
-    f[c] = s < used ? ml[s * step * 2 + 1] : 0.f;  // the sum, for now
+    const bool there = c * 16 + (lane & 15) < used;
+    base[c] = there ? both[c][0] : -kInf;
+    f[c] = there ? both[c][1] : 0.f;  // the sum, for now
     top = fmaxf(top, base[c]);
   }
   for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
@@ -567,19 +589,20 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_p
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) o[r][i] = 0.f;
   const float* values = p.part + first * D + lane * (D / 64);
+  constexpr int kAtOnce = 8;
 #pragma unroll
   for (int c = 0; c < kSplits / 16; ++c) {
     if (c * 16 >= used) break;
-    for (int s = c * 16; s < min(used, c * 16 + 16); s += 2) {
-      float x[2][kJoin][D / 64];
+    for (int s = c * 16; s < min(used, c * 16 + 16); s += kAtOnce) {
+      float x[kAtOnce][kJoin][D / 64];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
         for (int r = 0; r < kJoin; ++r)
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) x[u][r][i] = values[(min(s + u, used - 1) * step + min(r, rows - 1 - row0)) * D + i];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
         for (int r = 0; r < kJoin; ++r) {
           const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f[c]), r * 16 + ((s + u) & 15)));
