@@ -151,8 +151,9 @@ def _pages(op: int, what: str, block_table, lengths, refs, given, given_what, ou
                    cols, bs, op)
     lib = _lib()
     a.workspace_bytes = lib.pages_workspace(ctypes.byref(a))
-    workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
-    a.workspace = workspace.data_ptr()
+    if a.workspace_bytes:
+        workspace = torch.empty(a.workspace_bytes, dtype=torch.uint8, device=device)
+        a.workspace = workspace.data_ptr()
     _run(device, what, lib.pages_update, ctypes.byref(a))
     return out
 

@@ -34,11 +34,17 @@ def filled(seed, rows, cols, pages, bs, fill=0.7):
     return torch.tensor(table, dtype=torch.int32).view(rows, cols), ints(lengths, "cpu"), ints(refs, "cpu")
 
 
-class Both:
-    """The same rows on the GPU and with lists."""
+BIG = 1 << 13   # a cache of more pages than this is no longer the work of one workgroup
 
-    def __init__(self, table, lengths, refs, bs, pad=0):
+
+class Both:
+    """The same rows on the GPU and with lists; ``big``: behind as many pages that are held."""
+
+    def __init__(self, table, lengths, refs, bs, pad=0, big=False):
         rows, cols = table.shape
+        if big:
+            refs = torch.cat([torch.ones(BIG, dtype=torch.int32), refs])
+            table = torch.where((table >= 0) & (table < 1 << 20), table + BIG, table)
         wide = torch.full((rows, cols + pad), 77, dtype=torch.int32, device=DEV)
         wide[:, :cols] = table
         self.wide, self.table, self.bs = wide, wide[:, :cols], bs
@@ -79,11 +85,12 @@ def test_fork_by_hand():
     assert b.fork([-1, 3, 2]) == [[-1, -1]] * 3 and b.refs.tolist() == [1, 0, 1, 0, 0, 0, 0, 0, 0, 1]
 
 
+@pytest.mark.parametrize("big", [False, True])
 @pytest.mark.parametrize("bs", [16, 32, 64, 128])
 @pytest.mark.parametrize("rows,cols,pages", [(1, 1, 1), (2, 3, 5), (5, 7, 40), (33, 9, 400), (300, 20, 4500), (70, 300, 13000)])
-def test_forks(rows, cols, pages, bs):
+def test_forks(rows, cols, pages, bs, big):
     rng = random.Random(rows * bs)
-    b = Both(*filled(rows + bs, rows, cols, pages, bs), bs, pad=3)
+    b = Both(*filled(rows + bs, rows, cols, pages, bs), bs, pad=3, big=big)
     for kind in range(4):
         if kind == 0:
             parents = [rng.randrange(rows) for _ in range(rows)]
@@ -96,16 +103,26 @@ def test_forks(rows, cols, pages, bs):
         b.fork(parents)
 
 
+@pytest.mark.parametrize("big", [False, True])
 @pytest.mark.parametrize("bs", [16, 64])
 @pytest.mark.parametrize("rows,cols,pages", [(1, 1, 0), (1, 4, 3), (6, 5, 12), (40, 30, 700), (257, 40, 6000), (3, 2000, 5000)])
-def test_growth(rows, cols, pages, bs):
+def test_growth(rows, cols, pages, bs, big):
     rng = random.Random(rows + pages)
-    b = Both(*filled(rows, rows, cols, pages, bs, 0.4), bs, pad=1)
+    b = Both(*filled(rows, rows, cols, pages, bs, 0.4), bs, pad=1, big=big)
     for most in (0, 1, bs, 5 * bs, cols * bs):
         b.grow([rng.randint(-1, most) for _ in range(rows)])
     b.fork([i if rng.random() < 0.5 else -1 for i in range(rows)])
     b.grow([rng.randint(0, cols * bs // 2) for _ in range(rows)])
     b.grow([(1 << 31) - 1] * rows)
+
+
+@pytest.mark.parametrize("rows,cols,pages", [(1024, 4, 8192), (1025, 3, 4000), (1024, 5, 8192), (1, 4096, 8192), (1, 4097, 8192), (60, 40, 8193), (2000, 40, 65537)])
+def test_calls_next_to_the_limits_of_one_workgroup(rows, cols, pages):
+    rng = random.Random(rows)
+    b = Both(*filled(rows, rows, cols, pages, 16, 0.9), 16)
+    b.fork([rng.choice([i, i, -1, rng.randrange(rows)]) for i in range(rows)])
+    b.grow([rng.randint(0, 8 * cols) for _ in range(rows)])
+    b.compact()
 
 
 def test_pages_run_out():
@@ -122,11 +139,12 @@ def test_pages_run_out():
     assert b.fork([0, 1, 1]) == [[-1, -1], [-1, -1], [2, -1]] and b.lengths.tolist() == [32, 7, 0]
 
 
+@pytest.mark.parametrize("big", [False, True])
 @pytest.mark.parametrize("bs", [16, 128])
 @pytest.mark.parametrize("rows,cols,pages", [(1, 1, 1), (1, 2, 2), (4, 6, 64), (9, 20, 131), (20, 300, 4097), (60, 300, 20000)])
-def test_compaction(rows, cols, pages, bs):
+def test_compaction(rows, cols, pages, bs, big):
     rng = random.Random(pages)
-    b = Both(*filled(rows, rows, cols, pages, bs), bs, pad=2)
+    b = Both(*filled(rows, rows, cols, pages, bs), bs, pad=2, big=big)
     b.compact()
     b.fork([rng.choice([i, -1, rng.randrange(rows)]) for i in range(rows)])
     b.compact()
@@ -141,23 +159,26 @@ def test_compaction_moves_pages_of_the_callers_own():
 def test_pages_that_are_not_there():
     # entries outside the pages are handed on and count nowhere
     table = ints([[3, -5, 1 << 30, 2], [7, 0, -1, -1]], "cpu")
-    b = Both(table, ints([60, 20], "cpu"), ints([1, 0, 1, 1, 0, 0], "cpu"), 16)
-    b.fork([0, 0])
-    b.grow([4, 4])
-    b.compact()
-    b.fork([1, 0])
-    b.fork([5, 5])
-    b = Both(ints([[3, 9]], "cpu"), ints([20], "cpu"), ints([0, 0, 0, 1], "cpu"), 16)   # a last page that is not there
-    b2 = Both(ints([[3, 9], [-1, -1]], "cpu"), ints([20, 0], "cpu"), ints([0, 0, 0, 1], "cpu"), 16)
-    b.grow([16])
-    assert b2.fork([0, 0]) == [[-1, -1], [-1, -1]]
+    for big in (False, True):
+        b = Both(table, ints([60, 20], "cpu"), ints([1, 0, 1, 1, 0, 0], "cpu"), 16, big=big)
+        b.fork([0, 0])
+        b.grow([4, 4])
+        b.compact()
+        b.fork([1, 0])
+        b.fork([5, 5])
+        # a last page that is not there
+        b = Both(ints([[3, 1 << 30]], "cpu"), ints([20], "cpu"), ints([0, 0, 0, 1], "cpu"), 16, big=big)
+        b2 = Both(ints([[3, 1 << 30], [-1, -1]], "cpu"), ints([20, 0], "cpu"), ints([0, 0, 0, 1], "cpu"), 16, big=big)
+        b.grow([16])
+        assert b2.fork([0, 0]) == [[-1, -1], [-1, -1]]
 
 
 def test_lengths_outside_the_table():
-    b = Both(ints([[0, 1], [2, 3]], "cpu"), ints([1000, -7], "cpu"), ints([1, 1, 0, 0], "cpu"), 16)
-    assert b.grow([1, 20]) == [0, 20]
-    b.fork([1, 0])
-    b.compact()
+    for big in (False, True):
+        b = Both(ints([[0, 1], [2, 3]], "cpu"), ints([1000, -7], "cpu"), ints([1, 1, 0, 0], "cpu"), 16, big=big)
+        assert b.grow([1, 20]) == [0, 20]
+        b.fork([1, 0])
+        b.compact()
 
 
 def test_pages_of_many_chunks():

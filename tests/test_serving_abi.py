@@ -131,10 +131,12 @@ def test_pages_update_refuses(lib, bad):
 @pytest.mark.parametrize("op", [0, 1, 2])
 def test_pages_workspace(lib, op):
     assert lib.pages_update(None, None) == EINVAL and lib.pages_workspace(None) == 0
-    need = lib.pages_workspace(ctypes.byref(pages(op=op)))
-    assert need > 0
-    for ws, n in ((0, need), (A, need - 1)):
-        assert lib.pages_update(ctypes.byref(pages(op=op, workspace=ws, workspace_bytes=n)), None) == EWORKSPACE
+    assert lib.pages_workspace(ctypes.byref(pages(op=op))) == 0   # one workgroup's work
+    for more in (dict(num_pages=(1 << 13) + 1), dict(rows=1025), dict(block_table_cols=1 << 12, block_table_stride=1 << 12)):
+        need = lib.pages_workspace(ctypes.byref(pages(op=op, **more)))
+        assert need > 0
+        for ws, n in ((0, need), (A, need - 1)):
+            assert lib.pages_update(ctypes.byref(pages(op=op, workspace=ws, workspace_bytes=n, **more)), None) == EWORKSPACE
     nothing = dict(op=op, rows=0, num_pages=0, block_table=0, lengths=0, refs=0, given=0, out=0, workspace=0, workspace_bytes=0)
     assert lib.pages_update(ctypes.byref(pages(**nothing)), None) == OK
 
