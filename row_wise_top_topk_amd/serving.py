@@ -226,9 +226,10 @@ def pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tens
 
 def _matrix(t, what: str, dtype, device, rows: int):
     """(columns, row stride) of a 2-D operand with unit stride along its last axis."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 2 or t.shape[0] != rows:
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device else ()
+    if len(shape) != 2 or shape[0] != rows:
         raise ValueError(f"{what} must be a 2-D {dtype} tensor with a row for each of the logits, on their device")
-    cols = t.shape[1]
+    cols = shape[1]
     at, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{what} must have unit stride along its last axis")
@@ -239,8 +240,7 @@ def _row(t, what: str, dtype, device, rows: int):
     """Address of a 1-D operand with an entry for each row, None where it is not given."""
     if t is None:
         return None
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.dim() != 1 or t.shape[0] != rows
-            or not t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == (rows,) and t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous 1-D {dtype} tensor with an entry for each row, on the logits' device")
     return t.data_ptr()
 
@@ -280,7 +280,7 @@ def penalize_logits(logits: torch.Tensor, tokens: torch.Tensor = None, lengths: 
     rows = logits.shape[0]
     vocab, logits_at = _matrix(logits, "logits", logits.dtype, device, rows)
     if out is None:
-        out = torch.empty((rows, vocab), dtype=torch.float32, device=device)
+        out = torch.empty_like(logits, dtype=torch.float32, memory_format=torch.contiguous_format)
         out_at = vocab
     else:
         cols, out_at = _matrix(out, "out", torch.float32, device, rows)
