@@ -659,15 +659,22 @@ struct ChunkPlan {
   uint64_t rows;  // rows of partial results
 };
 
-// A walk of `tiles` tiles of each of `items` workgroups, in how many parts, `most` at
-// most: the card works on `at_once` workgroups, so that their rounds count.  A
-// workgroup's start costs what kStart tiles do, the join and its launch kJoinCost.
-constexpr int kStart = 4, kJoinCost = 8;
-int parts_of(int64_t items, int64_t tiles, int64_t at_once, int64_t most) {
+// In how many parts, `most` at most, the walks of `items` workgroups over up to
+// `tiles` tiles are cut.  The 256 compute units take the workgroups in rounds (two
+// small ones on a unit at once need as long as one after the other); where several
+// sequences share the call their lengths differ, so that half of the rounds are
+// counted and no last one.  A tile takes `tile` ns of a unit, `alone` at least; the
+// join costs its launch (with the host's part 10 us) and the partial results' way
+// through memory.
+int parts_of(int64_t items, bool several, int64_t tiles, int64_t rows, int dim, int waves, int64_t most) {
+  const int64_t tile = dim == 128 ? (waves == 8 ? 1900 : 1120) : (waves == 8 ? 1300 : 700), alone = dim == 128 ? tile : (waves == 8 ? tile : 950);
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= kSplits && (s == 1 || (s <= most && tiles >= 2 * s)); ++s) {
-    const int64_t cost = ((items * s + at_once - 1) / at_once) * ((tiles + s - 1) / s + kStart) + (s == 1 ? 0 : kJoinCost);
+  for (int s = 1; s <= kSplits && (s == 1 || (s <= most && s <= tiles)); ++s) {
+    const int64_t sixteenths = several ? items * s / 32 : (items * s + 255) / 256 * 16;
+    const int64_t step = tile * sixteenths / 16 > alone ? tile * sixteenths / 16 : alone;
+    const int64_t join = s == 1 ? 0 : 10000 + 200 * s + rows * s * (dim + 2) / 500;  // 8 bytes a value, at 4 TB/s
+    const int64_t cost = step * ((tiles + s - 1) / s) + join;
     if (cost < least) {
       least = cost;
       best = s;
@@ -682,30 +689,32 @@ ChunkPlan plan_of(const mi_chunk_attention_args* a) {
   int64_t most = (static_cast<int64_t>(a->block_table_cols) * a->block_size) + a->total;  // what a row can see
   if (a->max_length < most) most = a->max_length;
   const int64_t tiles = most / kTile + 2;
+  const int64_t seqs = a->total < a->num_seqs ? a->total : a->num_seqs;  // those that have tokens, at most
   auto with = [&](int waves) {
     p.waves = waves;
     p.tokens_per = a->cu == nullptr ? 1 : waves * 32 / group;
     p.slots = slots_of(a->total, a->num_seqs, p.tokens_per);
-    // workgroups that have rows (of each sequence one more than whole ones, at most)
-    return (a->total / p.tokens_per + (a->total < a->num_seqs ? a->total : a->num_seqs)) * a->kv_heads;
+    // workgroups that have rows: of each sequence one more than whole ones, at most
+    return (seqs <= 1 ? (a->total + p.tokens_per - 1) / p.tokens_per : a->total / p.tokens_per + seqs) * a->kv_heads;
   };
-  const bool wide = a->dim == 128;
-  // Eight wavefronts a workgroup widen the codes once for 256 rows.  With many short
-  // sequences the rows of their last workgroups are empty, half of them in the mean:
-  // from a third as many sequences as whole workgroups on, four wavefronts.  Measured
-  // (us, eight against four): one sequence, 2048 tokens behind 16000, 32/4 heads of
-  // 64: 376, 393; 96 behind 100003, 32/2 of 128: 178, 202; four of 200 behind 900,
-  // 16/4 of 64: 26.5, 29.3; five of 890 in all, 12/3 of 64: 55.7, 49.1; 64 single
-  // tokens and 512, 32/8 of 128: 154, 100.
+  // Eight wavefronts a workgroup widen the codes once for 256 rows; four start
+  // quicker and leave fewer rows empty.  Eight where there are 4000 tiles or more to
+  // walk over, unless there are many short sequences, a third as many as whole
+  // workgroups (half of a sequence's last workgroup is empty in the mean).  Measured
+  // (us, eight against four, each with its best parts): 128 columns: 96 tokens behind
+  // 100003, 32/2 heads (18800 tiles): 190, 210; 512 behind 4000, 32/8 (4700): 61, 64;
+  // 2000 behind 2000, 8/1 (4100): 56, 59; 300 behind 3000, 16/2 (1000): 37, 34; 128
+  // behind 8000, 8/8 (1000): 33, 30; 1000 alone, 16/4 (1100): 32, 25; 64 single tokens
+  // and 512, 32/8: 145, 95.  64 columns: five sequences of 890 tokens, 12/3: 50, 45;
+  // four of 200 behind 900, 16/4: 28, 23; 33 behind 500, 8/2: 17.6, 14.1.
   int64_t items = with(8);
-  if (a->num_seqs > 1 && 3 * static_cast<int64_t>(a->num_seqs) > a->total / p.tokens_per) items = with(4);
-  const int64_t at_once = p.waves == 8 ? 256 : (wide ? 512 : 768);
+  if (items * tiles < 4000 || (seqs > 1 && 3 * seqs > a->total / p.tokens_per)) items = with(4);
   // partial results of 2^17 rows at most (68 MB with 128 columns)
   const int64_t rows = p.slots * a->kv_heads * p.waves * 32;
-  const int64_t splits = items > 0 ? parts_of(items, tiles, at_once, (int64_t{1} << 17) / rows) : 1;
+  const int64_t splits = items > 0 ? parts_of(items, seqs > 1, tiles, a->total * a->heads, a->dim, p.waves, (int64_t{1} << 17) / rows) : 1;
   p.chunk = static_cast<int>((tiles + splits - 1) / splits);
   p.splits = static_cast<int>((tiles + p.chunk - 1) / p.chunk);
-  p.rows = p.splits > 1 ? static_cast<uint64_t>(p.slots) * a->kv_heads * p.splits * p.waves * 32 : 0;
+  p.rows = p.splits > 1 ? static_cast<uint64_t>(rows) * p.splits : 0;
   return p;
 }
 
