@@ -8,6 +8,16 @@
 // by one wavefront in two scans, and a page's own rank by two loads.  No kernel
 // waits for another workgroup, and only counts of holders are changed by atomics
 // (integers: their order does not matter).
+//
+// The bytes are few (512 rows of 1875 entries: 7 MB with the pages copied, 1.5 us at
+// the rate of a large copy), so that these kernels are chains of loads, each behind
+// the one before, and of launches: on the device 10.2 us for that fork, 15.3 us for
+// 256 rows that end and are filled again, 9.8 us for the list of a compaction.
+// What counts is that loads which do not depend on each other are in flight
+// together: with a branch around each load of a count, a chunk's free bits took 6.8
+// us instead of 4, and eight entries of a row at once instead of one made the fork's
+// first kernel 4.9 us instead of 6.5.  A caller without a graph waits for the host:
+// 8 us a call and 2.7 us for each further launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -21,6 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWords = 64;              // words of free bits of a chunk
 constexpr int kChunk = kWords * 64;     // pages of a chunk
+constexpr int kAtOnce = 8;              // entries of a row that a thread has in flight
 
 struct PagesArgs {
   int32_t* table;
@@ -55,16 +66,28 @@ __device__ __forceinline__ int wave_sum(int x) {
   return x;
 }
 
-// Sum over the workgroup; every thread gets it.
-__device__ __forceinline__ int block_sum(int x, int* box) {
-  x = wave_sum(x);
+// Sums over the workgroup; every thread gets them.
+template <int N>
+__device__ __forceinline__ void block_sums(int (&x)[N], int (*box)[kThreads / 64]) {
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) box[threadIdx.x >> 6] = x;
-  __syncthreads();
-  int all = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) all += box[w];
-  return all;
+  for (int i = 0; i < N; ++i) {
+    x[i] = wave_sum(x[i]);
+    if ((threadIdx.x & 63) == 0) box[i][threadIdx.x >> 6] = x[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) x[i] += box[i][w];
+  }
+}
+
+__device__ __forceinline__ int block_sum(int x, int* box) {
+  int all[1] = {x};
+  block_sums(all, reinterpret_cast<int(*)[kThreads / 64]>(box));
+  return all[0];
 }
 
 __device__ __forceinline__ int length_of(const PagesArgs& p, int row) {
@@ -82,12 +105,12 @@ __device__ __forceinline__ void free_bits(const PagesArgs& p, int64_t chunk, int
   const int64_t first = chunk * kChunk + wave * kMine * 64 + lane;
   int32_t held[kMine];
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) held[i] = first + i * 64 < p.pages ? p.refs[first + i * 64] : 1;
+  for (int i = 0; i < kMine; ++i) held[i] = p.refs[min(first + i * 64, p.pages - 1)];  // (a branch here would wait for each load)
   uint64_t mine = 0;
   int count = 0;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const uint64_t bits = __ballot(held[i] <= 0);
+    const uint64_t bits = __ballot(held[i] <= 0 && first + i * 64 < p.pages);
     if (lane == i) mine = bits;
     count += __popcll(bits);
   }
@@ -158,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
   const int32_t* from = p.table + (ends ? row : parent) * p.stride;
   int source = -1;
   if (part) {
+    source = from[whole];
     // who keeps the parent's last page: the parent, or the first of its forks
     if (tid == 0) s_first = p.in[parent] == parent ? -1 : row;
     __syncthreads();
@@ -170,20 +194,30 @@ __global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
       __syncthreads();
     }
     holds = s_first == row;
-    source = from[whole];
     if (source < 0 || source >= p.pages) {  // not there: handed on as it is
       holds = true;
       source = -1;
     }
   }
   const int had = pages_of(p, length_of(p, row)), has = whole + (part && holds ? 1 : 0);
-  for (int c = tid; c < p.cols; c += kThreads) {
-    const int old = c < had ? mine[c] : -1, now = c < has ? from[c] : -1;
-    if (old != now) {  // forks of one parent share most of what they had
-      if (old >= 0 && old < p.pages) atomicAdd(p.refs + old, -1);
-      if (now >= 0 && now < p.pages) atomicAdd(p.refs + now, 1);
+  int32_t* next = p.rows_new + static_cast<int64_t>(row) * p.cols;
+  for (int c0 = tid; c0 < p.cols; c0 += kThreads * kAtOnce) {
+    int old[kAtOnce], now[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int c = c0 + i * kThreads;
+      old[i] = c < had ? mine[c] : -1;
+      now[i] = c < has ? from[c] : -1;
     }
-    p.rows_new[static_cast<int64_t>(row) * p.cols + c] = now;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int c = c0 + i * kThreads;
+      if (c < p.cols) next[c] = now[i];
+      if (old[i] != now[i]) {  // forks of one parent share most of what they had
+        if (old[i] >= 0 && old[i] < p.pages) atomicAdd(p.refs + old[i], -1);
+        if (now[i] >= 0 && now[i] < p.pages) atomicAdd(p.refs + now[i], 1);
+      }
+    }
   }
   if (tid == 0) {
     p.asks[row] = part && !holds;
@@ -201,8 +235,16 @@ __global__ void __launch_bounds__(kThreads) fork_write_kernel(PagesArgs p) {
   }
   const int row = static_cast<int>(blockIdx.x - p.chunks);
   if (p.in[row] == row) return;
-  for (int c = threadIdx.x; c < p.cols; c += kThreads)
-    p.table[row * p.stride + c] = p.rows_new[static_cast<int64_t>(row) * p.cols + c];
+  const int32_t* next = p.rows_new + static_cast<int64_t>(row) * p.cols;
+  int32_t* mine = p.table + row * p.stride;
+  for (int c0 = threadIdx.x; c0 < p.cols; c0 += kThreads * kAtOnce) {
+    int now[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) now[i] = c0 + i * kThreads < p.cols ? next[c0 + i * kThreads] : 0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (c0 + i * kThreads < p.cols) mine[c0 + i * kThreads] = now[i];
+  }
 }
 
 // Fork, third step: pages for the forks' last tokens, and lengths.  A wavefront a row.
@@ -210,15 +252,20 @@ __global__ void __launch_bounds__(kThreads) fork_last_kernel(PagesArgs p) {
   const int lane = threadIdx.x & 63;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
   if (row >= p.rows) return;
-  const bool stays = p.in[row] == row;
-  int source = -1, page = -1;
-  int length = stays ? 0 : p.length[row];
-  if (p.asks[row] != 0) {
-    int64_t rank = 0;
-    for (int64_t i = lane; i < row; i += 64) rank += p.asks[i];
-    rank = wave_sum(static_cast<int>(rank));
-    const Spot s = find_free(p, rank);
-    source = p.source[row];
+  const int parent = p.in[row], asks_here = p.asks[row], length_new = p.length[row], from = p.source[row];
+  const bool stays = parent == row;  // (then it has no new length)
+  int source = -1, page = -1, length = stays ? 0 : length_new;
+  if (asks_here != 0) {
+    source = from;
+    int rank = 0;
+    for (int64_t i0 = lane; i0 < row; i0 += 64 * kAtOnce) {
+      int asks[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) asks[i] = p.asks[min(i0 + i * 64, row)];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) rank += i0 + i * 64 < row ? asks[i] : 0;
+    }
+    const Spot s = find_free(p, wave_sum(rank));
     const int whole = length >> p.lb;
     if (s.chunk < p.chunks) {
       page = static_cast<int>(s.chunk * kChunk + s.word * 64 + s.bit);
@@ -255,30 +302,32 @@ __global__ void __launch_bounds__(kThreads) grow_ask_kernel(PagesArgs p) {
 // Grow, second step: one workgroup a row, whose wavefronts share the pages that it
 // asks for.
 __global__ void __launch_bounds__(kThreads) grow_kernel(PagesArgs p) {
-  __shared__ int box[kThreads / 64];
+  __shared__ int box[3][kThreads / 64];
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int asks = p.asks[row];
+  const int asks = p.asks[row], length = length_of(p, row), had = pages_of(p, length), given = p.in[row];
   int64_t rank = 0;
   bool fits = asks == 0;
   if (asks > 0) {
     int64_t sum = 0;  // (a table's entries: rows * cols can pass 32 bits, pages cannot)
-    for (int i = tid; i < row; i += kThreads) sum += max(0, p.asks[i]);
+    int free = 0;
+    for (int64_t i = tid; i < max(static_cast<int64_t>(row), p.chunks); i += kThreads) {
+      const int ask = p.asks[min(i, static_cast<int64_t>(row))], count = p.counts[min(i, p.chunks)];
+      if (i < row) sum += max(0, ask);
+      if (i < p.chunks) free += count;
+    }
     // saturated: what passes the number of pages fits nowhere
-    rank = block_sum(static_cast<int>(sum < p.pages ? sum : p.pages) >> 8, box);
-    const int low = block_sum(static_cast<int>(sum < p.pages ? sum : p.pages) & 255, box);
-    rank = rank * 256 + low;
-    int64_t free = 0;
-    for (int64_t c = tid; c < p.chunks; c += kThreads) free += p.counts[c];
-    free = block_sum(static_cast<int>(free), box);
-    fits = rank + asks <= free;
-  }
-  const int length = length_of(p, row), had = pages_of(p, length);
-  if (tid == 0) {
-    const int more = p.in[row] < 0 || !fits ? 0 : p.in[row];
-    p.out[row] = more;
+    const int most = static_cast<int>(sum < p.pages ? sum : p.pages);
+    int all[3] = {most >> 8, most & 255, free};
+    block_sums(all, box);
+    rank = static_cast<int64_t>(all[0]) * 256 + all[1];
+    fits = rank + asks <= all[2];
   }
   __syncthreads();  // all have read the length
-  if (tid == 0 && p.out[row] > 0) p.lengths[row] = length + p.out[row];
+  if (tid == 0) {
+    const int more = given < 0 || !fits ? 0 : given;
+    p.out[row] = more;
+    if (more > 0) p.lengths[row] = length + more;
+  }
   if (asks <= 0 || !fits) return;
   const int share = (asks + kThreads / 64 - 1) / (kThreads / 64);
   int at = wave * share;
@@ -423,19 +472,18 @@ __device__ __forceinline__ int small_scan(int x, int* box, int& all) {
 // The free bits and their running numbers; returns the number of free pages.
 __device__ __forceinline__ int small_bits(const PagesArgs& p, Small& s) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kWaves = kSmallThreads / 64, kAtOnce = 8;
-  const int words = static_cast<int>((p.pages + 63) / 64);
+  constexpr int kWaves = kSmallThreads / 64;
+  const int pages = static_cast<int>(p.pages), words = (pages + 63) / 64;
   for (int w0 = wave * kAtOnce; w0 < words; w0 += kWaves * kAtOnce) {
     int32_t held[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const int64_t q = (w0 + i) * int64_t{64} + lane;
       // (past the caches: other wavefronts' atomics have changed them)
-      held[i] = q < p.pages ? __hip_atomic_load(p.refs + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
+      held[i] = __hip_atomic_load(p.refs + min((w0 + i) * 64 + lane, pages - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const uint64_t bits = __ballot(held[i] <= 0);
+      const uint64_t bits = __ballot(held[i] <= 0 && (w0 + i) * 64 + lane < pages);
       if (lane == 0 && w0 + i < words) s.words[w0 + i] = bits;
     }
   }
@@ -507,24 +555,24 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PagesArgs p) {
     }
     __syncthreads();
     constexpr int kMost = kSmallEntries / kSmallThreads;
-    int32_t next[kMost];
+    int32_t old[kMost], next[kMost];
     const int turns = (entries + kSmallThreads - 1) / kSmallThreads;
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
-      next[i] = -1;
+      old[i] = next[i] = -1;
       const int e = i * kSmallThreads + tid;
       if (i < turns && e < entries) {
         const int r = e / p.cols, c = e - r * p.cols, from = s.parent[r];
-        if (from != r) {
-          const int old = c < pages_of(p, s.length[r]) ? p.table[r * p.stride + c] : -1;
-          next[i] = c < s.has[r] ? p.table[from * p.stride + c] : -1;
-          if (old != next[i]) {
-            if (old >= 0 && old < p.pages) atomicAdd(p.refs + old, -1);
-            if (next[i] >= 0 && next[i] < p.pages) atomicAdd(p.refs + next[i], 1);
-          }
-        }
+        if (from != r && c < pages_of(p, s.length[r])) old[i] = p.table[r * p.stride + c];
+        if (from != r && c < s.has[r]) next[i] = p.table[from * p.stride + c];
       }
     }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      if (old[i] != next[i]) {
+        if (old[i] >= 0 && old[i] < p.pages) atomicAdd(p.refs + old[i], -1);
+        if (next[i] >= 0 && next[i] < p.pages) atomicAdd(p.refs + next[i], 1);
+      }
     __threadfence();
     __syncthreads();
     const int free = small_bits(p, s);
@@ -600,16 +648,16 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(PagesArgs p) {
 }
 
 // Whether one workgroup does the call: a launch instead of three (two to grow), which
-// the host saves 7 us with.  Measured on the device (us in a graph, one workgroup
-// against several): 64 rows of 55 entries, 2230 pages: fork 12.0, 11.0, grow 6.8, 8.1,
-// compact 5.2, 9.8; 4 rows of 32: 9.6, 8.7; 256 rows of 55, 10124 pages: fork 21, 12.
+// saves the host 7 us.  Measured on the device (us in a graph, one workgroup against
+// several): 64 rows of 55 entries, 2230 pages: fork 10.4, 10.0, grow 6.2, 6.5, compact
+// 4.6, 8.9; 4 rows of 32: fork 8.1, 8.7; 256 rows of 55, 10124 pages: fork 15.9, 9.9.
 bool is_small(const mi_pages_args* a) {
   return a->rows <= kSmallRows && static_cast<int64_t>(a->rows) * a->block_table_cols <= kSmallEntries && a->num_pages <= kSmallWords * 64;
 }
 
 struct CopyArgs {
-  char* cache[2];
-  float* scale[2];
+  char *k, *v;
+  float *k_scale, *v_scale;
   float* mean;
   const int32_t* copies;
   int64_t num, pages, page_bytes;
@@ -619,6 +667,8 @@ struct CopyArgs {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // `parts` workgroups share a pair, and go on to the pair `gridDim / parts` behind it.
+// Bound by memory: 5140 pages of 132 KB, read and written, in 266 us (5.1 TB/s; 277 us
+// with pointers and bounds looked up between the loads).
 __global__ void __launch_bounds__(kThreads) copy_kernel(CopyArgs p) {
   const int tid = threadIdx.x, part = blockIdx.x % p.parts;
   const int64_t step = gridDim.x / p.parts;
@@ -627,28 +677,27 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(CopyArgs p) {
     const int from = p.copies[2 * i], to = p.copies[2 * i + 1];
     if (from < 0 || from >= p.pages || to < 0 || to >= p.pages) continue;
     const int64_t per = p.page_bytes / 16, end = min((part + 1) * each, 2 * per);
-    for (int64_t a = part * each; a < end; a += kThreads * 4) {
+    char* to_k = p.k + to * p.page_bytes;
+    char* to_v = p.v + to * p.page_bytes;
+    const char* from_k = p.k + from * p.page_bytes;
+    const char* from_v = p.v + from * p.page_bytes;
+    for (int64_t a = part * each + tid; a < end; a += kThreads * 4) {
       u32x4 x[4];
-      int64_t at[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        at[j] = a + j * kThreads + tid;
-        if (at[j] < end) {
-          const int v = at[j] >= per;
-          x[j] = *reinterpret_cast<const u32x4*>(p.cache[v] + from * p.page_bytes + (at[j] - v * per) * 16);
-        }
+        const int64_t at = min(a + j * kThreads, end - 1);  // (a branch here would wait for each load)
+        x[j] = *reinterpret_cast<const u32x4*>((at < per ? from_k : from_v) + (at < per ? at : at - per) * 16);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (at[j] < end) {
-          const int v = at[j] >= per;
-          *reinterpret_cast<u32x4*>(p.cache[v] + to * p.page_bytes + (at[j] - v * per) * 16) = x[j];
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = a + j * kThreads;
+        if (at < end) *reinterpret_cast<u32x4*>((at < per ? to_k : to_v) + (at < per ? at : at - per) * 16) = x[j];
+      }
     }
     if (part == 0) {
       for (int h = tid; h < 2 * p.heads; h += kThreads) {
-        float* s = p.scale[h >= p.heads];
-        const int64_t k = h >= p.heads ? h - p.heads : h;
+        float* s = h < p.heads ? p.k_scale : p.v_scale;
+        const int64_t k = h < p.heads ? h : h - p.heads;
         s[static_cast<int64_t>(to) * p.heads + k] = s[static_cast<int64_t>(from) * p.heads + k];
       }
       for (int d = tid; d < p.mean_floats; d += kThreads)
@@ -766,10 +815,10 @@ MI_PAGES_EXPORT int pages_copy(const mi_pages_copy_args* a, hipStream_t stream) 
     return MI_ATTN_EINVAL;
   if (a->num == 0 || a->num_pages == 0) return MI_ATTN_OK;
   CopyArgs p;
-  p.cache[0] = static_cast<char*>(a->k_cache);
-  p.cache[1] = static_cast<char*>(a->v_cache);
-  p.scale[0] = a->k_scale;
-  p.scale[1] = a->v_scale;
+  p.k = static_cast<char*>(a->k_cache);
+  p.v = static_cast<char*>(a->v_cache);
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
   p.mean = a->k_mean;
   p.copies = a->copies;
   p.num = a->num;
