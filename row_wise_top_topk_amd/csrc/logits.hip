@@ -11,12 +11,13 @@
 // long where there are enough of them.
 //
 // Measured (in a graph): 64 rows of 128256, bf16, 300 to 8000 tokens, 20 biases and
-// a mask: 14.5 us, 51 MB at 3.5 TB/s; 256 x 32000, up to 500 tokens: 12.7 us, 49 MB.
+// a mask: 13.8 us, 51 MB at 3.7 TB/s; 256 x 32000, up to 500 tokens: 12.6 us, 49 MB.
 // A lane takes four ids, so that the stores of a wavefront are whole lines: with
 // eight ids a lane they took 17 and 16 us.  32 rows of 151937 behind 50000 to 100000
-// tokens: 25 us, 10.6 without the tokens: ten stretches count 75000 each, 8
-// instructions a token.  3 x 32000: 4.6 us, the chain from the lengths over the
-// tokens to the logits.
+// tokens: 19.3 us, 9.9 behind 500: thirteen stretches look at 75000 tokens each, 8
+// instructions a token.  3 x 32000: 3.8 us, the chain from the lengths over the
+// tokens to the logits.  Slower: the logits loaded before the tokens (18 us for the
+// first: loads come back in order), results written by a pass of their own.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -32,6 +33,8 @@ namespace {
 
 constexpr uint32_t kSaid = (1u << 21) - 1, kPrompt = 1u << 21;
 constexpr int kBiasBit = 22;
+constexpr int kThreads = 1024;
+constexpr uint32_t kDies = 8;
 
 struct Fp32 {};
 
@@ -80,7 +83,7 @@ __device__ __forceinline__ void load4(const char* from, int n, float (&x)[4]) {
 // Calls count(place) for the tokens [from, to) that are ids first + place, place < n.
 // A wavefront behind the last token leaves at once: with short rows of tokens the
 // instructions of all wavefronts would cost more than the loads.
-template <int kThreads, typename F>
+template <typename F>
 __device__ __forceinline__ void each_token(const int32_t* tokens, int from, int to, uint32_t first, uint32_t n, F count) {
   constexpr int kAtOnce = 4, kStep = kThreads * 4;
   auto take = [&](const int32_t (&id)[4]) {
@@ -113,14 +116,19 @@ __device__ __forceinline__ void each_token(const int32_t* tokens, int from, int 
 }
 
 // kCount: there are tokens or biases.
-template <typename T, bool kCount, int kThreads, int kUnits>
+template <typename T, bool kCount, int kUnits>
 __global__ void __launch_bounds__(kThreads) penalize_kernel(LogitArgs p) {
   constexpr int kStretch = kThreads * 4 * kUnits;
   __shared__ __attribute__((aligned(16))) uint32_t words[kCount ? kStretch : 4];
   constexpr int kSize = __is_same(T, Fp32) ? 4 : 2;
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / p.stretches;
-  const int64_t first = static_cast<int64_t>(blockIdx.x % p.stretches) * kStretch;
+  // The dies take workgroups in turn and have a cache each: a die works on consecutive
+  // rows, so that a row's tokens come into one cache (32 rows of 151937 behind 75000
+  // tokens: 25 us with a row's stretches over all dies, 21 so).
+  const uint32_t at = blockIdx.x % kDies * (gridDim.x / kDies) + blockIdx.x / kDies;
+  const int64_t row = at / p.stretches;
+  if (row >= p.rows) return;
+  const int64_t first = static_cast<int64_t>(at % p.stretches) * kStretch;
   const int n = static_cast<int>(min(static_cast<int64_t>(kStretch), p.vocab - first));
   const char* from = p.logits + (row * p.logits_stride + first) * kSize;
   const int32_t* mask = p.mask == nullptr ? nullptr : p.mask + row * p.mask_stride + (first >> 5);
@@ -140,8 +148,8 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(LogitArgs p) {
       len = max(0, min(len, p.token_cols));
       const int prompt = p.prompts == nullptr ? 0 : max(0, min(p.prompts[row], len));
       const int32_t* tokens = p.tokens + row * p.tokens_stride;
-      each_token<kThreads>(tokens, 0, prompt, static_cast<uint32_t>(first), n, [&](uint32_t at) { atomicOr(&words[at], kPrompt); });
-      each_token<kThreads>(tokens, prompt, len, static_cast<uint32_t>(first), n, [&](uint32_t at) { atomicAdd(&words[at], 1u); });
+      each_token(tokens, 0, prompt, static_cast<uint32_t>(first), n, [&](uint32_t at) { atomicOr(&words[at], kPrompt); });
+      each_token(tokens, prompt, len, static_cast<uint32_t>(first), n, [&](uint32_t at) { atomicAdd(&words[at], 1u); });
     }
     __syncthreads();
   }
@@ -188,25 +196,41 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(LogitArgs p) {
   }
 }
 
-template <typename T, int kThreads, int kUnits>
+int64_t workgroups(const LogitArgs& p, int units) { return p.rows * ((p.vocab + kThreads * 4 * units - 1) / (kThreads * 4 * units)); }
+
+template <typename T, int kUnits>
 int launch_as(LogitArgs p, hipStream_t stream) {
-  constexpr int kStretch = kThreads * 4 * kUnits;
-  p.stretches = static_cast<int>((p.vocab + kStretch - 1) / kStretch);
-  const int64_t grid = p.rows * p.stretches;
+  const int64_t all = workgroups(p, kUnits), grid = (all + kDies - 1) / kDies * kDies;
+  p.stretches = static_cast<int>(all / p.rows);
   if (grid > INT32_MAX) return MI_ATTN_EINVAL;
   const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
-  if (p.token_cols > 0 || p.bias_cols > 0) penalize_kernel<T, true, kThreads, kUnits><<<g, b, 0, stream>>>(p);
-  else penalize_kernel<T, false, kThreads, kUnits><<<g, b, 0, stream>>>(p);
+  if (p.token_cols > 0 || p.bias_cols > 0) penalize_kernel<T, true, kUnits><<<g, b, 0, stream>>>(p);
+  else penalize_kernel<T, false, kUnits><<<g, b, 0, stream>>>(p);
   return hipGetLastError() == hipSuccess ? MI_ATTN_OK : MI_ATTN_ELAUNCH;
 }
 
-// Small calls take stretches of 4096 ids, which spread over more of the card, the
-// others of 16384, which read the tokens less often.  Measured (us, 4096 against
-// 16384): 3 x 32000 ids: 4.6, 5.4; 1 x 50257: 4.6, 6.6; 8 x 200000: 6.1, 7.5; 64 x
-// 128256: 17.7, 14.5; 256 x 32000: 14.0, 12.7; 200 x 32000 behind 30000 tokens: 30.5, 17.4.
+// Stretches of one to four times 4096 ids.  512 workgroups run at once, two on a
+// compute unit, and a round of them takes about as long as their units and one more
+// for what comes before; the longest stretch of the cheapest, which reads the tokens
+// least often.  Measured (us in a graph, 1 to 4 units): 3 x 32000: 4.0, 4.5, 4.8, 5.4;
+// 8 x 128256: 5.3, 6.0, 6.9, 7.8; 20 x 128256: 9.3, 8.4, 8.0, 8.8; 32 x 151937: 13.4,
+// 12.0, 10.5, 11.8; behind 60000 tokens: 22.8, 18.5, 15.4, 16.4; 48 x 128256: 16.7,
+// 15.0, 15.5, 12.9; 64 x 128256: 24, 18.7, 17.6, 14.1; 300 x 32000: 26.1, 20.8, 19.1,
+// 20.2.
 template <typename T>
 int launch_penalize(const LogitArgs& p, hipStream_t stream) {
-  return p.rows * p.vocab <= (1 << 21) ? launch_as<T, 512, 2>(p, stream) : launch_as<T, 1024, 4>(p, stream);
+  int units = 1;
+  int64_t least = INT64_MAX;
+  for (int u = 1; u <= 4; ++u) {
+    const int64_t cost = (workgroups(p, u) + 511) / 512 * (u + 1);
+    if (cost <= least) {
+      least = cost;
+      units = u;
+    }
+  }
+  if (units == 1) return launch_as<T, 1>(p, stream);
+  if (units == 2) return launch_as<T, 2>(p, stream);
+  return units == 3 ? launch_as<T, 3>(p, stream) : launch_as<T, 4>(p, stream);
 }
 
 bool odd(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
