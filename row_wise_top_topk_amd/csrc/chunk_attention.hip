@@ -661,20 +661,25 @@ struct ChunkPlan {
 
 // In how many parts, `most` at most, the walks of `items` workgroups over up to
 // `tiles` tiles are cut.  The 256 compute units take the workgroups in rounds (two
-// small ones on a unit at once need as long as one after the other); where several
-// sequences share the call their lengths differ, so that half of the rounds are
-// counted and no last one.  A tile takes `tile` ns of a unit, `alone` at least; the
-// join costs its launch (with the host's part 10 us) and the partial results' way
-// through memory.
+// small ones on a unit at once need as long as one after the other).  Where several
+// sequences share the call their lengths differ: half of the work is counted, half
+// a walk in which the card runs empty, and an eighth of the join's bytes, which
+// passes over the parts that a sequence does not have.  A tile takes `tile` ns of a
+// unit, `alone` at least; the join costs its launch (with the host's part) and the
+// partial results' way through memory.  Measured: five sequences of 890 tokens behind
+// up to 7000, 12/3 heads: 101 us in one part, 49 in 7, 45 in 11 to 20; four of 200
+// behind 900, 16/4 heads: 23 in one, 28 in 4.
 int parts_of(int64_t items, bool several, int64_t tiles, int64_t rows, int dim, int waves, int64_t most) {
   const int64_t tile = dim == 128 ? (waves == 8 ? 1900 : 1120) : (waves == 8 ? 1300 : 700), alone = dim == 128 ? tile : (waves == 8 ? tile : 950);
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= kSplits && (s == 1 || (s <= most && s <= tiles)); ++s) {
-    const int64_t sixteenths = several ? items * s / 32 : (items * s + 255) / 256 * 16;
-    const int64_t step = tile * sixteenths / 16 > alone ? tile * sixteenths / 16 : alone;
-    const int64_t join = s == 1 ? 0 : 10000 + 200 * s + rows * s * (dim + 2) / 500;  // 8 bytes a value, at 4 TB/s
-    const int64_t cost = step * ((tiles + s - 1) / s) + join;
+    const int64_t walk = (tiles + s - 1) / s, bytes = rows * s * (dim + 2) * 8;
+    int64_t cost;
+    if (several) cost = tile * items * s / 512 * walk + alone * walk / 2;
+    else cost = tile * ((items * s + 255) / 256) * walk;
+    if (cost < alone * walk) cost = alone * walk;
+    if (s > 1) cost += several ? 14000 + 50 * s + bytes / 32000 : 10000 + 200 * s + bytes / 4000;  // (4 TB/s)
     if (cost < least) {
       least = cost;
       best = s;
