@@ -15,6 +15,24 @@
 // multiplies its scores; its V scale joins the exponent: the running maximum is
 // that of x = s + log2 s_v, the weights are 2^(x - max), and the sum of the
 // probabilities adds a page's weights divided by s_v.
+//
+// Measured (bf16, 128 columns unless said): 2048 tokens behind 32000 keys, 64/8
+// heads: 1.93 ms, 1150 TFLOP/s, where a large library product reaches 1240; 8192
+// alone, 32/4 heads: 0.53 ms, 1040 (64 tiles a walk, of which each end costs one);
+// 96 behind 100003, 32/2 heads: 162 us and 12 to join 21 parts; 64 columns, 2048
+// behind 16000, 32/4 heads: 0.37 ms, 780; 33 behind 500, 8/2 heads: 14 us, the chain
+// of nine tiles.  In the first the matrix unit is busy for 52 % of the cycles, the vector
+// unit (of 190 instructions a wavefront and tile 32 are exponentials) about as long,
+// LDS two thirds, at 2.1 GHz: two wavefronts a SIMD cover each other's chains, and
+// the power that the card may draw is near.  64 columns need the same exponentials
+// for half the products.
+//
+// Slower (ms, the first two): four wavefronts a workgroup, 2.30 and 0.59: the codes
+// are widened twice as often; the next tile's scores between this one's weights, in
+// one wavefront, 2.05 and 0.58, by 32 keys 2.25 and 0.55; 64 rows a wavefront, which
+// halve the reads of LDS, with one wavefront a SIMD, 2.96; operands read as they are
+// needed instead of six products ahead, 2.53 and 0.87.  With 64 columns a third and
+// fourth wavefront a SIMD spill.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -116,10 +134,12 @@ struct Codes {
   uint32_t lane;  // byte of its codes in a row
 
   __device__ __forceinline__ explicit Codes(uint32_t base) {
-    const int tid = threadIdx.x;
-    row = (tid / kLanes) % kTile;
-    lane = (tid % kLanes) * 16;
-    to = base + tile_at<D>(row, 2 * (tid % kLanes));
+    // Eight lanes, whose stores go together, write every other chunk of 128 bytes of
+    // two rows 8 apart, which the swizzle takes to different banks.
+    const int tid = threadIdx.x, at = tid % (kTile * kLanes), piece = (at & 3) | (kLanes == 8 ? (at & 8) >> 1 : 0);
+    row = at / (2 * kLanes) % 8 + at / (16 * kLanes) * 16 + (at & 4) * 2;
+    lane = piece * 16;
+    to = base + tile_at<D>(row, 2 * piece);
     if constexpr (kHalves == 1) to += tid / kLanes < kTile ? 0 : 2 * kBuf;
   }
   // `at`: the tile's first key, from the first of the ne blocks that pages[] is of;
@@ -543,7 +563,8 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
 }
 
 // Joins the parts of the rows' walks: a wavefront takes four rows, 16 parts of each
-// at a time to work out their weights, then adds the parts up in order.
+// at a time to work out their weights, then adds the parts up in order.  21 parts of
+// 96 tokens, 32 heads of 128: 34 MB in 12 us, the chain of three loads and memory.
 constexpr int kJoin = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_per) {
