@@ -21,10 +21,10 @@
 // alone, 32/4 heads: 0.53 ms, 1040 (64 tiles a walk, of which each end costs one);
 // 96 behind 100003, 32/2 heads: 162 us and 12 to join 21 parts; 64 columns, 2048
 // behind 16000, 32/4 heads: 0.37 ms, 780; 33 behind 500, 8/2 heads: 14 us, the chain
-// of nine tiles.  In the first the matrix unit is busy for 52 % of the cycles, the vector
-// unit (of 190 instructions a wavefront and tile 32 are exponentials) about as long,
-// LDS two thirds, at 2.1 GHz: two wavefronts a SIMD cover each other's chains, and
-// the power that the card may draw is near.  64 columns need the same exponentials
+// of nine tiles.  In the first the matrix unit is busy for 59 % of the cycles, the
+// vector unit (of 155 instructions a wavefront and tile 32 are exponentials) about as
+// long, LDS for 70 %: two wavefronts a SIMD cover each other's chains, and the card's
+// power holds the clock at 1.85 GHz, as in the library's product (69 %).  64 columns need the same exponentials
 // for half the products.
 //
 // Slower (ms, the first two): four wavefronts a workgroup, 2.30 and 0.59: the codes

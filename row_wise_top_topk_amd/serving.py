@@ -12,7 +12,7 @@ can be captured into a graph, and two graphs share nothing.
     kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens=cu)
     ...
     rows = penalize_logits(logits, tokens, lengths, repetition=r, mask=grammar)
-    best = topk_indices(rows, vocab, 40, order="value")
+    best = topk_indices(rows, ids, 40, order="value")        # ids: the vocabulary's size, a row each
     copies = pages_fork(block_table, lengths, refs, parents, 64)
     pages_copy(k_cache, v_cache, k_scale, v_scale, copies)   # in each layer's cache
 
