@@ -24,8 +24,8 @@
 // of nine tiles.  In the first the matrix unit is busy for 59 % of the cycles, the
 // vector unit (of 155 instructions a wavefront and tile 32 are exponentials) about as
 // long, LDS for 70 %: two wavefronts a SIMD cover each other's chains, and the card's
-// power holds the clock at 1.85 GHz, as in the library's product (69 %).  64 columns need the same exponentials
-// for half the products.
+// power holds the clock at 1.85 GHz, as in the library's product (69 %).  64 columns
+// need the same exponentials for half the products.
 //
 // Slower (ms, the first two): four wavefronts a workgroup, 2.30 and 0.59: the codes
 // are widened twice as often; the next tile's scores between this one's weights, in
@@ -661,13 +661,13 @@ void launch_walk(const ChunkArgs& p, unsigned grid, hipStream_t stream) {
 template <typename T, int D>
 int launch_chunk(const ChunkArgs& p, int waves, hipStream_t stream) {
   const int64_t grid = p.slots * p.kv_heads * p.splits;
-  if (grid > INT32_MAX) return MI_ATTN_EINVAL;
+  if (grid > UINT32_MAX / (waves * 64)) return MI_ATTN_EINVAL;  // a launch has less than 2^32 threads
   if (waves == 8) launch_walk<T, D, 8>(p, static_cast<unsigned>(grid), stream);
   else launch_walk<T, D, 4>(p, static_cast<unsigned>(grid), stream);
   if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   if (p.splits > 1) {
     const int64_t joins = p.slots * p.kv_heads * waves * 8 / kJoin;
-    if (joins > INT32_MAX) return MI_ATTN_EINVAL;
+    if (joins > UINT32_MAX / 256) return MI_ATTN_EINVAL;
     chunk_join_kernel<T, D><<<dim3(static_cast<unsigned>(joins)), dim3(256), 0, stream>>>(p, waves * 32);
     if (hipGetLastError() != hipSuccess) return MI_ATTN_ELAUNCH;
   }

@@ -202,7 +202,7 @@ template <typename T, int kUnits>
 int launch_as(LogitArgs p, hipStream_t stream) {
   const int64_t all = workgroups(p, kUnits), grid = (all + kDies - 1) / kDies * kDies;
   p.stretches = static_cast<int>(all / p.rows);
-  if (grid > INT32_MAX) return MI_ATTN_EINVAL;
+  if (grid > UINT32_MAX / kThreads) return MI_ATTN_EINVAL;  // a launch has less than 2^32 threads
   const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
   if (p.token_cols > 0 || p.bias_cols > 0) penalize_kernel<T, true, kUnits><<<g, b, 0, stream>>>(p);
   else penalize_kernel<T, false, kUnits><<<g, b, 0, stream>>>(p);

@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWords = 64;              // words of free bits of a chunk
 constexpr int kChunk = kWords * 64;     // pages of a chunk
+constexpr int64_t kMostBlocks = UINT32_MAX / kThreads;  // a launch has less than 2^32 threads
 constexpr int kAtOnce = 8;              // entries of a row that a thread has in flight
 
 struct PagesArgs {
@@ -785,16 +786,17 @@ MI_PAGES_EXPORT int pages_update(const mi_pages_args* a, hipStream_t stream) {
   const dim3 b(kThreads);
   auto blocks = [](int64_t n) { return dim3(static_cast<unsigned>(n)); };
   if (a->op == MI_PAGES_FORK) {
-    if (p.chunks + p.rows > INT32_MAX) return MI_ATTN_EINVAL;
+    if (p.chunks + p.rows > kMostBlocks) return MI_ATTN_EINVAL;
     fork_rows_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
     fork_write_kernel<<<blocks(p.chunks + p.rows), b, 0, stream>>>(p);
     fork_last_kernel<<<blocks((static_cast<int64_t>(p.rows) + 3) / 4), b, 0, stream>>>(p);
   } else if (a->op == MI_PAGES_GROW) {
+    if (p.rows > kMostBlocks) return MI_ATTN_EINVAL;
     grow_ask_kernel<<<blocks(p.chunks + (static_cast<int64_t>(p.rows) + kThreads - 1) / kThreads), b, 0, stream>>>(p);
     grow_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
   } else {
     const int64_t pairs = (p.pages / 2 + kThreads - 1) / kThreads;
-    if (pairs + p.rows > INT32_MAX) return MI_ATTN_EINVAL;
+    if (pairs + p.rows > kMostBlocks) return MI_ATTN_EINVAL;
     free_kernel<<<blocks(p.chunks), b, 0, stream>>>(p);
     compact_list_kernel<<<blocks(p.chunks), b, 0, stream>>>(p);
     compact_rows_kernel<<<blocks(pairs + (entries ? p.rows : 0)), b, 0, stream>>>(p, pairs);

@@ -87,7 +87,7 @@ def chunk(**kw):
     dict(v=0), dict(out=0), dict(lse=0), dict(lengths=0), dict(block_table=0), dict(k_cache=0), dict(v_cache=0), dict(k_scale=0),
     dict(v_scale=0), dict(q=A + 8), dict(k=A + 2), dict(v=A + 4), dict(out=A + 8), dict(k_cache=A + 8), dict(v_cache=A + 4),
     dict(k_scale=A + 2), dict(v_scale=A + 1), dict(lse=A + 2), dict(lengths=A + 2), dict(block_table=A + 1), dict(cu=A + 2),
-    dict(workspace=A + 8)], ids=str)
+    dict(workspace=A + 8), dict(num_seqs=(1 << 31) - 1), dict(total=(1 << 31) - 1, max_length=100000)], ids=str)
 def test_chunk_attention_refuses(lib, bad):
     assert lib.chunk_attention(ctypes.byref(chunk(**bad)), None) == EINVAL
 
@@ -123,7 +123,8 @@ def pages(**kw):
     dict(num_pages=1 << 31), dict(block_size=8), dict(block_size=24), dict(block_table_cols=1 << 26, block_table_stride=1 << 26),
     dict(block_table=0), dict(lengths=0), dict(refs=0), dict(given=0), dict(out=0), dict(given=0, op=1), dict(out=0, op=1),
     dict(out=0, op=2), dict(block_table=A + 2), dict(lengths=A + 1), dict(refs=A + 2), dict(given=A + 2), dict(out=A + 2),
-    dict(workspace=A + 8)], ids=str)
+    dict(workspace=A + 8), dict(rows=1 << 24, workspace_bytes=1 << 50), dict(rows=1 << 24, op=1, workspace_bytes=1 << 50),
+    dict(rows=1 << 24, op=2, workspace_bytes=1 << 50)], ids=str)
 def test_pages_update_refuses(lib, bad):
     assert lib.pages_update(ctypes.byref(pages(**bad)), None) == EINVAL
 
@@ -168,7 +169,8 @@ def penalize(**kw):
     dict(bias_stride=-1), dict(mask_stride=-1), dict(logits=0), dict(out=0), dict(tokens=0), dict(bias_ids=0), dict(bias=0),
     dict(logits=A + 2), dict(logits=A + 1, dtype=0), dict(out=A + 2), dict(tokens=A + 2), dict(lengths=A + 1), dict(prompt_lengths=A + 2),
     dict(repetition=A + 2), dict(frequency=A + 2), dict(presence=A + 2), dict(bias_ids=A + 2), dict(bias=A + 2), dict(mask=A + 2),
-    dict(out=A, logits_stride=128), dict(out=A, dtype=1)], ids=str)
+    dict(out=A, logits_stride=128), dict(out=A, dtype=1), dict(rows=1 << 23), dict(rows=1 << 16, vocab=1 << 21, logits_stride=1 << 21,
+                                                                                   out_stride=1 << 21)], ids=str)
 def test_logits_penalize_refuses(lib, bad):
     assert lib.logits_penalize(ctypes.byref(penalize(**bad)), None) == EINVAL
     assert lib.logits_penalize(None, None) == EINVAL
