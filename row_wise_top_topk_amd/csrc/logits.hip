@@ -153,12 +153,14 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(LogitArgs p) {
     }
     __syncthreads();
   }
-  const float r = p.repetition == nullptr ? 1.f : p.repetition[row], inverse = 1.f / r;
+  const float r = p.repetition == nullptr ? 1.f : p.repetition[row];
+  // (1 / r can be infinite where y / r is not)
+  const float raise = fabsf(r) < 0x1p-126f ? 0x1p64f : 1.f, divisor = r * raise, inverse = 1.f / divisor;
   const float f = p.frequency == nullptr ? 0.f : p.frequency[row], pr = p.presence == nullptr ? 0.f : p.presence[row];
   const float* bias = p.bias + row * p.bias_stride;
   auto changed = [&](float y, uint32_t w) {
     // y / r: a quotient that one step of Newton's rounds to nearest
-    const float q = y * inverse, near = fmaf(fmaf(-q, r, y), inverse, q);
+    const float z = y * raise, q = z * inverse, near = fmaf(fmaf(-q, divisor, z), inverse, q);
     const float up = fabsf(near) < kInf ? near : q;
     y = (w << (32 - kBiasBit)) != 0 ? (y > 0.f ? up : y * r) : y;
     const uint32_t said = w & kSaid;

@@ -103,6 +103,23 @@ def test_special_values():
     assert torch.isneginf(got[0, 33:]).all() and torch.isfinite(got[0, 6:33]).all()
 
 
+def test_repetitions_at_the_ends_of_their_range():
+    # the product of 1 / r, rounded, and x is within 2^-23 of the quotient, and below the
+    # least normal number each rounding is within 2^-150
+    values = torch.tensor([1.0, 1e-5, 3e38, 3e-39, 1e-45, 0.0, -1.0, -1e-5, -3e38, -3e-39, math.inf, -math.inf])
+    factors = torch.tensor([1e-39, 1e-45, 2e-38, 1.0, 1.5e38, 3e38, 0.0, math.inf])
+    x = {"logits": values.repeat(len(factors), 1), "tokens": torch.arange(len(values), dtype=torch.int32).repeat(len(factors), 1),
+         "repetition": factors}
+    got = mt.penalize_logits(**put(x)).cpu().double()
+    y, r = x["logits"].double(), factors.double()[:, None]
+    want = torch.where(y > 0, y / r, y * r)
+    large = want.abs() > torch.finfo(torch.float32).max * (1 + 2 ** -25)
+    want = torch.where(large, want.sign() * math.inf, want)
+    same = (got == want) | (got.isnan() & want.isnan())
+    off = (got - want).abs() <= want.abs() * 2 ** -22 + 2 ** -149
+    assert (same | (off & torch.isfinite(want))).all(), (got, want)
+
+
 def test_the_last_bias_of_an_id_counts():
     x = {"logits": torch.zeros(1, 10), "bias_ids": torch.tensor([[3, 3, 4, 3, 4]], dtype=torch.int32),
          "bias": torch.tensor([[1.0, 2.0, 3.0, 4.0, 5.0]])}
