@@ -724,17 +724,20 @@ ChunkPlan plan_of(const mi_chunk_attention_args* a) {
     return (seqs <= 1 ? (a->total + p.tokens_per - 1) / p.tokens_per : a->total / p.tokens_per + seqs) * a->kv_heads;
   };
   // Eight wavefronts a workgroup widen the codes once for 256 rows; four start
-  // quicker and leave fewer rows empty.  Eight where there are 4000 tiles or more to
-  // walk over, unless there are many short sequences, a third as many as whole
-  // workgroups (half of a sequence's last workgroup is empty in the mean).  Measured
-  // (us, eight against four, each with its best parts): 128 columns: 96 tokens behind
-  // 100003, 32/2 heads (18800 tiles): 190, 210; 512 behind 4000, 32/8 (4700): 61, 64;
-  // 2000 behind 2000, 8/1 (4100): 56, 59; 300 behind 3000, 16/2 (1000): 37, 34; 128
-  // behind 8000, 8/8 (1000): 33, 30; 1000 alone, 16/4 (1100): 32, 25; 64 single tokens
-  // and 512, 32/8: 145, 95.  64 columns: five sequences of 890 tokens, 12/3: 50, 45;
-  // four of 200 behind 900, 16/4: 28, 23; 33 behind 500, 8/2: 17.6, 14.1.
+  // quicker, leave fewer rows empty and with 64 columns run three workgroups on a unit
+  // instead of one.  Eight where there are 4000 tiles or more to walk over, unless
+  // there are several sequences, with 128 columns a third as many as whole workgroups
+  // (half of a sequence's last workgroup is empty in the mean).  Measured (us, eight
+  // against four, each with its best parts): 128 columns: 96 tokens behind 100003, 32/2
+  // heads (18800 tiles): 190, 210; 512 behind 4000, 32/8 (4700): 61, 64; 2000 behind
+  // 2000, 8/1 (4100): 56, 59; 300 behind 3000, 16/2 (1000): 37, 34; 128 behind 8000,
+  // 8/8 (1000): 33, 30; 1000 alone, 16/4 (1100): 32, 25; 16 of 256 behind 2000, 32/8:
+  // 163, 170; 30 of 100 behind 3000, 64/8: 398, 377; 64 single tokens and 512, 32/8:
+  // 145, 95.  64 columns: 2048 behind 64000, 16/2: 715, 740; 8192 alone, 32/8: 350,
+  // 335; 8 of 1000 behind 1000, 16/4: 95, 91; 64 of 128 behind 4000, 16/2: 235, 197;
+  // five of 890 tokens, 12/3: 58, 46; 33 behind 500, 8/2: 17.6, 14.1.
   int64_t items = with(8);
-  if (items * tiles < 4000 || (seqs > 1 && 3 * seqs > a->total / p.tokens_per)) items = with(4);
+  if (items * tiles < 4000 || (seqs > 1 && (a->dim == 64 || 3 * seqs > a->total / p.tokens_per))) items = with(4);
   // partial results of 2^17 rows at most (68 MB with 128 columns)
   const int64_t rows = p.slots * a->kv_heads * p.waves * 32;
   const int64_t splits = items > 0 ? parts_of(items, seqs > 1, tiles, a->total * a->heads, a->dim, p.waves, (int64_t{1} << 17) / rows) : 1;

@@ -112,6 +112,17 @@ def test_lengths_around_tiles(dtype, d, bs, heads, hk):
         check(x, bs, mt.chunk_attention(**put(x)))
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("d,bs,heads,hk", [(64, 16, 8, 2), (64, 128, 6, 6), (128, 32, 3, 1), (128, 64, 16, 2)])
+def test_one_sequence_in_a_wide_table(dtype, d, bs, heads, hk):
+    # room for 200000 keys: workgroups of 256 rows, in parts most of which are empty
+    for n, m in ((70, 70), (1, 900), (129, 1500), (300, 301)):
+        x = build(n, [m], [n], heads, hk, d, bs, dtype, extra=1, cols=200000 // bs)
+        check(x, bs, mt.chunk_attention(**put(x)))
+    x = build(5, [4300], [400], heads, hk, d, bs, dtype, cols=60000 // bs)
+    check(x, bs, mt.chunk_attention(**put(x)))
+
+
 @pytest.mark.parametrize("max_length", [None, 1, 100, 5000])
 @pytest.mark.parametrize("bs,d", [(16, 64), (128, 128), (64, 128)])
 def test_split_walks(max_length, bs, d):
