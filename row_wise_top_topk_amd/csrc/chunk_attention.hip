@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
   sum = half_sum(sum);
   const float base = m - kLower;
   if (!valid) return;
-  if (p.splits == 1) {
+  if (p.splits == 1 || rw.tiles <= p.chunk) {  // the walk is in one part
     store_chunk_row<T, D>(p, tok, head, half, acc, base, sum, sees);
     return;
   }
@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_p
   }
   const ChunkRows rw = rows_of(p, p.slots - 1 - from_last);
   const int rows = rw.tokens * p.group;  // those there are
-  if (row0 >= rows) return;
-  const int used = min(p.splits, max(1, (rw.tiles + p.chunk - 1) / p.chunk));
+  if (row0 >= rows || rw.tiles <= p.chunk) return;  // (the latter is done)
+  const int used = min(p.splits, (rw.tiles + p.chunk - 1) / p.chunk);
   float base[kSplits / 16], f[kSplits / 16], top = -kInf, l = 0.f;
 #pragma unroll
   for (int c = 0; c < kSplits / 16; ++c) {
