@@ -42,7 +42,14 @@ extern "C" {
  *              mi_block_attention.h (k's and v's token strides likewise below
  *              MI_ATTN_MAX_STRIDE).
  *   out        [total][H][D] of `dtype`, contiguous; lse fp32 [total][H].
- *   scales     positive and finite; V scales as in kv8_attention().
+ *   scales     positive and finite; V scales count as between 2^-80 and 2^100.
+ *              Where those that one query sees (new tokens: 1) lie more than 2^100
+ *              apart, keys under the smaller ones lose their share of the
+ *              weights' sum.  fp16 weights are kept to 2^-37 of a row's largest
+ *              where V scales lie in [2^-15, 2^8); below, what is lost is less
+ *              than half of fp16's least step for up to 2^18 keys; from 2^8 on,
+ *              where full codes pass fp16's range, it is 2^-37 of the largest
+ *              product of a weight and its scale.
  *   max_length the caller's bound of the lengths: the work is split by it, longer
  *              sequences are computed right but slowly.
  *   workspace  chunk_attention_workspace() bytes, 16-byte aligned, need not be

@@ -14,7 +14,12 @@
 // weights are the second product's operand as they stand.  A page's K scale
 // multiplies its scores; its V scale joins the exponent: the running maximum is
 // that of x = s + log2 s_v, the weights are 2^(x - max), and the sum of the
-// probabilities adds a page's weights divided by s_v.
+// probabilities adds a page's weights divided by s_v.  With fp16 the codes take the
+// scale's power of two on their way to LDS, as far as they stay exact, and the
+// exponent what is left of it: fp16 weights reach no further than 2^-36 of the
+// largest, so that keys in pages of small scales would lose theirs beside new
+// tokens, whose values have the scale 1 and may be as small (32000 keys of 2^-20
+// beside one of value 0, a scale of 2^-17: 0 instead of 0.03 of the values).
 //
 // Measured (bf16, 128 columns unless said): 2048 tokens behind 32000 keys, 64/8
 // heads: 1.93 ms, 1150 TFLOP/s, where a large library product reaches 1240; 8192
@@ -49,6 +54,11 @@ constexpr int kSplits = 64;   // parts of a walk, at most
 // V scales are held between these: 2^30 weights of up to 2^15, divided by the
 // least, stay within fp32
 constexpr float kLeast = 0x1p-80f, kMost = 0x1p100f;
+// fp16 holds every code times these powers of two and those between: codes go from
+// 2^-9 to 448, fp16 from 2^-24 to 65504
+constexpr int kUpLeast = -15, kUpMost = 7;
+template <typename T>
+constexpr bool kUp = __is_same(T, Fp16);  // bf16 weights have fp32's exponents and need none
 
 struct ChunkArgs {
   const char* q;
@@ -120,6 +130,7 @@ __device__ u32x4 nothing[kTile * 128 / 16];
 // NW wavefronts, in registers while the tile before it is worked on; the pages of
 // the tile behind it are looked up meanwhile.  A thread has 16 codes of each of
 // kPer rows, kStep rows apart, of the keys and of the values (or of one of them).
+// Values are multiplied by the power of two of their page.
 template <typename T, int D, int NW, bool kWide>
 struct Codes {
   static constexpr int kThreads = NW * 64, kLanes = D / 16, kUnits = 2 * kTile * kLanes / kThreads;
@@ -174,15 +185,27 @@ struct Codes {
       }
     }
   }
+  // The powers of two of the rows of the tile at `at`, as look() finds their pages.
+  __device__ __forceinline__ void powers(const ChunkArgs& p, const float* ups, int ne, int at, float (&up)[kPages]) const {
+#pragma unroll
+    for (int j = 0; j < kPages; ++j) {
+      up[j] = 1.f;
+      if constexpr (kUp<T>) {
+        const float of_page = ups[min((at + (kWide ? 0 : row + j * kStep)) >> p.lb, ne - 1)];
+        if (kHalves == 2 || static_cast<int>(threadIdx.x) / kLanes >= kTile) up[j] = of_page;  // (else the thread has keys)
+      }
+    }
+  }
   template <int buf>
-  __device__ __forceinline__ void store() const {
+  __device__ __forceinline__ void store(const float (&up)[kPages]) const {
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         constexpr int kApart = kStep * 2 * D;
-        *reinterpret_cast<MI_LDS u32x4*>(to + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][0], x[h][j][1]});
-        *reinterpret_cast<MI_LDS u32x4*>((to ^ 16) + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][2], x[h][j][3]});
+        const float by = kHalves == 2 && h == 0 ? 1.f : up[kWide ? 0 : j];
+        *reinterpret_cast<MI_LDS u32x4*>(to + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][0], x[h][j][1]}, by);
+        *reinterpret_cast<MI_LDS u32x4*>((to ^ 16) + (2 * h + buf) * kBuf + j * kApart) = widen<T>(u32x2{x[h][j][2], x[h][j][3]}, by);
       }
   }
 };
@@ -231,12 +254,13 @@ struct Fresh {
   }
 };
 
-template <int D>
+template <typename T, int D>
 struct ChunkShared {
   char k[2][kTile * 2 * D];
   char v[2][kTile * 2 * D];
   int32_t page[kSeg];  // -1: not there
   float ks[kSeg], lv[kSeg], iv[kSeg];
+  float up[kUp<T> ? kSeg : 1];
 };
 
 // A row's output from lane half `half`, which has the columns 32 i + 8 (r / 4) +
@@ -261,7 +285,7 @@ template <typename T, int D, bool kWide, int NW>
 __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p) {
   constexpr int kRowsHere = NW * 32;
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  ChunkShared<D>& sh = *reinterpret_cast<ChunkShared<D>*>(smem);
+  ChunkShared<T, D>& sh = *reinterpret_cast<ChunkShared<T, D>*>(smem);
   const int hk = blockIdx.x % p.kv_heads;
   const uint32_t rest = blockIdx.x / p.kv_heads;
   const int split = static_cast<int>(rest % p.splits);
@@ -294,7 +318,8 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
   const float c = p.scale * kLog2e;
   const Reads<D> rd(lds_offset(sh.k[0]));
   constexpr int kBuf = kTile * 2 * D;  // from one buffer to the other; the values lie two behind the keys
-  // A weight is rounded once, to the type of q.  fp16 has no bits below 2^-24, so
+  // A weight is rounded once, to the type of q, since the matrix unit takes no wider
+  // operand at this rate (2^-8 of it at most with bf16, 2^-11 with fp16).  fp16 has no bits below 2^-24, so
   // there the weights are relative to a maximum 2^12 below the row's, and with the
   // 2^3 that this may lag behind they go up to 2^15 (bf16 has fp32's exponents)
   constexpr float kLag = __is_same(T, Fp16) ? 3.f : 8.f, kLower = __is_same(T, Fp16) ? 12.f : 0.f;
@@ -484,13 +509,22 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     in.load(p, hk, at_of(s0), left_of(s0));
     if (tid < ne) {  // the scales come while the first codes do
       const int64_t at = static_cast<int64_t>(max(0, pg)) * p.kv_heads + hk;
-      const float ks = p.scales[0][at], vs = pg < 0 ? 1.f : fminf(fmaxf(p.scales[1][at], kLeast), kMost);
+      const float ks = p.scales[0][at];
+      float vs = pg < 0 ? 1.f : fminf(fmaxf(p.scales[1][at], kLeast), kMost);
+      if constexpr (kUp<T>) {
+        const int e = max(kUpLeast, min(static_cast<int>(__float_as_uint(vs) >> 23) - 127, kUpMost));
+        sh.up[tid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        vs *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // what is left of it, exactly
+      }
       sh.ks[tid] = pg < 0 ? 1.f : fmaxf(ks * c, 0x1p-149f);
       sh.lv[tid] = pg < 0 ? -kInf : __builtin_amdgcn_logf(vs);  // no weight
       sh.iv[tid] = 1.f / vs;
     }
     in.look(p, sh.page, ne, at_of(s0 + 1));
-    in.template store<0>();
+    if constexpr (kUp<T>) __syncthreads();
+    float up[decltype(in)::kPages];
+    in.powers(p, sh.up, ne, at_of(s0), up);
+    in.template store<0>(up);
     in.load(p, hk, at_of(s0 + 1), left_of(s0 + 1));
     in.look(p, sh.page, ne, at_of(s0 + 2));
     __syncthreads();
@@ -505,7 +539,8 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
         iv[i] = sh.iv[e];
       }
       const int left = left_of(t);
-      work(which, Int<1>{}, Int<2 * decltype(in)::kUnits>{}, left < kTile, 0, left - 1, ck, lv, iv, [&] { in.template store<buf ^ 1>(); },
+      in.powers(p, sh.up, ne, at_of(t + 1), up);
+      work(which, Int<1>{}, Int<2 * decltype(in)::kUnits>{}, left < kTile, 0, left - 1, ck, lv, iv, [&] { in.template store<buf ^ 1>(up); },
            [&] {
              in.load(p, hk, at_of(t + 2), left_of(t + 2));
              in.look(p, sh.page, ne, at_of(t + 3));
@@ -653,7 +688,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_p
 
 template <typename T, int D, int NW>
 void launch_walk(const ChunkArgs& p, unsigned grid, hipStream_t stream) {
-  const size_t lds = sizeof(ChunkShared<D>);
+  const size_t lds = sizeof(ChunkShared<T, D>);
   if (p.lb >= 6) chunk_attention_kernel<T, D, true, NW><<<dim3(grid), dim3(NW * 64), lds, stream>>>(p);
   else chunk_attention_kernel<T, D, false, NW><<<dim3(grid), dim3(NW * 64), lds, stream>>>(p);
 }

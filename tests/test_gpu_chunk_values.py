@@ -1,0 +1,80 @@
+"""GPU: attention of a chunk whose values are small or large as a whole, or not finite.
+
+Tolerances as in test_gpu_chunk.py.  Where all of a result comes from keys of one
+value it is also relative to the result: a weight's rounding (u), the result's (u),
+and 2 e of the scores; fp16 results below 2^-14 are rounded to multiples of 2^-24.
+"""
+
+import math
+
+import pytest
+import torch
+
+import row_wise_top_topk_amd as mt
+from test_gpu_chunk import build, check, put
+
+pytestmark = pytest.mark.gpu
+
+F16 = 2 ** -11
+
+
+def far_ahead(ratio, n, d, bs, v_exponent, in_cache):
+    """One key of value 0 far ahead of n others: 2^-ratio each, of one code.  Returns
+    the inputs, what the others add up to, and the error of the scores."""
+    x = build(1, [n + 1 + in_cache], [1], 1, 1, d, bs, torch.float16)
+    for name in ("q", "k", "v"):
+        x[name].zero_()
+    x["k_cache"].zero_()
+    x["k_scale"].fill_(1.0)
+    x["v_cache"].fill_(256.0)
+    x["v_scale"].fill_(2.0 ** v_exponent)
+    x["q"][0, 0, 0] = 16.0
+    want = ratio * math.log(2) / 16 * math.sqrt(d)
+    if in_cache:  # the key ahead is the cache's first one, in a page whose scale is 1
+        page = int(x["block_table"][0, 0])
+        x["k"][0, 0, 0] = -60000.0   # the new token has no weight
+        x["k_cache"][page, 0, 0, 0], x["k_scale"][page, 0] = 256.0, want / 256
+        x["v_cache"][page], x["v_scale"][page, 0] = 0.0, 1.0
+        score, some = 16 * float(x["k_scale"][page, 0]) * 256 / math.sqrt(d), n + 1 - bs
+    else:
+        x["k"][0, 0, 0] = want
+        score, some = 16 * float(x["k"][0, 0, 0]) / math.sqrt(d), n
+    p = math.exp(-score)
+    return x, 256 * 2.0 ** v_exponent * some * p / (1 + n * p), 2 ** -24 * (d + 64) * score + 2 ** -22 * score
+
+
+@pytest.mark.parametrize("max_length", [1, None])    # the walk in one part, in several
+@pytest.mark.parametrize("d,bs", [(64, 16), (64, 128), (128, 32), (128, 64)])
+@pytest.mark.parametrize("v_exponent", [-24, -17, -16, -15, -13, -5, 7, 8, 20])
+def test_fp16_small_weights_of_values_of_any_size(v_exponent, d, bs, max_length):
+    n = 32000
+    for ratio in (20, 22):
+        x, want, e = far_ahead(ratio, n, d, bs, v_exponent, 0)
+        got = mt.chunk_attention(**put(x), max_length=max_length)[0].cpu().double()
+        if want * (1 - F16) > 65504:
+            continue
+        # below 2^-15 a scale's rest joins the weight, which is 2^12 times as large and rounded to 2^-24
+        rest = n * 2 ** -37 * 256 * 2 ** -15 if v_exponent < -15 else 0.0
+        assert ((got - want).abs() <= (4 * F16 + 2 * e) * want + 2 ** -25 + rest).all(), (got.flatten()[0].item(), want)
+
+
+@pytest.mark.parametrize("max_length", [1, None])
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 128)])
+@pytest.mark.parametrize("v_exponent", [-15, -10])
+def test_fp16_pages_of_different_scales(v_exponent, d, bs, max_length):
+    x, want, e = far_ahead(20, 32000, d, bs, v_exponent, 1)
+    got = mt.chunk_attention(**put(x), max_length=max_length)[0].cpu().double()
+    assert ((got - want).abs() <= (4 * F16 + 2 * e) * want + 2 ** -25).all(), (got.flatten()[0].item(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,new,heads,hk,d,bs", [([300, 90], [70, 33], 6, 3, 64, 16), ([700], [260], 8, 1, 128, 32), ([1500], [700], 4, 2, 64, 64),
+                                                    ([900, 65], [300, 65], 4, 1, 128, 128)], ids=str)
+def test_small_values_and_any_scales(dtype, lens, new, heads, hk, d, bs):
+    g = torch.Generator().manual_seed(len(lens))
+    for low, high, by in ((-22, -13, -8), (-18, 9, 0), (5, 9, 5)):
+        x = build(high + 30, lens, new, heads, hk, d, bs, dtype)
+        x["v"] = (x["v"].float() * 2.0 ** by).to(dtype)
+        x["v_scale"] = torch.exp2(torch.empty(x["v_scale"].shape).uniform_(low, high, generator=g))
+        x["v_cache"] = x["v_cache"].clamp(-60, 60)   # (results within fp16's range)
+        check(x, bs, mt.chunk_attention(**put(x)))
