@@ -16,7 +16,8 @@
  * than its sequence the tokens that would stand before its start see nothing and
  * are not seen.  A query that sees no key, and a row behind the last sequence,
  * has out 0 and lse -inf.  Infinities and NaN count where they are visible only;
- * a visible infinity among the values whose weight is 0 in 32 bits gives NaN.
+ * those among the values then count whatever their weight, also one that is 0 in
+ * 32 bits.
  *
  * All pointers are device pointers owned by the caller; nothing is allocated or
  * synchronised, all work is enqueued on `stream`, results do not change from

@@ -237,9 +237,10 @@ struct Fresh {
     }
   }
   // kHide: some row does not see all of the tile, so that infinities and NaN among
-  // the values become 0 and are marked
+  // the values become 0; whether there were any
   template <int buf, bool kHide>
-  __device__ __forceinline__ void store(bool& odd) const {
+  __device__ __forceinline__ bool store() const {
+    bool odd = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -251,6 +252,7 @@ struct Fresh {
         }
         *reinterpret_cast<MI_LDS u32x4*>(to + (2 * h + buf) * kBuf + j * (kStep * 2 * D)) = c;
       }
+    return odd;
   }
 };
 
@@ -261,6 +263,7 @@ struct ChunkShared {
   int32_t page[kSeg];  // -1: not there
   float ks[kSeg], lv[kSeg], iv[kSeg];
   float up[kUp<T> ? kSeg : 1];
+  int32_t odd;         // an infinity or NaN is among the values that some row does not see
 };
 
 // A row's output from lane half `half`, which has the columns 32 i + 8 (r / 4) +
@@ -387,10 +390,11 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       const float shrink = now == -kInf ? 1.f : exp2_fast(m - now);
       m = now;
       sum *= shrink;
+      const float keeps = fmaxf(shrink, 0x1p-149f);  // an infinity stays one, nothing else does
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][r] *= shrink;
+        for (int r = 0; r < 16; ++r) acc[i][r] *= keeps;
     }
     get();
     const float base = m == -kInf ? 0.f : m - kLower;
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
 
   // The new tokens: tiles that all rows see, and tiles that some row sees a part of.
   const int n0 = max(e0, rw.tiles_context);
-  bool odd = false;
+  if (tid == 0) sh.odd = 0;
   const int least = max(rw.r0, rw.hidden);  // the first token here that sees anything
   auto first_of = [&](int t) { return (rw.first_new + t - rw.tiles_context) * kTile; };
   auto hides = [&](int t) { return first_of(t) + kTile - 1 > least || first_of(t) < rw.hidden; };
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     in.load(p, hk, rw, first_of(from));
     for (int t = from; t < to; ++t) {
       __syncthreads();
-      in.template store<0, true>(odd);
+      if (in.template store<0, true>()) sh.odd = 1;
       if (t + 1 < to) in.load(p, hk, rw, first_of(t + 1));
       __syncthreads();
       const int first = first_of(t), high = sees ? mine - first : -1;
@@ -461,13 +465,13 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     Fresh<T, D, NW> in(lds_offset(sh.k[0]));
     in.load(p, hk, rw, first_of(from));
     __syncthreads();
-    in.template store<0, false>(odd);
+    in.template store<0, false>();
     in.load(p, hk, rw, first_of(min(from + 1, to - 1)));
     __syncthreads();
     auto step = [&](auto which, int t) {
       constexpr int buf = decltype(which)::value;
       work(which, Int<0>{}, Int<2 * decltype(in)::kPer>{}, false, 0, 0, plain.ck, plain.lv, plain.iv,
-           [&] { in.template store<buf ^ 1, false>(odd); }, [&] { in.load(p, hk, rw, first_of(min(t + 2, to - 1))); });
+           [&] { in.template store<buf ^ 1, false>(); }, [&] { in.load(p, hk, rw, first_of(min(t + 2, to - 1))); });
     };
     for (int t = from; t < to; t += 2) {
       step(Int<0>{}, t);
@@ -475,6 +479,42 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       if (t + 1 < to) {
         step(Int<1>{}, t + 1);
         __syncthreads();
+      }
+    }
+  };
+  // Calls found(key, i, r, x) for the infinities and NaN x in the lane's columns (those
+  // of acc[i][r]) among the values of the new tokens from .. to - 1: a wavefront looks
+  // at 8 KB at a time, and then at the columns of the rows that have any.
+  auto each_odd = [&](int from, int to, auto found) {
+    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kAt = 8;
+    const int at = static_cast<int>(__lane_id());
+    const char* base = p.x[1] + (rw.begin * p.x_t[1] + hk * p.x_h[1]) * 2;
+    auto row_at = [&](int key) { return base + key * (p.x_t[1] * 2); };
+    for (int k0 = from; k0 < to; k0 += kRows * kAt) {
+      u32x4 x[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j)  // (rows behind the last one stand for it: found once more, with the same result)
+        x[j] = *reinterpret_cast<const u32x4*>(row_at(min(k0 + j * kRows + at / kLanes, to - 1)) + at % kLanes * 16);
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        bool any = false;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) finite_only<T>(x[j][z], any);
+        for (uint64_t rows = __ballot(any); rows != 0;) {
+          const int row = (__ffsll(static_cast<unsigned long long>(rows)) - 1) / kLanes;
+          rows &= ~(((1ull << kLanes) - 1) << (row * kLanes));
+          const int key = min(k0 + j * kRows + row, to - 1);
+          const char* v = row_at(key) + (at >> 5) * 8;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(v + i * 64 + (r >> 2) * 16 + (r & 2) * 2);
+              const float a = T::lo(w), b = T::hi(w);
+              if (!(fabsf(a) < kInf)) found(key, i, r, a);
+              if (!(fabsf(b) < kInf)) found(key, i, r + 1, b);
+            }
+        }
       }
     }
   };
@@ -486,8 +526,27 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       walk_part(from, from + 1);
       ++from;
     }
-    if (from < to) walk(from, to);
+    bool odd = false;
+    if (from < to) {
+      walk(from, to);
+      float finite[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) finite[r & 3] = fmaf(acc[i][r], 0.f, finite[r & 3]);
+      odd = __any((finite[0] + finite[1]) + (finite[2] + finite[3]) != 0.f);
+    }
     if (to < e1) walk_part(to, e1);
+    // Infinities and NaN among the values go to the rows that see them whatever their
+    // weight, which the products would take to 16 bits, and 0 times infinity to NaN:
+    // where there are any, their columns start anew and then take them.
+    if (__builtin_expect(odd || sh.odd != 0, 0)) {
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass)
+        each_odd(max(first_of(n0), rw.hidden), min(first_of(e1 - 1) + kTile, rw.r0 + rw.tokens), [&](int key, int i, int r, float x) {
+          if (sees && key <= mine) acc[i][r] = pass == 0 ? 0.f : acc[i][r] + x;
+        });
+    }
   }
 
   // The context, kSeg blocks' tiles at a time.
@@ -556,27 +615,6 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     }
     s0 = s1;
   }
-  // Infinities and NaN among the values that were left out, to the rows that see them
-  if (__syncthreads_or(odd)) {
-    for (int t = n0; t < e1; ++t) {
-      if (!hides(t)) continue;
-      const int from = max(first_of(t), rw.hidden), to = min(first_of(t) + kTile, rw.r0 + rw.tokens);
-      for (int key = from; key < to; ++key) {
-        const char* v = p.x[1] + ((rw.begin + key) * p.x_t[1] + hk * p.x_h[1]) * 2 + half * 8;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(v + i * 64 + (r >> 2) * 16 + (r & 2) * 2);
-            const float a = T::lo(w), b = T::hi(w);
-            if (sees && key <= mine) {
-              if (!(fabsf(a) < kInf)) acc[i][r] += a;
-              if (!(fabsf(b) < kInf)) acc[i][r + 1] += b;
-            }
-          }
-      }
-    }
-  }
   sum = half_sum(sum);
   const float base = m - kLower;
   if (!valid) return;
@@ -636,7 +674,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs p, int rows_p
   for (int c = 0; c < kSplits / 16; ++c) {
     const float w = base[c] == -kInf ? 0.f : exp2_fast(base[c] - top);
     l += f[c] * w;
-    f[c] = w;
+    f[c] = w == 0.f ? 0x1p-149f : w;  // (an infinity in a part of no weight stays one, nothing else does)
   }
   for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
   float o[kJoin][D / 64];

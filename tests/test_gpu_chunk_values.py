@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import row_wise_top_topk_amd as mt
-from test_gpu_chunk import build, check, put
+from test_gpu_chunk import build, check, put, want_of
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,50 @@ def test_small_values_and_any_scales(dtype, lens, new, heads, hk, d, bs):
         x["v_scale"] = torch.exp2(torch.empty(x["v_scale"].shape).uniform_(low, high, generator=g))
         x["v_cache"] = x["v_cache"].clamp(-60, 60)   # (results within fp16's range)
         check(x, bs, mt.chunk_attention(**put(x)))
+
+
+def agree(x, bs, got):
+    """As check(), where the results are finite; infinities and NaN in the same places."""
+    out, lse, size = want_of(x, bs)
+    got_out, got_lse = (t.cpu().double() for t in got)
+    u, d = torch.finfo(x["q"].dtype).eps / 2, x["q"].shape[2]
+    big = max(float(t[torch.isfinite(t)].abs().max()) for t in (x["v"], x["v_cache"] * x["v_scale"][..., None, None]) if torch.isfinite(t).any())
+    e = 2 ** -24 * (d + 64) * size + 2 ** -22 * size
+    assert torch.equal(torch.isnan(got_out), torch.isnan(out))
+    for inf in (math.inf, -math.inf):
+        assert torch.equal(got_out == inf, out == inf)
+    fine = torch.isfinite(out)
+    assert not fine.all() and fine.any()
+    assert ((got_out - out).abs() <= (2.25 * u + 2 * e[..., None]) * big)[fine].all()
+    assert ((got_lse - lse).abs() <= e + 2 ** -23 * lse.abs() + 1e-7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,hk,d,bs", [(4, 1, 64, 16), (6, 2, 64, 64), (3, 1, 128, 32), (8, 2, 128, 128)])
+@pytest.mark.parametrize("score", [0.0, -21.0, -300.0])     # weights that both types have, that fp16 has not, that 32 bits have not
+def test_infinities_and_nan_of_any_weight(score, heads, hk, d, bs, dtype):
+    for new, context, max_length in ((300, 70, None), (300, 0, 1), (620, 0, None)):
+        x = build(new, [new + context, 66], [new, 66], heads, hk, d, bs, dtype)
+        x["q"][:, :, 0], x["k"][:, :, 0] = 8.0, 0.0
+        x["v"][[10, 150, 290, 20, 40], :, [3, 3, 9, 12, 50]] = torch.tensor([math.inf, -math.inf, math.inf, math.nan, -math.inf]).to(dtype)[:, None]
+        x["k"][[10, 150, 290, 20, 40], :, 0] = score * math.sqrt(d) / 8
+        x["k_cache"][:, :, :, 0] = 0.0
+        agree(x, bs, mt.chunk_attention(**put(x), max_length=max_length))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 64)])
+def test_infinities_in_a_part_of_no_weight(d, bs, dtype):
+    # all new tokens far below the context, whose parts have all of the weight
+    x = build(4, [6000 + 140], [140], 2, 1, d, bs, dtype)
+    x["q"][:, :, 0], x["k"][:, :, 0] = 8.0, -300 * math.sqrt(d) / 8
+    x["k_cache"][:, :, :, 0] = 0.0
+    x["v"][[5, 100, 120], 0, [3, 4, 3]] = torch.tensor([math.inf, math.nan, -math.inf]).to(dtype)
+    agree(x, bs, mt.chunk_attention(**put(x)))
+
+
+def test_infinities_and_nan_in_long_prompts():
+    # rows of many tiles that all of them see
+    x = build(6, [1500], [1500], 2, 1, 64, 64, torch.float16)
+    x["v"][[0, 700, 1400], 0, [3, 60, 33]] = torch.tensor([math.inf, math.nan, -math.inf]).to(torch.float16)
+    agree(x, 64, mt.chunk_attention(**put(x)))
