@@ -119,10 +119,22 @@ def _run(device, what: str, fn, *args) -> None:
         raise RuntimeError(f"{what} failed: {_STATUS.get(status, 'unknown status')} (status {status})")
 
 
+def _dual_level() -> bool:
+    """Whether operands can have a forward-mode derivative."""
+    return getattr(_forward_ad, "_current_level", 0) >= 0
+
+
 def _no_tangent(t, what: str) -> None:
     """Refuses an operand with a forward-mode derivative, which the result would not have."""
-    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+    if _dual_level() and _forward_ad.unpack_dual(t).tangent is not None:
         raise ValueError(f"{what} has a tangent: there is no forward-mode derivative")
+
+
+def _no_tangents(operands) -> None:
+    """Likewise of (operand, name) pairs, where None is none."""
+    for t, what in operands:
+        if isinstance(t, torch.Tensor):
+            _no_tangent(t, what)
 
 
 def _heads(t, what: str, device=None, dtype=None, dim=None):

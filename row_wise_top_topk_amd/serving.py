@@ -29,8 +29,8 @@ import ctypes
 
 import torch
 
-from .attention import (_DTYPES, _block_size, _cache, _cache_sequences, _f32, _groups, _heads, _i32, _i64, _ints, _lib, _like,
-                        _no_tangent, _output, _ptr, _run, _scale, _table, _vp)
+from .attention import (_DTYPES, _block_size, _cache, _cache_sequences, _dual_level, _f32, _groups, _heads, _i32, _i64, _ints,
+                        _lib, _like, _no_tangents, _output, _ptr, _run, _scale, _table, _vp)
 
 __all__ = ["chunk_attention", "pages_fork", "pages_grow", "pages_compact", "pages_copy", "penalize_logits"]
 
@@ -270,10 +270,12 @@ def penalize_logits(logits: torch.Tensor, tokens: torch.Tensor = None, lengths: 
     ``[rows, (vocab + 31) // 32]``.  What is not given changes nothing; ids outside
     the vocabulary (-1 for padding) count nowhere.  Returns float32 ``[rows,
     vocab]``; ``out`` may be ``logits`` itself where that is float32, and shares no
-    memory with it otherwise."""
+    memory with it otherwise.  It has no gradient, whatever the operands ask for;
+    operands with a forward-mode derivative are refused."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS or logits.dim() != 2:
         raise ValueError("logits must be a 2-D bfloat16, float16 or float32 tensor [rows, vocab]")
-    _no_tangent(logits, "logits")
+    if _dual_level():
+        _no_tangents(((logits, "logits"), (repetition, "repetition"), (presence, "presence"), (frequency, "frequency"), (bias, "bias")))
     if not logits.is_cuda:
         raise ValueError("logits must be on a GPU")
     device = logits.device
