@@ -501,6 +501,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, device, hk=None, dim=None):
         if (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous()
                 or t.device != device):
             raise ValueError(f"{what} must be a contiguous float32 tensor [pages, kv_heads] on the others' device")
+    if _dual_level():
+        _no_tangents(((k_scale, "k_scale"), (v_scale, "v_scale")))
     return pages, heads, bs, d
 
 
@@ -541,6 +543,7 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache:
     _cache_sequences(cu_seqlens, lengths, n, total, device)
     if k_mean is not None:
         _output(k_mean, (pages, hk, dim), torch.float32, device, "k_mean")
+        _no_tangent(k_mean, "k_mean")
     a.k, a.v, a.k_cache, a.v_cache = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     a.k_scale, a.v_scale, a.k_mean = k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_mean)
     a.block_table, a.lengths, a.cu = block_table.data_ptr(), lengths.data_ptr(), _ptr(cu_seqlens)

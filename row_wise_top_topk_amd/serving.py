@@ -30,7 +30,7 @@ import ctypes
 import torch
 
 from .attention import (_DTYPES, _block_size, _cache, _cache_sequences, _dual_level, _f32, _groups, _heads, _i32, _i64, _ints,
-                        _lib, _like, _no_tangents, _output, _ptr, _run, _scale, _table, _vp)
+                        _lib, _like, _no_tangent, _no_tangents, _output, _ptr, _run, _scale, _table, _vp)
 
 __all__ = ["chunk_attention", "pages_fork", "pages_grow", "pages_compact", "pages_copy", "penalize_logits"]
 
@@ -219,6 +219,7 @@ def pages_copy(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tens
         raise ValueError("copies must have the shape [n, 2]")
     if k_mean is not None:
         _output(k_mean, (pages, hk, dim), torch.float32, device, "k_mean")
+        _no_tangent(k_mean, "k_mean")
     a = _CopyArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_mean), copies.data_ptr(),
                   copies.shape[0], pages, hk, dim, bs)
     _run(device, "pages_copy", _lib().pages_copy, ctypes.byref(a))
