@@ -6,8 +6,11 @@
 // free pages for each 4096; F(p), the number of free pages below p, is then a sum
 // of those numbers and of a few words' bits, so that the r-th free page is found
 // by one wavefront in two scans, and a page's own rank by two loads.  No kernel
-// waits for another workgroup, and only counts of holders are changed by atomics
-// (integers: their order does not matter).
+// waits for another workgroup, and only counts of holders and the least numbers of
+// forks are changed by atomics (integers: their order does not matter).  What the rows
+// before a row ask for is summed over groups of 1024 first, so that a call's work grows
+// with the rows, and with their square by a thousandth of it only (2^20 rows that all
+// ask: 1.9 ms to fork and 2.2 to grow, where sums row by row took 284 and 211).
 //
 // The bytes are few (512 rows of 1875 entries: 7 MB with the pages copied, 1.5 us at
 // the rate of a large copy), so that these kernels are chains of loads, each behind
@@ -33,6 +36,7 @@ constexpr int kWords = 64;              // words of free bits of a chunk
 constexpr int kChunk = kWords * 64;     // pages of a chunk
 constexpr int64_t kMostBlocks = UINT32_MAX / kThreads;  // a launch has less than 2^32 threads
 constexpr int kAtOnce = 8;              // entries of a row that a thread has in flight
+constexpr int kGroup = 1024;            // rows whose asks are summed once for all rows behind them
 
 struct PagesArgs {
   int32_t* table;
@@ -44,6 +48,8 @@ struct PagesArgs {
   int32_t* counts;   // [chunks] free pages
   int32_t* before;   // compact: [chunks * kWords] free pages below the word's first one
   int32_t* asks;     // fork, grow: [rows] pages that a row asks for
+  int64_t* sums;     // fork, grow: [groups] pages that a group's rows ask for
+  int32_t* first;    // fork of many rows: [rows] who keeps the row's last page: -1 the row itself, else the first fork
   int32_t* source;   // fork: [rows] page to copy, -1: none
   int32_t* length;   // fork: [rows] new lengths
   int32_t* rows_new; // fork: [rows][cols] new entries
@@ -61,15 +67,16 @@ __device__ __forceinline__ int wave_scan(int x) {  // inclusive
   return x;
 }
 
-__device__ __forceinline__ int wave_sum(int x) {
+template <typename N>
+__device__ __forceinline__ N wave_sum(N x) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
   return x;
 }
 
 // Sums over the workgroup; every thread gets them.
-template <int N>
-__device__ __forceinline__ void block_sums(int (&x)[N], int (*box)[kThreads / 64]) {
+template <typename T, int N>
+__device__ __forceinline__ void block_sums(T (&x)[N], T (*box)[kThreads / 64]) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -161,6 +168,19 @@ __device__ __forceinline__ Spot find_free(const PagesArgs& p, int64_t rank) {
   return s;
 }
 
+// Fork of many rows, before the first step: who keeps each row's last page.
+__global__ void __launch_bounds__(kThreads) fork_clear_kernel(PagesArgs p) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (row < p.rows) p.first[row] = p.rows;
+}
+
+__global__ void __launch_bounds__(kThreads) fork_first_kernel(PagesArgs p) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (row >= p.rows) return;
+  const int parent = p.in[row];
+  if (parent >= 0 && parent < p.rows) atomicMin(p.first + parent, parent == row ? -1 : static_cast<int>(row));
+}
+
 // Fork, first step: what each row becomes, beside the table, since others may
 // still read what it was.  One workgroup a row.
 __global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
@@ -184,17 +204,21 @@ __global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
   if (part) {
     source = from[whole];
     // who keeps the parent's last page: the parent, or the first of its forks
-    if (tid == 0) s_first = p.in[parent] == parent ? -1 : row;
-    __syncthreads();
-    if (s_first >= 0) {
-      for (int i = tid; i < row; i += kThreads)
-        if (p.in[i] == parent) {
-          atomicMin(&s_first, i);
-          break;
-        }
+    if (p.first != nullptr) {
+      holds = p.first[parent] == row;
+    } else {
+      if (tid == 0) s_first = p.in[parent] == parent ? -1 : row;
       __syncthreads();
+      if (s_first >= 0) {
+        for (int i = tid; i < row; i += kThreads)
+          if (p.in[i] == parent) {
+            atomicMin(&s_first, i);
+            break;
+          }
+        __syncthreads();
+      }
+      holds = s_first == row;
     }
-    holds = s_first == row;
     if (source < 0 || source >= p.pages) {  // not there: handed on as it is
       holds = true;
       source = -1;
@@ -227,14 +251,25 @@ __global__ void __launch_bounds__(kThreads) fork_rows_kernel(PagesArgs p) {
   }
 }
 
-// Fork, second step: the free pages, and the rows' new entries to the table.
+// Fork, second step: the free pages, what the groups of rows (but the last) ask for,
+// and the rows' new entries to the table.
 __global__ void __launch_bounds__(kThreads) fork_write_kernel(PagesArgs p) {
   __shared__ int box[kThreads / 64];
   if (blockIdx.x < p.chunks) {
     free_bits(p, blockIdx.x, box);
     return;
   }
-  const int row = static_cast<int>(blockIdx.x - p.chunks);
+  const int64_t place = blockIdx.x - p.chunks;
+  if (place >= p.rows) {
+    const int32_t* asks = p.asks + (place - p.rows) * kGroup;
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup / kThreads; ++i) all += asks[i * kThreads + threadIdx.x];
+    all = block_sum(all, box);
+    if (threadIdx.x == 0) p.sums[place - p.rows] = all;
+    return;
+  }
+  const int row = static_cast<int>(place);
   if (p.in[row] == row) return;
   const int32_t* next = p.rows_new + static_cast<int64_t>(row) * p.cols;
   int32_t* mine = p.table + row * p.stride;
@@ -258,14 +293,16 @@ __global__ void __launch_bounds__(kThreads) fork_last_kernel(PagesArgs p) {
   int source = -1, page = -1, length = stays ? 0 : length_new;
   if (asks_here != 0) {
     source = from;
-    int rank = 0;
-    for (int64_t i0 = lane; i0 < row; i0 += 64 * kAtOnce) {
+    int rank = 0;  // (no row asks for more than one)
+    const int64_t group = row / kGroup;
+    for (int64_t i0 = group * kGroup + lane; i0 < row; i0 += 64 * kAtOnce) {
       int asks[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) asks[i] = p.asks[min(i0 + i * 64, row)];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) rank += i0 + i * 64 < row ? asks[i] : 0;
     }
+    for (int64_t g = lane; g < group; g += 64) rank += static_cast<int>(p.sums[g]);
     const Spot s = find_free(p, wave_sum(rank));
     const int whole = length >> p.lb;
     if (s.chunk < p.chunks) {
@@ -285,43 +322,59 @@ __global__ void __launch_bounds__(kThreads) fork_last_kernel(PagesArgs p) {
   }
 }
 
-// Grow, first step: the free pages, and what each row asks for (-1: its table is
-// too narrow).
+// Grow, first step: the free pages, what each row asks for (-1: its table is too
+// narrow), and what a group of rows does.
 __global__ void __launch_bounds__(kThreads) grow_ask_kernel(PagesArgs p) {
   __shared__ int box[kThreads / 64];
+  __shared__ int64_t wide[1][kThreads / 64];
   if (blockIdx.x < p.chunks) {
     free_bits(p, blockIdx.x, box);
     return;
   }
-  const int64_t row = (blockIdx.x - p.chunks) * kThreads + threadIdx.x;
-  if (row >= p.rows) return;
-  const int64_t more = p.in[row] < 0 ? 0 : p.in[row], length = length_of(p, static_cast<int>(row));
-  const int64_t want = (length + more + (1 << p.lb) - 1) >> p.lb;
-  p.asks[row] = want > p.cols ? -1 : static_cast<int>(want) - pages_of(p, length);
+  const int64_t group = blockIdx.x - p.chunks;
+  constexpr int kMine = kGroup / kThreads;
+  int given[kMine], lengths[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int row = static_cast<int>(min(group * kGroup + i * kThreads + threadIdx.x, static_cast<int64_t>(p.rows - 1)));
+    given[i] = p.in[row];
+    lengths[i] = length_of(p, row);
+  }
+  int64_t all[1] = {0};
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int64_t row = group * kGroup + i * kThreads + threadIdx.x;
+    const int64_t more = given[i] < 0 ? 0 : given[i], want = (lengths[i] + more + (1 << p.lb) - 1) >> p.lb;
+    const int asks = want > p.cols ? -1 : static_cast<int>(want) - pages_of(p, lengths[i]);
+    if (row < p.rows) {
+      p.asks[row] = asks;
+      all[0] += max(0, asks);
+    }
+  }
+  block_sums(all, wide);
+  if (threadIdx.x == 0) p.sums[group] = all[0];
 }
 
 // Grow, second step: one workgroup a row, whose wavefronts share the pages that it
 // asks for.
 __global__ void __launch_bounds__(kThreads) grow_kernel(PagesArgs p) {
-  __shared__ int box[3][kThreads / 64];
+  __shared__ int64_t box[2][kThreads / 64];
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int asks = p.asks[row], length = length_of(p, row), had = pages_of(p, length), given = p.in[row];
   int64_t rank = 0;
   bool fits = asks == 0;
   if (asks > 0) {
-    int64_t sum = 0;  // (a table's entries: rows * cols can pass 32 bits, pages cannot)
-    int free = 0;
-    for (int64_t i = tid; i < max(static_cast<int64_t>(row), p.chunks); i += kThreads) {
-      const int ask = p.asks[min(i, static_cast<int64_t>(row))], count = p.counts[min(i, p.chunks)];
-      if (i < row) sum += max(0, ask);
-      if (i < p.chunks) free += count;
+    int64_t all[2] = {0, 0};  // what the rows before it ask for (entries of a table can pass 32 bits), free pages
+    const int64_t group = row / kGroup, first = group * kGroup, within = row - first;
+    for (int64_t i = tid; i < max(max(group, within), p.chunks); i += kThreads) {
+      const int64_t sum = p.sums[min(i, group)];
+      const int ask = p.asks[first + min(i, within)], count = p.counts[min(i, p.chunks)];
+      all[0] += (i < group ? sum : 0) + (i < within ? max(0, ask) : 0);
+      all[1] += i < p.chunks ? count : 0;
     }
-    // saturated: what passes the number of pages fits nowhere
-    const int most = static_cast<int>(sum < p.pages ? sum : p.pages);
-    int all[3] = {most >> 8, most & 255, free};
     block_sums(all, box);
-    rank = static_cast<int64_t>(all[0]) * 256 + all[1];
-    fits = rank + asks <= all[2];
+    rank = all[0];
+    fits = rank + asks <= all[1];
   }
   __syncthreads();  // all have read the length
   if (tid == 0) {
@@ -707,6 +760,13 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(CopyArgs p) {
   }
 }
 
+// Up to so many rows a workgroup looks for a parent's first fork among the rows
+// before it; beyond, two launches more find those of all rows at once.  Measured (us
+// in a graph, four forks of each parent, 55 entries a row, the scan against the
+// launches): 4200 rows: 24.8, 20.0 where no parent goes on, 16.6, 19.5 where all do;
+// 8192: 48.5, 26.8 and 25.6, 25.6.  Below, the launches cost 4 us of 11 to 15.
+constexpr int kScan = 4096;
+
 bool block_ok(int32_t bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -738,13 +798,15 @@ uint64_t lay_out(const mi_pages_args* a, char* at, PagesArgs* p) {
   q.words = reinterpret_cast<uint64_t*>(take(chunks * kWords * 8));
   q.counts = reinterpret_cast<int32_t*>(take((chunks + 1) * 4));
   q.before = nullptr;
-  q.asks = q.source = q.length = q.rows_new = nullptr;
+  q.asks = q.first = q.source = q.length = q.rows_new = nullptr;
+  q.sums = nullptr;
   if (a->op == MI_PAGES_COMPACT) q.before = reinterpret_cast<int32_t*>(take(chunks * kWords * 4));
-  else q.asks = reinterpret_cast<int32_t*>(take(rows * 4));
+  else q.asks = reinterpret_cast<int32_t*>(take(rows * 4)), q.sums = reinterpret_cast<int64_t*>(take((rows + kGroup - 1) / kGroup * 8));
   if (a->op == MI_PAGES_FORK) {
     q.source = reinterpret_cast<int32_t*>(take(rows * 4));
     q.length = reinterpret_cast<int32_t*>(take(rows * 4));
     q.rows_new = reinterpret_cast<int32_t*>(take(rows * a->block_table_cols * 4));
+    if (a->rows > kScan) q.first = reinterpret_cast<int32_t*>(take(rows * 4));
   }
   return n;
 }
@@ -786,13 +848,18 @@ MI_PAGES_EXPORT int pages_update(const mi_pages_args* a, hipStream_t stream) {
   const dim3 b(kThreads);
   auto blocks = [](int64_t n) { return dim3(static_cast<unsigned>(n)); };
   if (a->op == MI_PAGES_FORK) {
-    if (p.chunks + p.rows > kMostBlocks) return MI_ATTN_EINVAL;
+    const int64_t groups = (static_cast<int64_t>(p.rows) - 1) / kGroup, wide = (static_cast<int64_t>(p.rows) + kThreads - 1) / kThreads;
+    if (p.chunks + p.rows + groups > kMostBlocks) return MI_ATTN_EINVAL;
+    if (p.first != nullptr) {
+      fork_clear_kernel<<<blocks(wide), b, 0, stream>>>(p);
+      fork_first_kernel<<<blocks(wide), b, 0, stream>>>(p);
+    }
     fork_rows_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
-    fork_write_kernel<<<blocks(p.chunks + p.rows), b, 0, stream>>>(p);
+    fork_write_kernel<<<blocks(p.chunks + p.rows + groups), b, 0, stream>>>(p);
     fork_last_kernel<<<blocks((static_cast<int64_t>(p.rows) + 3) / 4), b, 0, stream>>>(p);
   } else if (a->op == MI_PAGES_GROW) {
     if (p.rows > kMostBlocks) return MI_ATTN_EINVAL;
-    grow_ask_kernel<<<blocks(p.chunks + (static_cast<int64_t>(p.rows) + kThreads - 1) / kThreads), b, 0, stream>>>(p);
+    grow_ask_kernel<<<blocks(p.chunks + (static_cast<int64_t>(p.rows) + kGroup - 1) / kGroup), b, 0, stream>>>(p);
     grow_kernel<<<blocks(p.rows), b, 0, stream>>>(p);
   } else {
     const int64_t pairs = (p.pages / 2 + kThreads - 1) / kThreads;
