@@ -482,42 +482,7 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       }
     }
   };
-  // Calls found(key, i, r, x) for the infinities and NaN x in the lane's columns (those
-  // of acc[i][r]) among the values of the new tokens from .. to - 1: a wavefront looks
-  // at 8 KB at a time, and then at the columns of the rows that have any.
-  auto each_odd = [&](int from, int to, auto found) {
-    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kAt = 8;
-    const int at = static_cast<int>(__lane_id());
-    const char* base = p.x[1] + (rw.begin * p.x_t[1] + hk * p.x_h[1]) * 2;
-    auto row_at = [&](int key) { return base + key * (p.x_t[1] * 2); };
-    for (int k0 = from; k0 < to; k0 += kRows * kAt) {
-      u32x4 x[kAt];
-#pragma unroll
-      for (int j = 0; j < kAt; ++j)  // (rows behind the last one stand for it: found once more, with the same result)
-        x[j] = *reinterpret_cast<const u32x4*>(row_at(min(k0 + j * kRows + at / kLanes, to - 1)) + at % kLanes * 16);
-#pragma unroll
-      for (int j = 0; j < kAt; ++j) {
-        bool any = false;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) finite_only<T>(x[j][z], any);
-        for (uint64_t rows = __ballot(any); rows != 0;) {
-          const int row = (__ffsll(static_cast<unsigned long long>(rows)) - 1) / kLanes;
-          rows &= ~(((1ull << kLanes) - 1) << (row * kLanes));
-          const int key = min(k0 + j * kRows + row, to - 1);
-          const char* v = row_at(key) + (at >> 5) * 8;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(v + i * 64 + (r >> 2) * 16 + (r & 2) * 2);
-              const float a = T::lo(w), b = T::hi(w);
-              if (!(fabsf(a) < kInf)) found(key, i, r, a);
-              if (!(fabsf(b) < kInf)) found(key, i, r + 1, b);
-            }
-        }
-      }
-    }
-  };
+  bool odd = false;  // the wavefront has met an infinity or NaN that all its rows see
   if (n0 < e1) {
     // the first tile can hold hidden tokens; the last ones are not seen by the first rows
     int from = n0, to = e1;
@@ -526,27 +491,25 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       walk_part(from, from + 1);
       ++from;
     }
-    bool odd = false;
     if (from < to) {
       walk(from, to);
+      // What is NaN here comes from an infinity or NaN among the values, which the end
+      // adds, or from a score, and then the sum is NaN too: it starts anew, so that an
+      // infinity of a weight that is 0 in 16 bits is one.
       float finite[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) finite[r & 3] = fmaf(acc[i][r], 0.f, finite[r & 3]);
       odd = __any((finite[0] + finite[1]) + (finite[2] + finite[3]) != 0.f);
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][r] = acc[i][r] != acc[i][r] ? 0.f : acc[i][r];
+      }
     }
     if (to < e1) walk_part(to, e1);
-    // Infinities and NaN among the values go to the rows that see them whatever their
-    // weight, which the products would take to 16 bits, and 0 times infinity to NaN:
-    // where there are any, their columns start anew and then take them.
-    if (__builtin_expect(odd || sh.odd != 0, 0)) {
-#pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass)
-        each_odd(max(first_of(n0), rw.hidden), min(first_of(e1 - 1) + kTile, rw.r0 + rw.tokens), [&](int key, int i, int r, float x) {
-          if (sees && key <= mine) acc[i][r] = pass == 0 ? 0.f : acc[i][r] + x;
-        });
-    }
   }
 
   // The context, kSeg blocks' tiles at a time.
@@ -614,6 +577,40 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
       }
     }
     s0 = s1;
+  }
+  // Infinities and NaN among the new values, to the rows that see them, whatever their
+  // weight: a wavefront looks at 8 KB at a time, and key by key where it finds any.
+  if (odd || (n0 < e1 && sh.odd != 0)) {
+    constexpr int kLanes = D / 8, kRowsAt = 64 / kLanes, kAt = 8;
+    const int at = static_cast<int>(__lane_id()), to = min(first_of(e1 - 1) + kTile, rw.r0 + rw.tokens);
+    const char* base = p.x[1] + (rw.begin * p.x_t[1] + hk * p.x_h[1]) * 2;
+    auto row_at = [&](int key) { return base + key * (p.x_t[1] * 2); };
+#pragma unroll 1
+    for (int k0 = max(first_of(n0), rw.hidden); k0 < to; k0 += kRowsAt * kAt) {
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {  // (rows behind the last one stand for it)
+        const u32x4 x = *reinterpret_cast<const u32x4*>(row_at(min(k0 + j * kRowsAt + at / kLanes, to - 1)) + at % kLanes * 16);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) finite_only<T>(x[z], any);
+      }
+      if (!__any(any)) continue;
+#pragma unroll 1
+      for (int key = k0; key < min(k0 + kRowsAt * kAt, to); ++key) {
+        const char* v = row_at(key) + (at >> 5) * 8;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(v + i * 64 + (r >> 2) * 16 + (r & 2) * 2);
+            const float a = T::lo(w), b = T::hi(w);
+            if (sees && key <= mine) {
+              if (!(fabsf(a) < kInf)) acc[i][r] += a;
+              if (!(fabsf(b) < kInf)) acc[i][r + 1] += b;
+            }
+          }
+      }
+    }
   }
   sum = half_sum(sum);
   const float base = m - kLower;

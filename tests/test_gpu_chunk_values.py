@@ -125,3 +125,19 @@ def test_infinities_and_nan_in_long_prompts():
     x = build(6, [1500], [1500], 2, 1, 64, 64, torch.float16)
     x["v"][[0, 700, 1400], 0, [3, 60, 33]] = torch.tensor([math.inf, math.nan, -math.inf]).to(torch.float16)
     agree(x, 64, mt.chunk_attention(**put(x)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 64)])
+def test_infinities_beside_a_nan_of_the_cache(d, bs, dtype):
+    # the cache's NaN stays, also in a column whose new values hold an infinity of no weight
+    x = build(9, [400 + 300, 70], [300, 70], 2, 1, d, bs, dtype)
+    x["q"][:, :, 0], x["k"][:, :, 0] = 8.0, 0.0
+    x["k"][10, 0, 0] = -300 * math.sqrt(d) / 8
+    x["k_cache"][:, :, :, 0] = 0.0
+    x["v"][10, 0, 3:5] = math.inf
+    x["v_cache"][int(x["block_table"][0, 2]), 0, 5, 3] = math.nan
+    agree(x, bs, mt.chunk_attention(**put(x), max_length=1))
+    got = mt.chunk_attention(**put(x))[0]
+    agree(x, bs, (got, mt.chunk_attention(**put(x))[1]))
+    assert torch.isnan(got[:300, :, 3]).all() and (got[10:300, :, 4] == math.inf).all()
