@@ -52,7 +52,8 @@ extern "C" {
  *              where full codes pass fp16's range, it is 2^-37 of the largest
  *              product of a weight and its scale.
  *   max_length the caller's bound of the lengths: the work is split by it, longer
- *              sequences are computed right but slowly.
+ *              sequences are computed right but slowly, and so are few tokens of
+ *              sequences that are far shorter.
  *   workspace  chunk_attention_workspace() bytes, 16-byte aligned, need not be
  *              cleared; calls that overlap in time need one each.
  */

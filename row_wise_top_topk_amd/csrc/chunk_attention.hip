@@ -21,11 +21,12 @@
 // tokens, whose values have the scale 1 and may be as small (32000 keys of 2^-20
 // beside one of value 0, a scale of 2^-17: 0 instead of 0.03 of the values).
 //
-// Measured (bf16, 128 columns unless said): 2048 tokens behind 32000 keys, 64/8
-// heads: 1.93 ms, 1150 TFLOP/s, where a large library product reaches 1240; 8192
-// alone, 32/4 heads: 0.53 ms, 1040 (64 tiles a walk, of which each end costs one);
-// 96 behind 100003, 32/2 heads: 162 us and 12 to join 21 parts; 64 columns, 2048
-// behind 16000, 32/4 heads: 0.37 ms, 780; 33 behind 500, 8/2 heads: 14 us, the chain
+// Measured (bf16, 128 columns unless said; cards differ by 7 %): 2048 tokens behind
+// 32000 keys, 64/8 heads: 1.88 to 2.02 ms, 1100 to 1180 TFLOP/s, nine tenths of a
+// large library product on the same card; fp16 1.98; 8192 alone, 32/4 heads: 0.50 to
+// 0.54 ms, 1010 to 1090 (64 tiles a walk, of which each end costs one); 96 behind
+// 100003, 32/2 heads: 157 us and 12 to join 21 parts; 64 columns, 2048 behind 16000,
+// 32/4 heads: 0.32 to 0.37 ms, 770 to 890; 33 behind 500, 8/2 heads: 14 us, the chain
 // of nine tiles.  In the first the matrix unit is busy for 59 % of the cycles, the
 // vector unit (of 155 instructions a wavefront and tile 32 are exponentials) about as
 // long, LDS for 70 %: two wavefronts a SIMD cover each other's chains, and the card's
@@ -751,7 +752,10 @@ struct ChunkPlan {
 };
 
 // In how many parts, `most` at most, the walks of `items` workgroups over up to
-// `tiles` tiles are cut.  The 256 compute units take the workgroups in rounds (two
+// `tiles` tiles are cut.  `tiles` is that of the caller's bound, and a part has as many
+// whatever the sequence's own length: behind a bound far above it a walk lies in few
+// parts or one (96 tokens behind 8000, 32/8 heads: 39 us with its own length as bound,
+// 195 with 131072; 96 behind 100003, 32/2 heads: 161, and 1140 with 2^20).  The 256 compute units take the workgroups in rounds (two
 // small ones on a unit at once need as long as one after the other).  Where several
 // sequences share the call their lengths differ: half of the work is counted, half
 // a walk in which the card runs empty, and an eighth of the join's bytes, which

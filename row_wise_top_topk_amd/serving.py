@@ -8,7 +8,7 @@ device.  Outputs and scratch memory come from PyTorch's allocator, so a call
 can be captured into a graph, and two graphs share nothing.
 
     pages_grow(block_table, lengths, refs, new, 64)          # room for the new tokens
-    out, lse = chunk_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens=cu)
+    out, lse = chunk_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens=cu, max_length=longest)
     kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens=cu)
     ...
     rows = penalize_logits(logits, tokens, lengths, repetition=r, mask=grammar)
@@ -93,7 +93,9 @@ def chunk_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: 
     is read there only: the chunk may be appended before, after or never.  A
     prompt's first chunk has nothing in the cache.  ``max_length`` bounds the
     lengths where the caller knows them (default: what the table can hold, and
-    the chunk); it only decides how the work is split.
+    the chunk); it only decides how the work is split.  A few tokens behind a long
+    context need it: a bound far above the lengths, as that of a wide table, can
+    cost them several times the time.
 
     Pages and table columns that are not there give no keys.  Returns ``(out,
     lse)`` as ``kv8_attention`` does: ``[tokens, heads, dim]`` of q's type, and
