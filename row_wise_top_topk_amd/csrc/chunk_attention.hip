@@ -305,11 +305,10 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
   const bool valid = tl < rw.tokens;
   const int mine = rw.r0 + (valid ? tl : 0);  // the row's token among the chunk's
   const bool sees = valid && mine >= rw.hidden;
-  const int64_t tok = rw.begin + mine;
 
   u32x4 q[D / 16];
   {
-    const char* from = p.q + (tok * p.q_t + (valid ? head : hk * p.group) * p.q_h) * 2 + half * 16;
+    const char* from = p.q + ((rw.begin + mine) * p.q_t + (valid ? head : hk * p.group) * p.q_h) * 2 + half * 16;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) q[i] = valid ? *reinterpret_cast<const u32x4*>(from + i * 32) : u32x4{0, 0, 0, 0};
   }
@@ -580,44 +579,68 @@ __global__ void __launch_bounds__(NW * 64, 2) chunk_attention_kernel(ChunkArgs p
     s0 = s1;
   }
   // Infinities and NaN among the new values, to the rows that see them, whatever their
-  // weight: a wavefront looks at 8 KB at a time, and key by key where it finds any.
+  // weight.  A wavefront looks at 8 KB at a time; those that all rows see are added up
+  // as they lie there, 8 columns a lane, the others' rows are gone over key by key.
   if (odd || (n0 < e1 && sh.odd != 0)) {
     constexpr int kLanes = D / 8, kRowsAt = 64 / kLanes, kAt = 8;
-    const int at = static_cast<int>(__lane_id()), to = min(first_of(e1 - 1) + kTile, rw.r0 + rw.tokens);
+    const int at = static_cast<int>(__lane_id()), end = min(first_of(e1 - 1) + kTile, rw.r0 + rw.tokens);
+    int from = n0, to = e1;  // the tiles that all rows see
+    while (from < to && hides(to - 1)) --to;
+    if (from < to && hides(from)) ++from;
     const char* base = p.x[1] + (rw.begin * p.x_t[1] + hk * p.x_h[1]) * 2;
     auto row_at = [&](int key) { return base + key * (p.x_t[1] * 2); };
+    float added[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int k0 = max(first_of(n0), rw.hidden); k0 < to; k0 += kRowsAt * kAt) {
+    for (int k0 = first_of(n0); k0 < end; k0 += kRowsAt * kAt) {
+      const bool all = k0 >= first_of(from) && k0 < first_of(to);
       bool any = false;
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {  // (rows behind the last one stand for it)
-        const u32x4 x = *reinterpret_cast<const u32x4*>(row_at(min(k0 + j * kRowsAt + at / kLanes, to - 1)) + at % kLanes * 16);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(row_at(min(k0 + j * kRowsAt + at / kLanes, end - 1)) + at % kLanes * 16);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) finite_only<T>(x[z], any);
+        for (int z = 0; z < 4; ++z) {
+          finite_only<T>(x[z], any);
+          const float a = T::lo(x[z]), b = T::hi(x[z]);
+          added[2 * z] += all && !(fabsf(a) < kInf) ? a : 0.f;
+          added[2 * z + 1] += all && !(fabsf(b) < kInf) ? b : 0.f;
+        }
       }
-      if (!__any(any)) continue;
+      if (all || !__any(any)) continue;
 #pragma unroll 1
-      for (int key = k0; key < min(k0 + kRowsAt * kAt, to); ++key) {
+      for (int key = k0; key < min(k0 + kRowsAt * kAt, end); ++key) {
         const char* v = row_at(key) + (at >> 5) * 8;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(v + i * 64 + (r >> 2) * 16 + (r & 2) * 2);
-            const float a = T::lo(w), b = T::hi(w);
-            if (sees && key <= mine) {
-              if (!(fabsf(a) < kInf)) acc[i][r] += a;
-              if (!(fabsf(b) < kInf)) acc[i][r + 1] += b;
+          for (int r = 0; r < 16; r += 4) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(v + i * 64 + (r >> 2) * 16);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float a = z & 1 ? T::hi(w[z >> 1]) : T::lo(w[z >> 1]);
+              acc[i][r + z] += sees && key >= rw.hidden && key <= mine && !(fabsf(a) < kInf) ? a : 0.f;
             }
           }
       }
     }
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+#pragma unroll
+      for (int d = kLanes; d < 64; d <<= 1) added[z] += __shfl_xor(added[z], d);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float low = __shfl(added[r & 3], 4 * i + (r >> 2)), high = __shfl(added[4 + (r & 3)], 4 * i + (r >> 2));
+        acc[i][r] += sees ? (at < 32 ? low : high) : 0.f;
+      }
   }
   sum = half_sum(sum);
   const float base = m - kLower;
   if (!valid) return;
   if (p.splits == 1 || rw.tiles <= p.chunk) {  // the walk is in one part
-    store_chunk_row<T, D>(p, tok, head, half, acc, base, sum, sees);
+    int token = mine;
+    asm volatile("" : "+v"(token));  // (worked out again here: the walks need its registers)
+    store_chunk_row<T, D>(p, rw.begin + token, head, half, acc, base, sum, sees);
     return;
   }
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowsHere + row;

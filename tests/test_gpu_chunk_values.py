@@ -141,3 +141,22 @@ def test_infinities_beside_a_nan_of_the_cache(d, bs, dtype):
     got = mt.chunk_attention(**put(x))[0]
     agree(x, bs, (got, mt.chunk_attention(**put(x))[1]))
     assert torch.isnan(got[:300, :, 3]).all() and (got[10:300, :, 4] == math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,hk,d,bs", [(3, 1, 64, 32), (4, 2, 128, 64)])
+def test_many_infinities_and_nan(heads, hk, d, bs, dtype):
+    # in all kinds of tiles at once; a column that is NaN from the first token on, columns without any
+    x = build(13, [640 + 90, 130], [640, 130], heads, hk, d, bs, dtype, extra=3)
+    g = torch.Generator().manual_seed(2)
+    pick = torch.rand(x["v"].shape, generator=g) < 0.003
+    pick[..., d // 2:] = False
+    values = torch.tensor([math.inf, -math.inf, math.nan]).to(dtype)
+    x["v"][pick] = values[torch.randint(0, 3, (int(pick.sum()),), generator=g)]
+    x["v"][..., d - 3] = math.nan
+    x["v"][:, 0, d - 9] = math.inf
+    want = want_of(x, bs)
+    out, lse = (t.cpu().double() for t in mt.chunk_attention(**put(x), max_length=1))
+    assert (out[-3:] == 0).all() and torch.isneginf(lse[-3:]).all()
+    agree({n: t[:-3] if n in ("q", "k", "v") else t for n, t in x.items()}, bs, (out[:-3], lse[:-3]))
+    assert torch.equal(torch.isnan(out), torch.isnan(want[0]))
